@@ -23,6 +23,10 @@
  *       takes V in f16, so NoPE magnitudes must stay below 65536 (the append flags larger
  *       ones with NVFP4_MLA_DEV_FP8_RANGE and stores them anyway).
  *
+ *  (Attention over whole sequences through a page table, and operations on the pages, follow further
+ *  down: nvfp4_paged_mla_decode, nvfp4_mla_copy_pages, nvfp4_mla_fork_sequences,
+ *  nvfp4_mla_resize_sequences, nvfp4_mla_compact_pages. The pages have no counterpart to them.)
+ *
  *  2. nvfp4_sparse_mla_decode: DeepSeek-style sparse MLA decode over one shared latent KV
  *     head: for each query row (b, i) and head h, the keys are the records its top-k index
  *     list selects (FlashMLA PR 18, "Kernel:" paragraph: keys dequantized to bf16, QK^T over
@@ -82,11 +86,16 @@ typedef enum {
 
 /* Bits the kernels OR into *dev_status. */
 #define NVFP4_MLA_DEV_SLOT_OUT_OF_RANGE 0x1u  /* quantize_append: slot >= num_slots (skipped) */
-#define NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE 0x2u /* decode: index >= num_slots (masked)          */
+#define NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE 0x2u /* decode: index >= num_slots (masked); a page,
+                                                 sequence or length outside its table          */
 #define NVFP4_MLA_DEV_TIMEOUT 0x4u            /* decode: a pipeline wait gave up; out invalid */
 #define NVFP4_MLA_DEV_FP8_RANGE 0x8u          /* quantize_append, 656 B: a NoPE |x| >= 65536  */
 #define NVFP4_MLA_DEV_POSITION_OUT_OF_RANGE 0x10u /* norm_rope_quantize_append: position outside
                                                      [0, num_positions) (token skipped)         */
+#define NVFP4_MLA_DEV_PAGES_EXHAUSTED 0x20u   /* resize_sequences: too few free pages (no sequence
+                                                 grew; those that shrink did)                  */
+#define NVFP4_MLA_DEV_LENGTH_OUT_OF_RANGE 0x40u /* resize_sequences: a new length below 0 or beyond
+                                                   the page table (that sequence unchanged)    */
 
 /*
  * Quantize-and-append (write side).
@@ -242,6 +251,133 @@ NVFP4_MLA_API int nvfp4_sparse_mla_decode_no_alloc(const void* q, const uint8_t*
                                                    int32_t s_q, int32_t h_q, int32_t topk, float sm_scale,
                                                    const float* attn_sink, void* out, float* lse,
                                                    int32_t num_splits, uint32_t* dev_status, void* stream);
+
+/*
+ * ---- Sequences in pages -------------------------------------------------------------------------
+ *
+ * The calls below see the pool as num_pages pages of page_size records: page p is the slots
+ * [p page_size, (p + 1) page_size). page_size is a power of two, 1 to 4096. A batch of sequences is
+ *   page_table  int32 [batch, max_pages], rows table_stride elements apart (table_stride >=
+ *               max_pages): the pages of each sequence, in order. Entries behind a sequence's last
+ *               page are not read; the calls that change the table leave -1 there.
+ *   seq_lens    int32 [batch]: tokens of each sequence. Token t of sequence b lies in slot
+ *               page_table[b][t / page_size] * page_size + t % page_size, the slot that
+ *               nvfp4_mla_quantize_append writes its record to. Lengths are read as clamped to
+ *               [0, max_pages * page_size].
+ *   page_refs   int32 [num_pages], 16-byte aligned: how many table entries name each page. A page is
+ *               free exactly when its count is 0; there is no other free list. A pool starts with
+ *               all counts 0, all lengths 0 and all entries -1.
+ * All of it lives on the device and is read there: no call needs a length or a page on the host, so
+ * every call may be captured into a graph, and a replay follows the lengths of its time. The result of
+ * each call depends on its inputs alone. A table entry within a sequence's length that names no page
+ * of the pool sets NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE and is passed over (as a key: masked). batch *
+ * max_pages and max_pages * page_size must stay below 2^31.
+ */
+
+/*
+ * Scratch size of nvfp4_paged_mla_decode (host-only, no CUDA call; the same on every device): the
+ * parts of query rows whose keys were read by several CTAs. It depends on min(s_q * h_q, 64) only.
+ */
+NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s_q, int32_t h_q, size_t* bytes);
+
+/*
+ * Attention of the last s_q tokens of each sequence over all tokens of the sequence up to their own
+ * position, for decoding (s_q = 1), several tokens a step, and chunks of a prompt:
+ *   q            bf16 [batch, s_q, h_q, 576], contiguous, 16-byte aligned (512 NoPE dims, 64 RoPE).
+ *                Query i of sequence b has position seq_lens[b] - s_q + i; its record and those of
+ *                the tokens before it are in the cache already.
+ *   cache        uint8 [num_pages * page_size, record_bytes & 0xFFFF], 16-byte aligned.
+ *   record_bytes 352, 352 | NVFP4_MLA_SCALES_BLOCK_ORDER or 432 (656-byte fp8 records are not
+ *                supported by this call: NVFP4_MLA_ERR_UNSUPPORTED).
+ *   h_q          1 to 128.
+ *   sm_scale, attn_sink, out, lse: as in nvfp4_sparse_mla_decode, the sum running over the tokens
+ *                at positions 0 .. seq_lens[b] - s_q + i. A query with a negative position (a
+ *                sequence shorter than s_q, an empty one, padding of the batch) gets out = 0,
+ *                lse = -inf.
+ *   workspace    device scratch of at least ..._workspace_size bytes, 256-byte aligned; needs no
+ *                initialization. Calls that may overlap on the GPU need one each.
+ * Precision: as nvfp4_sparse_mla_decode on NVFP4 records (parts of a row are f16 normalized outputs,
+ * joined in fp32). A NaN in a query or in a record makes NaN the rows that see it, and only those.
+ */
+NVFP4_MLA_API int nvfp4_paged_mla_decode(const void* q, const uint8_t* cache, int64_t num_pages, int32_t page_size,
+                                         int32_t record_bytes, const int32_t* page_table, int64_t table_stride,
+                                         int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t s_q,
+                                         int32_t h_q, float sm_scale, const float* attn_sink, void* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * Scratch size of fork_sequences, resize_sequences and compact_pages (host-only): enough for each of
+ * them with these sizes. num_pairs: pairs of a fork (0 if none is made).
+ */
+NVFP4_MLA_API int nvfp4_mla_pages_workspace_size(int32_t batch, int32_t max_pages, int64_t num_pages,
+                                                 int32_t num_pairs, size_t* bytes);
+
+/*
+ * Copies page src[k] to page dst[k] (int32 [n], device) in every cache of a model.
+ *   caches       HOST array of num_caches (1..256) device pointers, one cache per layer, each
+ *                uint8 [num_pages * page_size, record_bytes & 0xFFFF], 16-byte aligned. Any record
+ *                width of this library.
+ * A pair with a negative page is skipped (padding); one with a page >= num_pages is skipped and sets
+ * NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE. All pairs are copied at once: targets should be distinct, and no
+ * page both source and target (else which bytes such a target holds afterwards is unspecified).
+ * Page counts are not touched. n == 0 is valid and launches nothing.
+ */
+NVFP4_MLA_API int nvfp4_mla_copy_pages(uint8_t* const* caches, int32_t num_caches, int64_t num_pages,
+                                       int32_t page_size, int32_t record_bytes, const int32_t* src,
+                                       const int32_t* dst, int32_t n, uint32_t* dev_status, void* stream);
+
+/*
+ * Forks sequences: for every pair k, sequence dst[k] (int32 [num_pairs], device) becomes a copy of
+ * sequence src[k]. Nothing is copied but the table row and the length: the pages are shared and
+ * counted, and a page is copied when one of its sequences grows into it (resize_sequences). The old
+ * pages of dst[k] are given back. All pairs read the state before the call, so a permutation of
+ * sequences (a beam-search step) is one call. Of several pairs with the same target the last one
+ * counts; a pair with a negative sequence is skipped, one with a sequence >= batch is skipped and
+ * sets NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE.
+ */
+NVFP4_MLA_API int nvfp4_mla_fork_sequences(int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                           int32_t* seq_lens, int32_t batch, int32_t* page_refs, int64_t num_pages,
+                                           int32_t page_size, const int32_t* src, const int32_t* dst,
+                                           int32_t num_pairs, void* workspace, size_t workspace_bytes,
+                                           uint32_t* dev_status, void* stream);
+
+/*
+ * Gives each sequence the length new_lens[b] (int32 [batch]).
+ *  - A shorter one gives back the pages behind its new end (0 frees the sequence): prompts that have
+ *    finished, drafted tokens that were rejected. These pages may be taken by the same call.
+ *  - A longer one takes the lowest free pages, sequence by sequence. If its last page is partly
+ *    filled and shared, it first takes a page of its own for it, into which the records it holds are
+ *    copied in every cache (`caches`, as in copy_pages; num_caches 0: no records are copied).
+ *  - slots (int64 [batch, max_new], 8-byte aligned; unused when max_new is 0) receives the slots of
+ *    the first max_new new tokens of each sequence, -1 behind its last one: the slot_mapping of the
+ *    append that writes them.
+ * If there are fewer free pages than the call needs, no sequence grows, all slots are -1 and
+ * NVFP4_MLA_DEV_PAGES_EXHAUSTED is set. A new length below 0 or above max_pages * page_size leaves
+ * its sequence unchanged and sets NVFP4_MLA_DEV_LENGTH_OUT_OF_RANGE.
+ */
+NVFP4_MLA_API int nvfp4_mla_resize_sequences(int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                             int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                                             int32_t* page_refs, int64_t num_pages, int32_t page_size,
+                                             uint8_t* const* caches, int32_t num_caches, int32_t record_bytes,
+                                             int64_t* slots, int32_t max_new, void* workspace,
+                                             size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * Compacts a pool: afterwards the n pages in use are pages 0 .. n - 1. The i-th used page at or
+ * behind page n moves, in every cache, into the i-th free page before it; other pages stay.
+ *   table_out, refs_out   the new table and counts; each may be the old one (in place) or a buffer
+ *                of its own: then the old table still names intact records until its pages are taken.
+ *                refs_out 16-byte aligned.
+ *   page_map     int32 [num_pages]: receives the new page of every old one, -1 for a free one.
+ *   live         int32 [1]: receives n.
+ */
+NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_caches, int32_t record_bytes,
+                                          const int32_t* page_table, int64_t table_stride, int32_t* table_out,
+                                          int64_t table_out_stride, int32_t max_pages, const int32_t* seq_lens,
+                                          int32_t batch, const int32_t* page_refs, int32_t* refs_out,
+                                          int64_t num_pages, int32_t page_size, int32_t* page_map, int32_t* live,
+                                          void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                          void* stream);
 
 /*
  * Self-test of the decode's wait bound (no counterpart on the pages). Every pipeline wait in

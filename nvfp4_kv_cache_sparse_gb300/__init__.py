@@ -34,6 +34,8 @@ DEV_INDEX_OUT_OF_RANGE = 0x2
 DEV_TIMEOUT = 0x4
 DEV_FP8_RANGE = 0x8
 DEV_POSITION_OUT_OF_RANGE = 0x10
+DEV_PAGES_EXHAUSTED = 0x20
+DEV_LENGTH_OUT_OF_RANGE = 0x40
 
 EXPORTED = (
     "nvfp4_mla_quantize_append",
@@ -45,6 +47,13 @@ EXPORTED = (
     "nvfp4_mla_status_string",
     "nvfp4_mla_version",
     "nvfp4_mla_selftest_wait_timeout",
+    "nvfp4_paged_mla_decode_workspace_size",
+    "nvfp4_paged_mla_decode",
+    "nvfp4_mla_pages_workspace_size",
+    "nvfp4_mla_copy_pages",
+    "nvfp4_mla_fork_sequences",
+    "nvfp4_mla_resize_sequences",
+    "nvfp4_mla_compact_pages",
 )
 
 _lib: Optional[ctypes.CDLL] = None
@@ -91,6 +100,15 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.nvfp4_mla_version.argtypes = []
     lib.nvfp4_mla_selftest_wait_timeout.restype = ctypes.c_int
     lib.nvfp4_mla_selftest_wait_timeout.argtypes = [P, P, P]
+    for name, types in (("nvfp4_paged_mla_decode_workspace_size", [i32, i32, i32, ctypes.POINTER(sz)]),
+                        ("nvfp4_paged_mla_decode", [P, P, i64, i32, i32, P, i64, i32, P, i32, i32, i32, f32, P, P, P, P, sz, P, P]),
+                        ("nvfp4_mla_pages_workspace_size", [i32, i32, i64, i32, ctypes.POINTER(sz)]),
+                        ("nvfp4_mla_copy_pages", [P, i32, i64, i32, i32, P, P, i32, P, P]),
+                        ("nvfp4_mla_fork_sequences", [P, i64, i32, P, i32, P, i64, i32, P, P, i32, P, sz, P, P]),
+                        ("nvfp4_mla_resize_sequences", [P, i64, i32, P, P, i32, P, i64, i32, P, i32, i32, P, i32, P, sz, P, P]),
+                        ("nvfp4_mla_compact_pages", [P, i32, i32, P, i64, P, i64, i32, P, i32, P, P, i64, i32, P, P, P, sz, P, P])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = types
     _lib = lib
     return lib
 
@@ -256,3 +274,7 @@ def selftest_wait_timeout(device=None, stream=None) -> Tuple[int, int]:
            load().nvfp4_mla_selftest_wait_timeout(_ptr(status), _ptr(elapsed), _stream(stream)))
     torch.cuda.synchronize(device)
     return int(status.item()), int(elapsed.item())
+
+
+from .paged import (compact_pages, copy_pages, fork_sequences, paged_mla_decode, paged_workspace_size,  # noqa: E402,F401
+                    pages_workspace_size, resize_sequences)

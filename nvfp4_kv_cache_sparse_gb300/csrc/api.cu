@@ -91,6 +91,47 @@ int check_decode_shape(int32_t batch, int32_t s_q, int32_t h_q, int32_t topk, in
     return NVFP4_MLA_OK;
 }
 
+// log2 of a page size, -1 for one that is not allowed
+int page_shift_of(int32_t page_size) {
+    if (page_size < 1 || page_size > 4096 || (page_size & (page_size - 1)) != 0) return -1;
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+// The sizes shared by the calls on sequences in pages.
+int check_pages(int32_t batch, int32_t max_pages, int64_t num_pages, int32_t page_size, int64_t table_stride) {
+    if (page_shift_of(page_size) < 0 || batch < 0 || max_pages < 0 || num_pages < 0 || num_pages > 0x7FFFFFFF) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(batch) * max_pages > 0x7FFFFFFF || static_cast<int64_t>(max_pages) * page_size > 0x7FFFFFFF)
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    return table_stride < max_pages ? NVFP4_MLA_ERR_INVALID_ARG : NVFP4_MLA_OK;
+}
+
+int check_caches(uint8_t* const* caches, int32_t num_caches, int32_t record_bytes) {
+    if (!record_ok(record_bytes)) return NVFP4_MLA_ERR_UNSUPPORTED;
+    if (num_caches < 0 || num_caches > nvfp4mla::kMaxCaches || (num_caches > 0 && !caches)) return NVFP4_MLA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_caches; ++i)
+        if (!caches[i] || !aligned(caches[i], 16)) return NVFP4_MLA_ERR_INVALID_ARG;
+    return NVFP4_MLA_OK;
+}
+
+// Workspaces of the page calls, in 32-bit words. Resize: the free pages it hands out, four words per
+// sequence. Fork: a staged row and a length per pair. Compact: movers, their counts and holes.
+size_t resize_words(int32_t batch, int64_t num_pages) { return static_cast<size_t>(num_pages) + 4 * static_cast<size_t>(batch); }
+size_t fork_words(int32_t max_pages, int32_t num_pairs) { return static_cast<size_t>(num_pairs) * (static_cast<size_t>(max_pages) + 1); }
+size_t compact_words(int64_t num_pages) { return 3 * static_cast<size_t>(num_pages / 2) + 1; }
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    return workspace && bytes >= need && aligned(workspace, 256) ? NVFP4_MLA_OK : NVFP4_MLA_ERR_WORKSPACE;
+}
+
+int check_paged_shape(int32_t batch, int32_t s_q, int32_t h_q) {
+    if (batch < 0 || s_q < 0) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (h_q < 1 || h_q > 128) return NVFP4_MLA_ERR_UNSUPPORTED;
+    // query rows are counted in 31 bits
+    return static_cast<int64_t>(batch) * s_q > 0x7FFFFFFF / 128 ? NVFP4_MLA_ERR_INVALID_ARG : NVFP4_MLA_OK;
+}
+
 }  // namespace
 
 namespace nvfp4mla {
@@ -253,6 +294,211 @@ NVFP4_MLA_API int nvfp4_sparse_mla_decode(const void* q, const uint8_t* cache, i
     d.part_lse = need ? reinterpret_cast<float*>(ws + n_part * 512 * sizeof(uint16_t)) : nullptr;
     d.dev_status = dev_status;
     const cudaError_t e = nvfp4mla::launch_sparse_decode(d, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s_q, int32_t h_q, size_t* bytes) {
+    if (!bytes) return NVFP4_MLA_ERR_INVALID_ARG;
+    const int st = check_paged_shape(batch, s_q, h_q);
+    if (st != NVFP4_MLA_OK) return st;
+    *bytes = batch == 0 || s_q == 0 ? 0 : nvfp4mla::paged_workspace_bytes(nvfp4mla::paged_row_tile(static_cast<int64_t>(s_q) * h_q));
+    return NVFP4_MLA_OK;
+}
+
+NVFP4_MLA_API int nvfp4_paged_mla_decode(const void* q, const uint8_t* cache, int64_t num_pages, int32_t page_size,
+                                         int32_t record_bytes, const int32_t* page_table, int64_t table_stride,
+                                         int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t s_q,
+                                         int32_t h_q, float sm_scale, const float* attn_sink, void* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+    int st = check_paged_shape(batch, s_q, h_q);
+    if (st != NVFP4_MLA_OK) return st;
+    if (!record_ok(record_bytes) || record_width(record_bytes) == 656) return NVFP4_MLA_ERR_UNSUPPORTED;
+    st = check_pages(batch, max_pages, num_pages, page_size, table_stride);
+    if (st != NVFP4_MLA_OK) return st;
+    if (batch == 0 || s_q == 0) return NVFP4_MLA_OK;
+    // a table without columns (or a pool without pages) has nothing to read: its pointer may be null
+    if (!q || !seq_lens || !out || !lse || (max_pages > 0 && !page_table) || (num_pages > 0 && !cache)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(lse, 4) || !aligned(attn_sink, 4))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    const int64_t rows_per_seq = static_cast<int64_t>(s_q) * h_q;
+    st = check_workspace(workspace, workspace_bytes, nvfp4mla::paged_workspace_bytes(nvfp4mla::paged_row_tile(rows_per_seq)));
+    if (st != NVFP4_MLA_OK) return st;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::PagedDecodeArgs d;
+    d.q = q;
+    d.cache = cache;
+    d.num_pages = static_cast<int>(num_pages);
+    d.page_shift = page_shift_of(page_size);
+    d.record_bytes = record_width(record_bytes);
+    d.block_scales = block_scales(record_bytes);
+    d.page_table = page_table;
+    d.table_stride = table_stride;
+    d.capacity = max_pages << d.page_shift;
+    d.seq_lens = seq_lens;
+    d.batch = batch;
+    d.s_q = s_q;
+    d.h_q = h_q;
+    d.sm_scale = sm_scale;
+    d.attn_sink = attn_sink;
+    d.out = out;
+    d.lse = lse;
+    d.ctas = sms;
+    d.dev_status = dev_status;
+    const cudaError_t e = nvfp4mla::launch_paged_decode(d, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_mla_pages_workspace_size(int32_t batch, int32_t max_pages, int64_t num_pages,
+                                                 int32_t num_pairs, size_t* bytes) {
+    if (!bytes || num_pairs < 0) return NVFP4_MLA_ERR_INVALID_ARG;
+    const int st = check_pages(batch, max_pages, num_pages, 1, max_pages);
+    if (st != NVFP4_MLA_OK) return st;
+    size_t words = resize_words(batch, num_pages);
+    if (fork_words(max_pages, num_pairs) > words) words = fork_words(max_pages, num_pairs);
+    if (compact_words(num_pages) > words) words = compact_words(num_pages);
+    *bytes = round256(4 * words);
+    return NVFP4_MLA_OK;
+}
+
+NVFP4_MLA_API int nvfp4_mla_copy_pages(uint8_t* const* caches, int32_t num_caches, int64_t num_pages,
+                                       int32_t page_size, int32_t record_bytes, const int32_t* src,
+                                       const int32_t* dst, int32_t n, uint32_t* dev_status, void* stream) {
+    int st = check_pages(0, 0, num_pages, page_size, 0);
+    if (st == NVFP4_MLA_OK) st = check_caches(caches, num_caches, record_bytes);
+    if (st != NVFP4_MLA_OK) return st;
+    if (n < 0 || num_caches < 1) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (n == 0) return NVFP4_MLA_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return NVFP4_MLA_ERR_INVALID_ARG;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    const nvfp4mla::PoolArgs pool = {caches, num_caches, static_cast<int>(num_pages), page_shift_of(page_size), record_width(record_bytes)};
+    const cudaError_t e = nvfp4mla::launch_copy_pages(pool, src, dst, n, dev_status, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_mla_fork_sequences(int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                           int32_t* seq_lens, int32_t batch, int32_t* page_refs, int64_t num_pages,
+                                           int32_t page_size, const int32_t* src, const int32_t* dst,
+                                           int32_t num_pairs, void* workspace, size_t workspace_bytes,
+                                           uint32_t* dev_status, void* stream) {
+    int st = check_pages(batch, max_pages, num_pages, page_size, table_stride);
+    if (st != NVFP4_MLA_OK) return st;
+    if (num_pairs < 0) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (num_pairs == 0) return NVFP4_MLA_OK;
+    if (!seq_lens || !src || !dst || (max_pages > 0 && !page_table) || (num_pages > 0 && !page_refs)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(page_refs, 16))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, round256(4 * fork_words(max_pages, num_pairs)));
+    if (st != NVFP4_MLA_OK) return st;
+    if (device_sm_count(&st) <= 0) return st;
+    nvfp4mla::ForkArgs a;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.width = max_pages;
+    a.shift = page_shift_of(page_size);
+    a.seq_lens = seq_lens;
+    a.batch = batch;
+    a.page_refs = page_refs;
+    a.num_pages = static_cast<int>(num_pages);
+    a.src = src;
+    a.dst = dst;
+    a.pairs = num_pairs;
+    a.stage = static_cast<int32_t*>(workspace);
+    a.status = dev_status;
+    const cudaError_t e = nvfp4mla::launch_fork(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_mla_resize_sequences(int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                             int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                                             int32_t* page_refs, int64_t num_pages, int32_t page_size,
+                                             uint8_t* const* caches, int32_t num_caches, int32_t record_bytes,
+                                             int64_t* slots, int32_t max_new, void* workspace,
+                                             size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+    int st = check_pages(batch, max_pages, num_pages, page_size, table_stride);
+    if (st == NVFP4_MLA_OK) st = check_caches(caches, num_caches, record_bytes);
+    if (st != NVFP4_MLA_OK) return st;
+    if (max_new < 0) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (batch == 0) return NVFP4_MLA_OK;
+    if (!seq_lens || !new_lens || (max_pages > 0 && !page_table) || (num_pages > 0 && !page_refs) || (max_new > 0 && !slots))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(page_refs, 16) || !aligned(slots, 8))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, round256(4 * resize_words(batch, num_pages)));
+    if (st != NVFP4_MLA_OK) return st;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::ResizeArgs a;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.width = max_pages;
+    a.shift = page_shift_of(page_size);
+    a.seq_lens = seq_lens;
+    a.new_lens = new_lens;
+    a.batch = batch;
+    a.page_refs = page_refs;
+    a.num_pages = static_cast<int>(num_pages);
+    a.slots = slots;
+    a.max_new = max_new;
+    int32_t* w = static_cast<int32_t*>(workspace);
+    a.offset = w;
+    a.cow_src = w + batch;
+    a.cow_dst = w + 2 * static_cast<int64_t>(batch);
+    a.cow_records = w + 3 * static_cast<int64_t>(batch);
+    a.free_list = w + 4 * static_cast<int64_t>(batch);
+    a.status = dev_status;
+    const nvfp4mla::PoolArgs pool = {caches, num_caches, a.num_pages, a.shift, record_width(record_bytes)};
+    const cudaError_t e = nvfp4mla::launch_resize(a, pool, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_caches, int32_t record_bytes,
+                                          const int32_t* page_table, int64_t table_stride, int32_t* table_out,
+                                          int64_t table_out_stride, int32_t max_pages, const int32_t* seq_lens,
+                                          int32_t batch, const int32_t* page_refs, int32_t* refs_out,
+                                          int64_t num_pages, int32_t page_size, int32_t* page_map, int32_t* live,
+                                          void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                          void* stream) {
+    int st = check_pages(batch, max_pages, num_pages, page_size, table_stride);
+    if (st == NVFP4_MLA_OK) st = check_caches(caches, num_caches, record_bytes);
+    if (st != NVFP4_MLA_OK) return st;
+    if (table_out_stride < max_pages || !live || !aligned(live, 4)) return NVFP4_MLA_ERR_INVALID_ARG;
+    // in place, the old and the new table are the same rows
+    if (page_table == table_out && table_stride != table_out_stride) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (num_pages > 0 && (!page_refs || !refs_out || !page_map)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(batch) * max_pages > 0 && (!page_table || !table_out || !seq_lens)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || !aligned(table_out, 4) || !aligned(seq_lens, 4) || !aligned(page_map, 4) ||
+        !aligned(page_refs, 16) || !aligned(refs_out, 16))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, round256(4 * compact_words(num_pages)));
+    if (st != NVFP4_MLA_OK) return st;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::CompactArgs a;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.table_out = table_out;
+    a.table_out_stride = table_out_stride;
+    a.width = max_pages;
+    a.shift = page_shift_of(page_size);
+    a.seq_lens = seq_lens;
+    a.batch = batch;
+    a.page_refs = page_refs;
+    a.refs_out = refs_out;
+    a.num_pages = static_cast<int>(num_pages);
+    a.page_map = page_map;
+    a.live = live;
+    int32_t* w = static_cast<int32_t*>(workspace);
+    const int64_t half = num_pages / 2;
+    a.moves = w;
+    a.mover = w + 1;
+    a.mover_refs = a.mover + half;
+    a.hole = a.mover_refs + half;
+    a.status = dev_status;
+    const nvfp4mla::PoolArgs pool = {caches, num_caches, a.num_pages, a.shift, record_width(record_bytes)};
+    const cudaError_t e = nvfp4mla::launch_compact(a, pool, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
 }
 

@@ -75,4 +75,90 @@ cudaError_t launch_split_merge(const DecodeArgs& a, cudaStream_t stream);
 // One time-bounded mbarrier wait that runs out (see nvfp4_mla_selftest_wait_timeout).
 cudaError_t launch_wait_timeout_probe(uint32_t* status, uint64_t* elapsed_ns, cudaStream_t stream);
 
+// ---- attention over whole sequences through a page table (paged_decode.cu)
+struct PagedDecodeArgs {
+    const void* q;               // bf16 [batch, s_q, h_q, 576]
+    const uint8_t* cache;        // [num_pages << page_shift, record_bytes]
+    int num_pages;
+    int page_shift;
+    int record_bytes;            // 352 or 432
+    bool block_scales;
+    const int32_t* page_table;   // [batch, max_pages], rows table_stride apart
+    int64_t table_stride;
+    int capacity;                // max_pages << page_shift
+    const int32_t* seq_lens;
+    int batch, s_q, h_q;
+    float sm_scale;
+    const float* attn_sink;      // nullable [h_q]
+    void* out;                   // bf16 [batch, s_q, h_q, 512]
+    float* lse;
+    int ctas;                    // CTAs of the attention grid
+    uint16_t* part_out;          // workspace, see paged_workspace_bytes
+    float* part_lse;
+    int32_t* hdr;
+    uint32_t* dev_status;
+};
+constexpr int kPagedMaxCtas = 160;               // no sm_103 device has more SMs
+int paged_row_tile(int64_t rows_per_seq);        // query rows that share a CTA's keys: 16, 32 or 64
+size_t paged_workspace_bytes(int row_tile);
+cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t stream);
+cudaError_t launch_paged_decode_n16(const PagedDecodeArgs& d, cudaStream_t stream);
+cudaError_t launch_paged_decode_n32(const PagedDecodeArgs& d, cudaStream_t stream);
+cudaError_t launch_paged_decode_n64(const PagedDecodeArgs& d, cudaStream_t stream);
+
+// ---- operations on pages (page_ops.cu)
+constexpr int kMaxCaches = 256;
+struct PoolArgs {
+    uint8_t* const* caches;      // host array of num_caches device pointers
+    int num_caches, num_pages, shift;
+    int record_bytes;
+};
+struct ResizeArgs {
+    int32_t* page_table;
+    int64_t table_stride;
+    int width, shift;
+    int32_t* seq_lens;
+    const int32_t* new_lens;
+    int batch;
+    int32_t* page_refs;
+    int num_pages;
+    int64_t* slots;              // [batch, max_new]
+    int max_new;
+    int32_t *free_list, *offset, *cow_src, *cow_dst, *cow_records;   // workspace
+    uint32_t* status;
+};
+struct ForkArgs {
+    int32_t* page_table;
+    int64_t table_stride;
+    int width, shift;
+    int32_t* seq_lens;
+    int batch;
+    int32_t* page_refs;
+    int num_pages;
+    const int32_t *src, *dst;
+    int pairs;
+    int32_t* stage;              // workspace [pairs, width + 1]
+    uint32_t* status;
+};
+struct CompactArgs {
+    const int32_t* page_table;
+    int64_t table_stride;
+    int32_t* table_out;
+    int64_t table_out_stride;
+    int width, shift;
+    const int32_t* seq_lens;
+    int batch;
+    const int32_t* page_refs;
+    int32_t* refs_out;
+    int num_pages;
+    int32_t *page_map, *live;
+    int32_t *mover, *mover_refs, *hole, *moves;   // workspace
+    uint32_t* status;
+};
+cudaError_t launch_copy_pages(const PoolArgs& pool, const int32_t* src, const int32_t* dst, int n, uint32_t* status, int sms,
+                              cudaStream_t stream);
+cudaError_t launch_resize(const ResizeArgs& a, const PoolArgs& pool, int sms, cudaStream_t stream);
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream);
+cudaError_t launch_compact(const CompactArgs& a, const PoolArgs& pool, int sms, cudaStream_t stream);
+
 }  // namespace nvfp4mla
