@@ -271,7 +271,7 @@ NVFP4_MLA_API int nvfp4_sparse_mla_decode_no_alloc(const void* q, const uint8_t*
  * every call may be captured into a graph, and a replay follows the lengths of its time. The result of
  * each call depends on its inputs alone. A table entry within a sequence's length that names no page
  * of the pool sets NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE and is passed over (as a key: masked). batch *
- * max_pages and max_pages * page_size must stay below 2^31.
+ * max_pages, max_pages * page_size and num_pages * page_size must stay below 2^31.
  */
 
 /*

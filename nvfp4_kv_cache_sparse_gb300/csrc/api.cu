@@ -102,7 +102,8 @@ int page_shift_of(int32_t page_size) {
 // The sizes shared by the calls on sequences in pages.
 int check_pages(int32_t batch, int32_t max_pages, int64_t num_pages, int32_t page_size, int64_t table_stride) {
     if (page_shift_of(page_size) < 0 || batch < 0 || max_pages < 0 || num_pages < 0 || num_pages > 0x7FFFFFFF) return NVFP4_MLA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(batch) * max_pages > 0x7FFFFFFF || static_cast<int64_t>(max_pages) * page_size > 0x7FFFFFFF)
+    if (static_cast<int64_t>(batch) * max_pages > 0x7FFFFFFF || static_cast<int64_t>(max_pages) * page_size > 0x7FFFFFFF ||
+        num_pages * page_size > 0x7FFFFFFF)
         return NVFP4_MLA_ERR_INVALID_ARG;
     return table_stride < max_pages ? NVFP4_MLA_ERR_INVALID_ARG : NVFP4_MLA_OK;
 }

@@ -75,60 +75,4 @@ __device__ __forceinline__ uint32_t gather_byte4(const uint4& w, int q) {
     return __byte_perm(__byte_perm(w.x, w.y, sel), __byte_perm(w.z, w.w, sel), 0x5410);
 }
 
-// Read-only global loads that do not allocate in L1 (every record byte is used once per CTA).
-__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
-}
-
-// One key's share of a converter thread q (0..3): record bytes 64c + 16q .. + 15 (c = 0..3), the codes
-// of 16-dim blocks 8c + 2q and 8c + 2q + 1, and the scale bytes of those blocks.
-template <int R, bool kBlkOrder>
-struct KeyRaw {
-    // 352-byte records with the permuted placement (block s at 320 + 8 (s & 3) + (s >> 2)): the eight
-    // scale bytes of the thread's blocks lie in one 16-byte half of the field; otherwise all 32 bytes
-    static constexpr bool kPermuted = R == 352 && !kBlkOrder;
-    uint4 codes[4];
-    uint4 sc[kPermuted ? 1 : 2];
-
-    __device__ __forceinline__ void load_codes(const uint8_t* rec, int q, int c) { codes[c] = ldg_stream16(rec + 64 * c + 16 * q); }
-    __device__ __forceinline__ void load_scales(const uint8_t* rec, int q) {
-        if constexpr (kPermuted) {
-            sc[0] = ldg_stream16(rec + 320 + 16 * (q & 1));
-        } else {
-            constexpr int sb = R == 352 ? 320 : 256;
-            sc[0] = ldg_stream16(rec + sb);
-            sc[1] = ldg_stream16(rec + sb + 16);
-        }
-    }
-    __device__ __forceinline__ void load(const uint8_t* rec, int q) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) load_codes(rec, q, c);
-        load_scales(rec, q);
-    }
-    // the scale pairs of blocks c = 0..3, two per word (c even: low half)
-    __device__ __forceinline__ void scale_pairs(int q, uint32_t (&sp)[2]) const {
-        sp[0] = (scale_pair(0, q) & 0xFFFFu) | (scale_pair(1, q) << 16);
-        sp[1] = (scale_pair(2, q) & 0xFFFFu) | (scale_pair(3, q) << 16);
-    }
-    // byte 0: the scale of block 8c + 2q, byte 1: of block 8c + 2q + 1
-    __device__ __forceinline__ uint32_t scale_pair(int c, int q) const {
-        if constexpr (kPermuted) {
-            // block 8c + 2q at byte 16 (q & 1) + 2c + (q >> 1), the next block eight bytes further
-            const uint32_t wa = c < 2 ? sc[0].x : sc[0].y, wb = c < 2 ? sc[0].z : sc[0].w;
-            const uint32_t bi = static_cast<uint32_t>(2 * c + (q >> 1)) & 3u;
-            return __byte_perm(wa, wb, bi | ((bi + 4u) << 4));
-        } else {
-            // block s at byte s: bytes 2q, 2q + 1 of word 2c + (q >> 1)
-            const uint32_t w[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
-            const uint32_t wv = (q >> 1) != 0 ? w[2 * c + 1] : w[2 * c];
-            const uint32_t lo = 2u * static_cast<uint32_t>(q & 1);
-            return __byte_perm(wv, 0u, lo | ((lo + 1u) << 4));
-        }
-    }
-};
-
 }  // namespace nvfp4mla

@@ -9,32 +9,36 @@
 //
 // Work split. The s_q * h_q query rows of a sequence lie one behind the other in q; N of them (16, 32
 // or 64: the kernel's row tile) share every key that is dequantized, so a job is (sequence, row tile)
-// and costs ceil(keys / 128) tiles of 128 keys. The tiles of all jobs, one job behind the other, are
+// and costs ceil(keys / 64) tiles of 64 keys. The tiles of all jobs, one job behind the other, are
 // cut into as many equal runs as there are CTAs (one per SM), whatever the lengths are: the lengths
 // are read on the device, so a captured call follows them. A job that lies in one run is finished by
 // its CTA; the parts of a job that was cut go to the workspace (at most two per CTA, f16 outputs
 // divided by their own sums, fp32 log-sum-exps) and a second kernel joins them.
 //
 // Contractions. As keys outnumber rows, both products have the keys or the value dims on the MMA's M
-// side: S^T [128 keys x N] = K Q^T and O^T [512 dims x N] += V^T P^T (four M = 128 MMAs per 16
+// side: S^T [64 keys x N] = K Q^T and O^T [512 dims x N] += V^T P^T (four M = 128 MMAs per 16
 // keys). A record is dequantized once, into f16 (exact: an e2m1 x e4m3 product has few bits), and
-// read twice: K-major as K, MN-major as V^T. The 64 RoPE dims of K come from tensor memory. Queries
-// are f16 times a power of two per row (exact within 2^28 of the row's largest), scores fp32, P f16.
+// read twice: K-major as K, MN-major as V^T. Queries are f16 times a power of two per row (exact
+// within 2^28 of the row's largest), scores fp32, P f16.
 //
-// Pipeline. Shared memory holds a ring of kRing blocks (128 keys x 128 dims, 32 KB); a block is
-// filled by the converters, read by the QK MMAs, and freed by the PV MMAs of its tile. With a ring
-// of more than four blocks the first blocks of tile i + 1 are converted and multiplied (into the
-// other of two score buffers) while tile i is in its softmax.
+// Pipeline. Shared memory holds a ring of kRing blocks (64 keys x 128 dims, 16 KB), two tiles and more:
+// a block is filled by the converters, read by the QK MMAs, and freed by the PV MMAs of its tile.
+// The conversion of one tile, the softmax of another and the MMAs of both run side by side (two
+// score buffers, two P buffers); the MMA issuer takes whichever of the next PV and the next QK block
+// is ready, PV first, as it frees the ring. Tiles of 64 keys, not 128: what a CTA can have in flight is
+// bounded by shared memory, and a tile of 128 keys (128 KB) left the ring half empty while its
+// softmax ran (16 rows, 352-byte records: 3.5 us per 128 keys with a ring of 1.5 such tiles).
 //
 // Softmax. A lazy reference maximum per row (log2 domain): P = 2^(z - m); a tile moves m only where
-// some score exceeds m + 8. A softmax thread holds one key's scores of 16 or 32 rows; it writes P
-// against the current references at once, the warps vote, and only where a reference has to move is
-// O^T rescaled and the pass redone. Row sums stay in fp32 registers (a key lane's share each) and
-// are added up across lanes at the end of a job.
+// some score exceeds m + 8: the warps vote once per tile, and only then is O^T rescaled. The scores of
+// an M = 64 MMA lie in 16 lanes of each lane quadrant; 16x256b loads spread them over the warp, two
+// keys and a quarter of the columns a thread. Row sums stay in fp32 registers (a thread's share of its
+// columns) and are added up at the end of a job.
 //
-// Masks. A key behind the sequence's end, in a page outside the pool, or with a NaN scale gets a zero
-// row in shared memory (V and K share it, and 0 x NaN in PV would reach rows that do not see the
-// key); P is 0 for a key that a row does not see and NaN for a NaN key that it sees.
+// Masks. A key behind the sequence's end or in a page outside the pool gets a zero row in shared memory
+// (V and K share it, and 0 x NaN in PV would reach rows that do not see the key), a block of dims
+// with a NaN scale likewise; P is 0 for a key that a row does not see and NaN for a NaN key that it
+// sees.
 //
 // Every wait is bounded by time; on timeout the CTA sets NVFP4_MLA_DEV_TIMEOUT, stops issuing work,
 // drains what it issued and returns.
@@ -55,52 +59,59 @@
 namespace nvfp4mla {
 namespace paged {
 
-constexpr int kTile = 128;                 // keys per tile (M of the QK MMAs)
+constexpr int kTile = 64;                  // keys per tile (M of the QK MMAs)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
+constexpr int kSubBlk = 8192;              // 64 keys x 64 dims
+constexpr int kBlk = 16384;                // 64 keys x 128 dims
+constexpr int kAhead = 8;                  // tiles whose keys' slots are looked up ahead
+// Shared memory (offsets from a 1024-byte aligned base)
+constexpr int kOffCM = 512;                // float [N/2][4]: per row pair {ch_a, ch_b, -m_a, -m_b}: the score scale
+                                           // sm_scale log2(e) 2^-pre and the negated reference maximum
+constexpr int kOffAlpha = 1024;            // float [N]: rescale factors, then 1 / l
+constexpr int kOffXmax = 1280;             // float [N][4]: per-row values of the four key quadrants
+constexpr int kOffPos = 2304;              // int [N]: each row's position (its last visible key)
+constexpr int kOffNan = 2560;              // uint8 [4][2][64]: keys with a NaN scale, by tile and converter group
+constexpr int kOffScan = 3072;             // int64 [32]
+constexpr int kOffTile = 3328;             // int4 [kAhead]: first key position, row 0's position, flags, job
+constexpr int kOffSlot = 3456;             // int [kAhead][64]: the keys' slots; -1: no key, -2: its page is outside the pool
+constexpr int kOffQ = 6144;
+static_assert(kOffSlot + kAhead * kTile * 4 <= kOffQ, "control area");
+
 template <int N>
 struct Shape {
     static constexpr int kSoft = N == 16 ? 4 : 8;        // softmax warps
-    static constexpr int kConv = N == 64 ? 8 : 16;       // converter warps
-    static constexpr int kKeys = 16 / kConv;             // keys of a converter thread
-    static constexpr int kThreads = 32 * (kSoft + kConv + 1);
-    static constexpr int kRpt = 4 * N / kSoft;           // rows of a softmax thread (it has one key)
-    static constexpr int kRopeDims = 256 / kSoft;        // RoPE dims a softmax thread converts
-    static constexpr int kRing = N == 16 ? 6 : N == 32 ? 5 : 4;
-    static constexpr int kEarly = kRing - 4;             // blocks of the next tile that fit beside a whole tile
-    // tensor memory columns: O^T four blocks, two score buffers, the RoPE rows of K
-    static constexpr uint32_t kColO = 0, kColS = 4 * N, kColR = 6 * N;
+    static constexpr int kConv = 16;                     // converter warps: two groups, even and odd blocks
+    static constexpr int kThreads = 32 * (kSoft + kConv + 2);
+    static constexpr int kCols = 4 * N / kSoft;          // rows (score columns) of a softmax warp
+    static constexpr int kRing = N == 16 ? 10 : N == 32 ? 9 : 7;
+    static constexpr int kRopeRing = N == 64 ? 2 : 3;    // tiles whose RoPE dims are held (see the converters)
+    // tensor memory columns: O^T four blocks, two score buffers
+    static constexpr uint32_t kColO = 0, kColS = 4 * N;
     static constexpr int kTmemCols = N == 16 ? 128 : N == 32 ? 256 : 512;
-    static_assert(6 * N + 32 <= kTmemCols, "tensor memory");
-    // shared memory (offsets from a 1024-byte aligned base)
+    static_assert(6 * N <= kTmemCols, "tensor memory");
     static constexpr int kQBlk = N * 128;                // N rows x 64 dims
-    static constexpr int kOffQ = 4096;
     static constexpr int kOffK = kOffQ + 9 * kQBlk;
-    static constexpr int kOffP = kOffK + kRing * 32768;
-    static constexpr int kSmemBytes = kOffP + N * 256;
+    static constexpr int kOffRope = kOffK + kRing * kBlk;
+    static constexpr int kOffP = kOffRope + kRopeRing * kSubBlk;
+    static constexpr int kPBytes = N * 128;              // P of a tile: 64 keys x N rows
+    static constexpr int kSmemBytes = kOffP + 2 * kPBytes;
     static constexpr int kSmemAlloc = kSmemBytes + 1024;
     static_assert(kSmemAlloc <= 232448, "shared memory");
-    static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
+    static_assert(kOffQ % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
 };
-constexpr int kSubBlk = 16384;             // 128 keys x 64 dims
-constexpr int kBlk = 32768;
-constexpr int kOffCM = 256;                // float [N/2][4]: per row pair {ch_a, ch_b, -m_a, -m_b}
-constexpr int kOffAlpha = 768;             // float [N]: rescale factors, then 1 / l
-constexpr int kOffXmax = 1024;             // float [N][4]: per-row values of the four key quadrants
-constexpr int kOffPos = 2048;              // int [N]: each row's position (its last visible key)
-constexpr int kOffNan = 2304;              // uint8 [2][128]: keys with a NaN scale, by tile parity
-constexpr int kOffScan = 2560;             // int64 [32]
 
 struct __align__(8) Ctl {
     uint64_t qload;           // q boxes landed (TMA, tx-counted)
     uint64_t qready;          // softmax warps: q converted in shared memory
-    uint64_t kfull[6];        // converter warps: a ring block is written
-    uint64_t kfree[6];        // PV commit: a ring block has been read
-    uint64_t ropefull;        // softmax warps: RoPE rows of the tile in tensor memory
-    uint64_t sfull;           // QK commit: S^T ready (every earlier MMA completed too)
-    uint64_t pfull;           // softmax warps: P^T written (and O^T rescaled)
+    uint64_t kfull[10];       // converter warps of a group: a ring block is written
+    uint64_t kfree[10];       // PV commit: a ring block has been read
+    uint64_t sfull[2];        // QK commit, by tile parity: S^T ready (every MMA issued before completed too)
+    uint64_t pfull[2];        // softmax warps, by tile parity: P^T written (and O^T rescaled)
+    uint64_t tfull[kAhead];   // look-up warp: slots and description of a tile
+    uint64_t tfree[kAhead];   // every other warp has taken them
     uint64_t drain;           // every MMA issued completed
     int64_t total;            // tiles of all jobs
     uint32_t tmem_base;
@@ -177,14 +188,13 @@ struct Walk {
         t = 0;
     }
     __device__ __forceinline__ bool last_of_segment() const { return left == 1 || t == j.tiles - 1; }
-    // byte offset of the record of key `key` (0..127) of the tile; -1: none, -2: its page is outside the pool
-    template <int R>
-    __device__ __forceinline__ int64_t record(const KernelArgs& a, int key) const {
+    // slot of key `key` (0..63) of the tile; -1: no such key, -2: its page is outside the pool
+    __device__ __forceinline__ int slot(const KernelArgs& a, int key) const {
         const int pos = kTile * t + key;
-        if (left <= 0 || pos >= j.keys) return -1;
+        if (pos >= j.keys) return -1;
         const int page = __ldg(a.page_table + j.seq * a.table_stride + (pos >> a.page_shift));
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) return -2;
-        return ((static_cast<int64_t>(page) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * R;
+        return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
     }
 };
 
@@ -216,11 +226,90 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+// 16 lanes x 8 kGroups consecutive 32-bit columns over the warp: thread t gets, for each group of eight
+// columns, columns 2 (t & 3), 2 (t & 3) + 1 of lane t >> 2 and of lane (t >> 2) + 8.
+template <int kGroups>
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[4 * kGroups]) {
+    static_assert(kGroups == 2 || kGroups == 4, "");
+    if constexpr (kGroups == 2)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+}
+__device__ __forceinline__ uint32_t ldg_stream2(const void* p) {
+    uint16_t r;
+    asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
     return r;
 }
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// What a converter thread reads of one key: of the two 128-dim blocks c = group, group + 2 the record
+// bytes 64c + 16q .. + 15 (the codes of 16-dim blocks 8c + 2q and 8c + 2q + 1) and their scales, and RoPE
+// dims 16q + 8 group .. + 7.
+template <int R, bool kBlkOrder>
+struct HalfRecord {
+    // 352-byte records place block s's scale at 320 + 8 (s & 3) + (s >> 2): the thread's four scales lie in
+    // one 16-byte half of the field; otherwise block s's scale is at byte s, two pairs
+    static constexpr bool kPermuted = R == 352 && !kBlkOrder;
+    uint4 codes[2];
+    uint32_t sc[kPermuted ? 4 : 2];
+    uint32_t rope[R == 352 ? 2 : 4];
+
+    __device__ __forceinline__ void load_codes(const uint8_t* rec, int q, int group, int i) { codes[i] = ldg_stream16(rec + 64 * (group + 2 * i) + 16 * q); }
+    __device__ __forceinline__ void load_scales(const uint8_t* rec, int q, int group) {
+        if constexpr (kPermuted) {
+            const uint4 x = ldg_stream16(rec + 320 + 16 * (q & 1));
+            sc[0] = x.x; sc[1] = x.y; sc[2] = x.z; sc[3] = x.w;
+        } else {
+            const uint8_t* p = rec + (R == 352 ? 320 : 256) + 8 * group + 2 * q;
+            sc[0] = ldg_stream2(p);
+            sc[1] = ldg_stream2(p + 16);
+        }
+    }
+    __device__ __forceinline__ void load_rope(const uint8_t* rec, int q, int group) {
+        if constexpr (R == 352) {
+            const uint2 x = ldg_stream8(rec + 256 + 16 * q + 8 * group);
+            rope[0] = x.x; rope[1] = x.y;
+        } else {
+            const uint4 x = ldg_stream16(rec + 304 + 32 * q + 16 * group);
+            rope[0] = x.x; rope[1] = x.y; rope[2] = x.z; rope[3] = x.w;
+        }
+    }
+    // the scales of the 16-dim blocks of 128-dim block group + 2i: low byte 8c + 2q, next byte 8c + 2q + 1
+    __device__ __forceinline__ uint32_t scale_pair(int q, int group, int i) const {
+        if constexpr (kPermuted) {
+            const uint32_t bi = static_cast<uint32_t>(2 * group + (q >> 1)) & 3u;   // byte 16 (q & 1) + 2c + (q >> 1)
+            return __byte_perm(i == 0 ? sc[0] : sc[1], i == 0 ? sc[2] : sc[3], bi | ((bi + 4u) << 4)) & 0xFFFFu;
+        } else {
+            return sc[i];
+        }
+    }
+    // RoPE dims as 16-bit values (f16; the bf16 of 432-byte records as they are)
+    __device__ __forceinline__ uint4 rope_values() const {
+        if constexpr (R == 352) {
+            const uint2 a = e4m3x4_to_f16(rope[0]), b = e4m3x4_to_f16(rope[1]);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            return make_uint4(rope[0], rope[1], rope[2], rope[3]);
+        }
+    }
+};
 // Starts bringing `bytes` (a multiple of 16, from a 16-byte boundary) into L2.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -232,7 +321,7 @@ template <int R, bool kBlkOrder, int N>
 __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ KernelArgs a) {
     using S = Shape<N>;
     constexpr int kSoftThreads = 32 * S::kSoft;
-    constexpr int kWarpMma = S::kSoft + S::kConv;
+    constexpr int kWarpMma = S::kSoft + S::kConv, kWarpLook = kWarpMma + 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Ctl* ctl = reinterpret_cast<Ctl*>(smem);
@@ -244,12 +333,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         mbar_init(&ctl->qload, 1);
         mbar_init(&ctl->qready, S::kSoft);
         for (int s = 0; s < S::kRing; ++s) {
-            mbar_init(&ctl->kfull[s], S::kConv);
+            mbar_init(&ctl->kfull[s], S::kConv / 2);
             mbar_init(&ctl->kfree[s], 1);
         }
-        mbar_init(&ctl->ropefull, S::kSoft);
-        mbar_init(&ctl->sfull, 1);
-        mbar_init(&ctl->pfull, S::kSoft);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl->sfull[s], 1);
+            mbar_init(&ctl->pfull[s], S::kSoft);
+        }
+        for (int s = 0; s < kAhead; ++s) {
+            mbar_init(&ctl->tfull[s], 1);
+            mbar_init(&ctl->tfree[s], S::kSoft + S::kConv + 1);
+        }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0u;
         fence_barrier_init();
@@ -328,10 +422,11 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         // nothing to do in this CTA
     } else if (warp < S::kSoft) {
         // ======================= softmax warps =======================
-        const int qd = warp & 3;              // TMEM lane quadrant: keys 32 qd.. of a tile
-        const int h2 = warp >> 2;
-        const int key = 32 * qd + lane;
-        const int rb = S::kRpt * h2;          // rows rb .. rb + kRpt - 1
+        constexpr int kGroups = S::kCols / 8;
+        const int qd = warp & 3;              // TMEM lane quadrant: keys 16 qd .. 16 qd + 15 of a tile, and 128 dims' share of O^T
+        const int rb = S::kCols * (warp >> 2);   // rows rb .. rb + kCols - 1
+        const int k0 = 16 * qd + (lane >> 2); // this thread's keys: k0 and k0 + 8; its rows: c0 + 8g, c0 + 8g + 1
+        const int c0 = rb + 2 * (lane & 3);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * qd) << 16);
         const uint32_t cm_s = sbase + kOffCM;
         const uint32_t alpha_s = sbase + kOffAlpha;
@@ -340,54 +435,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         auto ch_addr = [&](int r) { return cm_s + 16 * (r >> 1) + 4 * (r & 1); };
         auto negm_addr = [&](int r) { return cm_s + 16 * (r >> 1) + 8 + 4 * (r & 1); };
 
-        constexpr int kRopeVec = S::kRopeDims * (R == 352 ? 1 : 2) / 16;
-        uint4 rope[kRopeVec];
-        auto load_rope = [&](int64_t off) {
-            if (off >= 0) {
-                const uint8_t* src = a.cache + off + (R == 352 ? 256 : 304) + h2 * (16 * kRopeVec);
-#pragma unroll
-                for (int e = 0; e < kRopeVec; ++e) rope[e] = ldg_stream16(src + 16 * e);
-            }
-        };
-        // the RoPE dims of this key into tensor memory; zero for a key that is not there
-        auto store_rope = [&](bool there) {
-#pragma unroll
-            for (int part = 0; part < S::kRopeDims / 32; ++part) {
-                uint32_t v[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = 0u;
-                if (there) {
-                    if constexpr (R == 352) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint4 x = rope[2 * part + e];
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const uint2 f = e4m3x4_to_f16(w[m]);
-                                v[8 * e + 2 * m] = f.x;
-                                v[8 * e + 2 * m + 1] = f.y;
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 x = rope[4 * part + e];
-                            v[4 * e] = x.x;
-                            v[4 * e + 1] = x.y;
-                            v[4 * e + 2] = x.z;
-                            v[4 * e + 3] = x.w;
-                        }
-                    }
-                }
-                tmem_st16(lane_base + S::kColR + (S::kRopeDims / 2) * h2 + 16 * part, v);
-            }
-            tmem_wait_st();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->ropefull);
-        };
-
         bool ok = true;
         // q of a job's rows into shared memory (TMA); rows behind the sequence's last one are those of the
         // next sequence or zeros, and reach columns that nothing reads
@@ -395,7 +442,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             if (threadIdx.x == 0) {
                 mbar_arrive_expect_tx(&ctl->qload, 9u * S::kQBlk);
                 for (int bx = 0; bx < 9; ++bx)
-                    tma_load_2d(sbase + S::kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.rows_per_seq + j.row0, &ctl->qload);
+                    tma_load_2d(sbase + kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.rows_per_seq + j.row0, &ctl->qload);
             }
         };
         // per-row prescale and f16 (bf16 RoPE for 432-byte records) in place; the rows' scales and positions
@@ -407,7 +454,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             if (ok) {
 #pragma unroll 3
                 for (int k = kChunks * part; k < kChunks * part + kChunks; ++k) {
-                    const uint4 x = lds_u128(sbase + S::kOffQ + (k >> 3) * S::kQBlk + swz(r, k & 7));
+                    const uint4 x = lds_u128(sbase + kOffQ + (k >> 3) * S::kQBlk + swz(r, k & 7));
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
@@ -433,7 +480,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
 #pragma unroll 3
                 for (int k = kChunks * part; k < kChunks * part + kChunks; ++k) {
                     const bool bf = R == 432 && k >= 64;   // bf16 RoPE of 432-byte records
-                    const uint32_t addr = sbase + S::kOffQ + (k >> 3) * S::kQBlk + swz(r, k & 7);
+                    const uint32_t addr = sbase + kOffQ + (k >> 3) * S::kQBlk + swz(r, k & 7);
                     const uint4 x = lds_u128(addr);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t y[4];
@@ -451,174 +498,204 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             named_bar_sync(1, kSoftThreads);   // the rows' scales, references and positions are written
         };
 
-        Walk<N> cur, ahead;
-        cur.start(a, ctl->job0, ctl->tile0, count);
-        ahead = cur;
-        load_q(cur.j);
-        int64_t off = ahead.template record<R>(a, key);
-        load_rope(off);
-        ahead.next(a);
-        int64_t off_n = ahead.template record<R>(a, key);
         int seg = 0;
-        stage_q(cur.j, seg);
-        store_rope(off >= 0);
+        const Job first_job = job_info<N>(a, ctl->job0);
+        load_q(first_job);
+        stage_q(first_job, seg);
         bool seg_first = true;
-        int seg_tile = cur.t;                  // the segment's first tile
-        float l[S::kRpt];                      // this key lane's share of each row's sum of 2^(z - m)
+        int seg_tile = ctl->tile0;             // the segment's first tile
+        float l[kGroups][2];                   // this thread's share of its rows' sums of 2^(z - m)
 #pragma unroll
-        for (int e = 0; e < S::kRpt; ++e) l[e] = 0.0f;
+        for (int g = 0; g < kGroups; ++g) l[g][0] = l[g][1] = 0.0f;
         int4 hdr = make_int4(0, 0, 0, 0);
 
-        // P^T in shared memory. N = 64: row = key, 64 rows of the tile across (MN-major B operand); N = 16, 32:
-        // row = query row, 64 keys across, twice (K-major B operand)
-        const uint32_t p_key = N == 64 ? sbase + S::kOffP + (key >> 3) * 1024 + (key & 7) * 128
-                                       : sbase + S::kOffP + (key >> 6) * (N * 128) + (key & 7) * 2;
-        const uint32_t p_chunk = static_cast<uint32_t>((key & 63) >> 3) << 4;
-
-        // Every softmax warp takes part in every named barrier below, also after a wait ran out (then it only
-        // passes the barriers), so no warp can be left waiting on a missing one. Tensor-memory loads and stores
-        // are warp-collective: masks change values only.
+        // Every softmax warp takes part in every named barrier below, also after a wait ran out in it, until
+        // the next vote, where all leave together: no warp is left waiting on a missing one. Tensor-memory loads
+        // and stores are warp-collective: masks change values only.
         for (int it = 0; it < count; ++it) {
-            if (it + 1 < count) load_rope(off_n);   // in flight while this tile is scored
-            ahead.next(a);
-            const int64_t off_n2 = ahead.template record<R>(a, key);
-            const bool there = off >= 0;
-            const int pos = kTile * cur.t + key;
-            const bool full = kTile * cur.t + kTile - 1 <= cur.j.first_pos;   // every row sees every key of the tile
+            const int at = it % kAhead;
+            if (ok) ok = wait_warp(ctl, &ctl->tfull[at], (it / kAhead) & 1, a.status);
+            const uint32_t slot_s = sbase + kOffSlot + 4 * kTile * at;
+            const bool there0 = ok && static_cast<int>(lds_u32(slot_s + 4 * k0)) >= 0;
+            const bool there1 = ok && static_cast<int>(lds_u32(slot_s + 4 * k0 + 32)) >= 0;
+            const uint4 tile = lds_u128(sbase + kOffTile + 16 * at);
+            const int pos0 = static_cast<int>(tile.x), pos = pos0 + k0;
+            const bool last_of_segment = (tile.z & 2u) != 0u || it + 1 == count;
+            const bool full = pos0 + kTile - 1 <= static_cast<int>(tile.y);   // every row sees every key of the tile
             const uint32_t s_col = lane_base + S::kColS + N * (it & 1) + rb;
-            float ln[S::kRpt];
-            float nan_add = 0.0f;
-            // one pass over this key's scores: P (against the current references), the sums, the largest z - m
-            auto score = [&]() -> float {
+            float z[kGroups][4];
+            // z - m of this thread's scores (-inf for a row that does not see the key); returns the largest
+            auto load_z = [&]() -> float {
+                uint32_t sv[4 * kGroups];
+                tmem_ld_16x256<kGroups>(s_col, sv);
+                tmem_wait_ld();
                 float tmax = -INFINITY;
 #pragma unroll
-                for (int part = 0; part < S::kRpt / 16; ++part) {
-                    uint32_t sv[16];
-                    tmem_ld16(s_col + 16 * part, sv);
-                    tmem_wait_ld();
+                for (int g = 0; g < kGroups; ++g) {
+                    const uint4 c = lds_u128(cm_s + 8 * (c0 + 8 * g));
+                    const uint64_t ch = f32x2_pack(__uint_as_float(c.x), __uint_as_float(c.y));
+                    const uint64_t nm = f32x2_pack(__uint_as_float(c.z), __uint_as_float(c.w));
+                    const float2 a0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g]), __uint_as_float(sv[4 * g + 1])), ch, nm));
+                    const float2 a1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g + 2]), __uint_as_float(sv[4 * g + 3])), ch, nm));
+                    z[g][0] = a0.x;
+                    z[g][1] = a0.y;
+                    z[g][2] = a1.x;
+                    z[g][3] = a1.y;
+                }
+                if (!full) {
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2) {
-                        uint32_t pw[4];
+                    for (int g = 0; g < kGroups; ++g) {
+                        const uint2 qp = lds_u64(pos_s + 4 * (c0 + 8 * g));
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int e = 8 * c2 + 2 * g, r = 16 * part + e;   // rows rb + r, rb + r + 1
-                            const uint4 c = lds_u128(cm_s + 8 * (rb + r));
-                            uint64_t z2 = f32x2_fma(f32x2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
-                                                    f32x2_pack(__uint_as_float(c.x), __uint_as_float(c.y)),
-                                                    f32x2_pack(__uint_as_float(c.z), __uint_as_float(c.w)));
-                            z2 = f32x2_add(z2, f32x2_pack(nan_add, nan_add));
-                            const float2 z = f32x2_unpack(z2);
-                            bool v0 = there, v1 = there;
-                            if (!full) {
-                                const uint2 qp = lds_u64(pos_s + 4 * (rb + r));
-                                v0 = there && pos <= static_cast<int>(qp.x);
-                                v1 = there && pos <= static_cast<int>(qp.y);
-                            }
-                            tmax = fmax3(tmax, v0 ? z.x : -INFINITY, v1 ? z.y : -INFINITY);
-                            const float p0 = v0 ? ex2_approx(z.x) : 0.0f, p1 = v1 ? ex2_approx(z.y) : 0.0f;
-                            ln[r] = l[r] + p0;
-                            ln[r + 1] = l[r + 1] + p1;
-                            pw[g] = pack_f16x2(p0, p1);
-                            if constexpr (N != 64) {
-                                const int rr = S::kRpt * h2 + r;
-                                const uint32_t base = p_key + static_cast<uint32_t>((rr >> 3) * 1024 + (rr & 7) * 128);
-                                sts_u16(base + (p_chunk ^ ((rr & 7) << 4)), static_cast<uint16_t>(pw[g]));
-                                sts_u16(base + 128 + (p_chunk ^ (((rr & 7) + 1) << 4)), static_cast<uint16_t>(pw[g] >> 16));
-                            }
-                        }
-                        if constexpr (N == 64)
-                            sts_u128(p_key + (((4 * h2 + 2 * part + c2) ^ (key & 7)) << 4), make_uint4(pw[0], pw[1], pw[2], pw[3]));
+                        for (int e = 0; e < 4; ++e)
+                            if (pos + 8 * (e >> 1) > static_cast<int>((e & 1) ? qp.y : qp.x)) z[g][e] = -INFINITY;
                     }
                 }
+                if (!there0 || !there1) {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!(e < 2 ? there0 : there1)) z[g][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) tmax = fmax3(fmax3(tmax, z[g][0], z[g][1]), z[g][2], z[g][3]);
                 return tmax;
             };
             float tmax = -INFINITY;
-            if (ok) ok = wait_warp(ctl, &ctl->kfull[(4 * it) % S::kRing], (4 * it / S::kRing) & 1, a.status);
-            if (ok) ok = wait_warp(ctl, &ctl->sfull, it & 1, a.status);
+            uint32_t nan0 = 0u, nan1 = 0u;
+            // (the scores' MMAs were issued behind the waits for the blocks that the flags were written before)
+            if (ok) ok = wait_warp(ctl, &ctl->sfull[it & 1], (it >> 1) & 1, a.status);
             if (ok) {
+                if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
                 tc_fence_after_sync();
-                if (lds_u8(sbase + kOffNan + 128 * (it & 1) + key) != 0u) nan_add = NAN;
-                tmax = score();
+                const uint32_t nan_s = sbase + kOffNan + 128 * (it & 3) + k0;
+                nan0 = lds_u8(nan_s) | lds_u8(nan_s + 64);
+                nan1 = lds_u8(nan_s + 8) | lds_u8(nan_s + 72);
+                tmax = load_z();
             }
-            // ---- does any row need a new reference? (one barrier reduction)
-            if (bar_red_or(1, kSoftThreads, tmax > kRescaleThreshold)) {
-                // per row: the tile's largest z over the 128 keys (warp maximum, then the four quadrants)
-                float mine = -INFINITY;
-#pragma unroll
-                for (int part = 0; part < S::kRpt / 16; ++part) {
-                    uint32_t sv[16];
-                    if (ok) {
-                        tmem_ld16(s_col + 16 * part, sv);
-                        tmem_wait_ld();
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int r = rb + 16 * part + e;
-                        bool v = ok && there;
-                        if (!full) v = v && pos <= static_cast<int>(lds_u32(pos_s + 4 * r));
-                        const float wm = warp_max(v ? __uint_as_float(sv[e]) * lds_f32(ch_addr(r)) : -INFINITY);
-                        if (lane == 16 * part + e) mine = wm;
-                    }
+            // ---- does any row need a new reference? (one barrier reduction; also entered where a wait ran out,
+            // and then left by every softmax warp at once)
+            if (bar_red_or(1, kSoftThreads, tmax > kRescaleThreshold || !ok)) {
+                // O^T stands still once the PV of the tile before has completed
+                if (ok && !seg_first) {
+                    const int g = 4 * it - 1;
+                    ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                    tc_fence_after_sync();
                 }
-                if (lane < S::kRpt) sts_f32(xmax_s + 16 * (rb + lane) + 4 * qd, mine);
+                if (bar_red_or(1, kSoftThreads, !ok)) {
+                    ok = false;
+                    break;
+                }
+                // per row: the tile's largest z over the 64 keys (a thread's two, the warp's, then the four quadrants)
+                {
+                    uint32_t sv[4 * kGroups];
+                    tmem_ld_16x256<kGroups>(s_col, sv);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = c0 + 8 * g + e;
+                            const int last = static_cast<int>(lds_u32(pos_s + 4 * r));
+                            const float ch = lds_f32(ch_addr(r));
+                            float m = -INFINITY;
+                            if (there0 && pos <= last) m = __uint_as_float(sv[4 * g + e]) * ch;
+                            if (there1 && pos + 8 <= last) m = fmaxf(m, __uint_as_float(sv[4 * g + 2 + e]) * ch);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            if (lane < 4) sts_f32(xmax_s + 16 * r + 4 * qd, m);
+                        }
+                }
                 named_bar_sync(1, kSoftThreads);
-                if (qd == 0 && lane < S::kRpt) {   // one thread per row: the new reference and the rescale factor
-                    const uint4 x = lds_u128(xmax_s + 16 * (rb + lane));
+                if (qd == 0 && lane < S::kCols) {   // one thread per row: the new reference and the rescale factor
+                    const int r = rb + lane;
+                    const uint4 x = lds_u128(xmax_s + 16 * r);
                     const float zt = fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
                                            fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
-                    const float mo = -lds_f32(negm_addr(rb + lane));
+                    const float mo = -lds_f32(negm_addr(r));
                     float al = 1.0f;
                     if (zt > mo + kRescaleThreshold) {
                         al = mo == -INFINITY ? 0.0f : ex2_approx(mo - zt);
-                        sts_f32(negm_addr(rb + lane), -zt);
+                        sts_f32(negm_addr(r), -zt);
                     }
-                    sts_f32(alpha_s + 4 * (rb + lane), al);
+                    sts_f32(alpha_s + 4 * r, al);
                 }
                 named_bar_sync(1, kSoftThreads);
-                if (ok) {
-                    if (!seg_first) {
-                        // O^T (dims 128b + key lane, this warp's rows) *= alpha; PV of the previous tile has
-                        // completed (it was issued before the QK whose commit was just waited for)
+                if (!seg_first) {
+                    // O^T (this warp's 32 lanes of each block of dims, its rows) *= alpha
 #pragma unroll 1
-                        for (int c = 0; c < 4 * (S::kRpt / 16); ++c) {
-                            const int r0 = rb + 16 * (c % (S::kRpt / 16));
-                            const uint32_t col = lane_base + S::kColO + N * (c / (S::kRpt / 16)) + r0;
-                            uint32_t o[16];
-                            tmem_ld16(col, o);
-                            tmem_wait_ld();
+                    for (int c = 0; c < 4 * (S::kCols / 16); ++c) {
+                        const int r0 = rb + 16 * (c % (S::kCols / 16));
+                        const uint32_t col = lane_base + S::kColO + N * (c / (S::kCols / 16)) + r0;
+                        uint32_t o[16];
+                        tmem_ld16(col, o);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha_s + 4 * (r0 + e)));
-                            tmem_st16(col, o);
-                        }
-                        tmem_wait_st();
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha_s + 4 * (r0 + e)));
+                        tmem_st16(col, o);
                     }
+                    tmem_wait_st();
+                }
 #pragma unroll
-                    for (int e = 0; e < S::kRpt; ++e) l[e] *= lds_f32(alpha_s + 4 * (rb + e));
-                    (void)score();   // P and the sums again against the moved references
+                for (int g = 0; g < kGroups; ++g) {
+                    l[g][0] *= lds_f32(alpha_s + 4 * (c0 + 8 * g));
+                    l[g][1] *= lds_f32(alpha_s + 4 * (c0 + 8 * g) + 4);
+                }
+                (void)load_z();   // against the moved references
+            }
+            if ((nan0 | nan1) != 0u) {   // a NaN key: NaN for the rows that see it
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((e < 2 ? nan0 : nan1) != 0u && z[g][e] != -INFINITY) z[g][e] = NAN;
+            }
+            // P^T in shared memory. N = 64: row = key, 64 rows of the tile across (MN-major B operand); N = 16, 32:
+            // row = query row, 64 keys across (K-major B operand)
+            const uint32_t p_s = sbase + S::kOffP + S::kPBytes * (it & 1);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int c = c0 + 8 * g;
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(z[g][e]);
+                l[g][0] += p[0] + p[2];
+                l[g][1] += p[1] + p[3];
+                const uint32_t w0 = pack_f16x2(p[0], p[1]), w1 = pack_f16x2(p[2], p[3]);
+                if constexpr (N == 64) {
+                    sts_u32(p_s + swz(k0, c >> 3) + 2 * (c & 7), w0);
+                    sts_u32(p_s + swz(k0 + 8, c >> 3) + 2 * (c & 7), w1);
+                } else {
+                    const uint32_t x = p_s + 2 * (k0 & 7);
+                    sts_u16(x + swz(c, k0 >> 3), static_cast<uint16_t>(w0));
+                    sts_u16(x + swz(c + 1, k0 >> 3), static_cast<uint16_t>(w0 >> 16));
+                    sts_u16(x + swz(c, (k0 >> 3) + 1), static_cast<uint16_t>(w1));
+                    sts_u16(x + swz(c + 1, (k0 >> 3) + 1), static_cast<uint16_t>(w1 >> 16));
                 }
             }
-            if (ok) {
-#pragma unroll
-                for (int e = 0; e < S::kRpt; ++e) l[e] = ln[e];
-                fence_proxy_async_smem();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->pfull);
-                // RoPE rows of the next tile (this tile's QK, which read the current ones, is done)
-                if (it + 1 < count) store_rope(off_n >= 0);
-            }
-            off = off_n;
-            off_n = off_n2;
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->pfull[it & 1]);
             seg_first = false;
 
-            if (cur.last_of_segment()) {
-                const Job j = cur.j;
-                const int t_end = cur.t;
-                Walk<N> nxt = cur;
-                nxt.next(a);
+            if (last_of_segment) {
+                const Job j = job_info<N>(a, static_cast<int>(tile.w));
+                const int t_end = pos0 / kTile;
                 const bool more = it + 1 < count;
-                if (more && ok) load_q(nxt.j);   // every QK of this segment has completed
+                Job next_job = j;
+                int next_tile = 0;
+                if (more) {
+                    if (ok) ok = wait_warp(ctl, &ctl->tfull[(it + 1) % kAhead], ((it + 1) / kAhead) & 1, a.status);
+                    if (ok) {
+                        const uint4 nt = lds_u128(sbase + kOffTile + 16 * ((it + 1) % kAhead));
+                        next_job = job_info<N>(a, static_cast<int>(nt.w));
+                        next_tile = static_cast<int>(nt.x) / kTile;
+                        load_q(next_job);   // every QK of this segment has completed
+                    }
+                }
                 // ---- row sums, O^T / l, out (or the job's part) and lse
                 bool have_o = false;
                 if (ok) {
@@ -630,18 +707,18 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 const bool whole = seg_tile == 0 && t_end == j.tiles - 1;
                 const int slot = 2 * blockIdx.x + (seg_tile == 0 ? 1 : 0);
                 const int64_t row = static_cast<int64_t>(j.seq) * a.rows_per_seq + j.row0;
-                float sums = 0.0f;
 #pragma unroll
-                for (int e = 0; e < S::kRpt; ++e) {
-                    float v = l[e];
-                    l[e] = 0.0f;
+                for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (lane == e) sums = v;
-                }
-                if (lane < S::kRpt) sts_f32(xmax_s + 16 * (rb + lane) + 4 * qd, sums);
+                    for (int e = 0; e < 2; ++e) {
+                        float v = l[g][e];
+                        l[g][e] = 0.0f;
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                        if (lane < 4) sts_f32(xmax_s + 16 * (c0 + 8 * g + e) + 4 * qd, v);
+                    }
                 named_bar_sync(1, kSoftThreads);
-                if (qd == 0 && lane < S::kRpt) {
+                if (qd == 0 && lane < S::kCols) {
                     const int r = rb + lane;
                     const uint4 x = lds_u128(xmax_s + 16 * r);
                     const float sum = (__uint_as_float(x.x) + __uint_as_float(x.y)) + (__uint_as_float(x.z) + __uint_as_float(x.w));
@@ -668,8 +745,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 uint16_t* dst = whole ? reinterpret_cast<uint16_t*>(a.out) + row * 512
                                       : a.part_out + static_cast<int64_t>(slot) * N * 512;
 #pragma unroll 1
-                for (int c = 0; c < 4 * (S::kRpt / 16); ++c) {
-                    const int b = c / (S::kRpt / 16), r0 = rb + 16 * (c % (S::kRpt / 16));
+                for (int c = 0; c < 4 * (S::kCols / 16); ++c) {
+                    const int b = c / (S::kCols / 16), r0 = rb + 16 * (c % (S::kCols / 16));
                     uint32_t o[16];
                     if (have_o) {
                         tmem_ld16(lane_base + S::kColO + N * b + r0, o);
@@ -696,188 +773,219 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 named_bar_sync(1, kSoftThreads);   // the factors and references have been read
                 if (more) {
                     ++seg;
-                    stage_q(nxt.j, seg);
+                    stage_q(next_job, seg);
                     seg_first = true;
-                    seg_tile = nxt.t;
+                    seg_tile = next_tile;
                 }
             }
-            cur.next(a);
         }
         if (threadIdx.x == 0) a.hdr[blockIdx.x] = hdr;
     } else if (warp < kWarpMma) {
-        // ============ converters: K dims 0-511, 16-dim blocks 8c + 2q, 8c + 2q + 1 of each key ============
-        const int t = threadIdx.x - 32 * S::kSoft;
-        // lane l of converter warp w: key 8w + (l & 7) (and 64 more), quarter q = l >> 3: the eight lanes of a
-        // quarter-warp store to eight bank slots, and the four quarters of a key load one 64-byte run
+        // ============ converters: two groups of eight warps, group g the 128-dim blocks g and g + 2 ============
+        const int group = (warp - S::kSoft) >> 3;
+        const int t = (threadIdx.x - 32 * S::kSoft) & 255;
+        // lane l of a group's warp w: key 8w + (l & 7), quarter q = l >> 3: the eight lanes of a quarter-warp
+        // store to eight bank slots, and the four quarters of a key load one 64-byte run
         const int q = (t >> 3) & 3;
         const int j = (t & 7) + 8 * (t >> 5);
-        const uint32_t k_s = sbase + S::kOffK;
+        const uint32_t row_s = sbase + S::kOffK + (q >> 1) * kSubBlk;
+        const int ch0 = 4 * (q & 1);
         bool ok = true;
-        KeyRaw<R, kBlkOrder> raw[S::kKeys];
-        int64_t o[S::kKeys], n[S::kKeys], m[S::kKeys];   // records of this tile, the next, the one behind
-        Walk<N> ahead;
-        ahead.start(a, ctl->job0, ctl->tile0, count);
-#pragma unroll
-        for (int u = 0; u < S::kKeys; ++u) {
-            o[u] = ahead.template record<R>(a, j + 64 * u);
-            if (o[u] >= 0) raw[u].load(a.cache + o[u], q);
-        }
-        // records that will be loaded later go into L2: eight keys of a warp are one run of a page (of eight
-        // records or more), else each record by itself
-        auto prefetch = [&](const int64_t (&r)[S::kKeys]) {
-#pragma unroll
-            for (int u = 0; u < S::kKeys; ++u) {
-                if (a.page_shift >= 3) {
-                    if (lane == 0 && r[u] >= 0) prefetch_l2_bulk(a.cache + r[u], 8u * R);
-                } else if (q == 0 && r[u] >= 0) {
-                    prefetch_l2_bulk(a.cache + r[u], R);
-                }
-            }
+        HalfRecord<R, kBlkOrder> raw;
+        int cur = -1, nxt = -1;                       // slots of this thread's key in this tile, in the next
+        auto take = [&](int k) {
+            nxt = -1;
+            if (k >= count) return;
+            if (ok) ok = wait_warp(ctl, &ctl->tfull[k % kAhead], (k / kAhead) & 1, a.status);
+            if (ok) nxt = static_cast<int>(lds_u32(sbase + kOffSlot + 4 * kTile * (k % kAhead) + 4 * j));
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&ctl->tfree[k % kAhead]);
         };
-        ahead.next(a);
-#pragma unroll
-        for (int u = 0; u < S::kKeys; ++u) n[u] = ahead.template record<R>(a, j + 64 * u);
-        prefetch(n);
-        ahead.next(a);
-#pragma unroll
-        for (int u = 0; u < S::kKeys; ++u) m[u] = ahead.template record<R>(a, j + 64 * u);
-        prefetch(m);
-        int slot = 0, round = 0;                          // ring slot of the next block, times around the ring
+        take(0);
+        cur = nxt;
+        if (cur >= 0) {
+            const uint8_t* rec = a.cache + static_cast<int64_t>(cur) * R;
+            raw.load_codes(rec, q, group, 0);
+            raw.load_codes(rec, q, group, 1);
+            raw.load_scales(rec, q, group);
+            raw.load_rope(rec, q, group);
+        }
+        int slot = group, round = 0;                  // ring slot of this group's next block, times around the ring
         for (int k = 0; k < count; ++k) {
-            bool v[S::kKeys];
-            uint32_t sp[S::kKeys][2];
+            take(k + 1);
+            const uint8_t* next_rec = a.cache + static_cast<int64_t>(max(nxt, 0)) * R;
+            const uint32_t sp0 = raw.scale_pair(q, group, 0), sp1 = raw.scale_pair(q, group, 1);
+            // dims with a NaN scale become zeros, and the key's scores NaN
+            const uint32_t nan = __ballot_sync(0xffffffffu, cur >= 0 && has_nan_e4m3(sp0 | (sp1 << 16)));
+            const bool bad = ((nan >> (lane & 7)) & 0x01010101u) != 0u;
+            const bool v = cur >= 0 && !bad;
+            if (q == 0) sts_u8(sbase + kOffNan + 128 * (k & 3) + 64 * group + j, bad ? 1u : 0u);
+            if (nxt >= 0) raw.load_scales(next_rec, q, group);
 #pragma unroll
-            for (int u = 0; u < S::kKeys; ++u) {
-                if (q == 0 && o[u] == -2 && a.status != nullptr) atomicOr(a.status, 0x2u);
-                v[u] = o[u] >= 0;
-                raw[u].scale_pairs(q, sp[u]);
-                // a key with a NaN scale becomes a zero row, and its scores NaN
-                const uint32_t nan = __ballot_sync(0xffffffffu, v[u] && (has_nan_e4m3(sp[u][0]) || has_nan_e4m3(sp[u][1])));
-                const bool bad = ((nan >> (lane & 7)) & 0x01010101u) != 0u;
-                if (bad) v[u] = false;
-                if (q == 0) sts_u8(sbase + kOffNan + 128 * (k & 1) + j + 64 * u, bad ? 1u : 0u);
-                if (n[u] >= 0) raw[u].load_scales(a.cache + n[u], q);
-            }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (round > 0) ok = wait_warp(ctl, &ctl->kfree[slot], (round - 1) & 1, a.status);
+            for (int i = 0; i < 2; ++i) {
+                if (ok && round > 0) ok = wait_warp(ctl, &ctl->kfree[slot], (round - 1) & 1, a.status);
                 if (!ok) break;
-                const uint32_t blk = k_s + slot * kBlk + (q >> 1) * kSubBlk;
-                const int ch0 = 4 * (q & 1);
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int u = 0; u < S::kKeys; ++u) {
-                    const uint32_t s2 = sp[u][b >> 1] >> (16 * (b & 1));
-                    const __half2 sa = scale_half2(s2 & 0xFFu), sb = scale_half2((s2 >> 8) & 0xFFu);
-                    const int row = j + 64 * u;
-                    sts_u128(blk + swz(row, ch0), v[u] ? dq8(raw[u].codes[b].x, sa) : z);
-                    sts_u128(blk + swz(row, ch0 + 1), v[u] ? dq8(raw[u].codes[b].y, sa) : z);
-                    sts_u128(blk + swz(row, ch0 + 2), v[u] ? dq8(raw[u].codes[b].z, sb) : z);
-                    sts_u128(blk + swz(row, ch0 + 3), v[u] ? dq8(raw[u].codes[b].w, sb) : z);
-                }
+                const uint32_t blk = row_s + slot * kBlk;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t sp = i == 0 ? sp0 : sp1;
+                const __half2 sa = scale_half2(sp & 0xFFu), sb = scale_half2(sp >> 8);
+                sts_u128(blk + swz(j, ch0), v ? dq8(raw.codes[i].x, sa) : zero);
+                sts_u128(blk + swz(j, ch0 + 1), v ? dq8(raw.codes[i].y, sa) : zero);
+                sts_u128(blk + swz(j, ch0 + 2), v ? dq8(raw.codes[i].z, sb) : zero);
+                sts_u128(blk + swz(j, ch0 + 3), v ? dq8(raw.codes[i].w, sb) : zero);
+                // The RoPE dims go to the buffer of kRopeRing tiles ago: the PV commit that freed this group's first
+                // block of the tile (or, before the ring's first round, no tile at all) came behind that QK
+                if (i == 0) sts_u128(sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk + swz(j, 2 * q + group), cur >= 0 ? raw.rope_values() : zero);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->kfull[slot]);
-#pragma unroll
-                for (int u = 0; u < S::kKeys; ++u)
-                    if (n[u] >= 0) raw[u].load_codes(a.cache + n[u], q, b);
-                if (++slot == S::kRing) {
-                    slot = 0;
+                if (nxt >= 0) {
+                    raw.load_codes(next_rec, q, group, i);
+                    if (i == 0) raw.load_rope(next_rec, q, group);
+                }
+                slot += 2;
+                if (slot >= S::kRing) {
+                    slot -= S::kRing;
                     ++round;
                 }
             }
             if (!ok) break;
-            ahead.next(a);
+            cur = nxt;
+        }
+    } else if (warp == kWarpLook) {
+        // ============ look-up warp: the slots of the keys of every tile, and their records into L2 ============
+        Walk<N> w;
+        w.start(a, ctl->job0, ctl->tile0, count);
+        bool first = true;
+        for (int it = 0; it < count; ++it) {
+            const int at = it % kAhead;
+            if (it >= kAhead && !wait_warp(ctl, &ctl->tfree[at], (it / kAhead - 1) & 1, a.status)) break;
+            int slot[2];
 #pragma unroll
-            for (int u = 0; u < S::kKeys; ++u) {
-                o[u] = n[u];
-                n[u] = m[u];
-                m[u] = ahead.template record<R>(a, j + 64 * u);
+            for (int e = 0; e < 2; ++e) slot[e] = w.slot(a, 32 * e + lane);
+            bool outside = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                outside = outside || slot[e] == -2;
+                sts_u32(sbase + kOffSlot + 4 * (kTile * at + 32 * e + lane), static_cast<uint32_t>(slot[e]));
+                // eight keys are one run of a page (of eight records or more)
+                if (a.page_shift >= 3) {
+                    if ((lane & 7) == 0 && slot[e] >= 0) prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[e]) * R, 8u * R);
+                } else if (slot[e] >= 0) {
+                    prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[e]) * R, R);
+                }
             }
-            prefetch(m);
+            if (outside && a.status != nullptr) atomicOr(a.status, 0x2u);
+            const bool last = w.last_of_segment();
+            if (lane == 0)
+                sts_u128(sbase + kOffTile + 16 * at, make_uint4(static_cast<uint32_t>(kTile * w.t), static_cast<uint32_t>(w.j.first_pos),
+                                                                (first ? 1u : 0u) | (last ? 2u : 0u), static_cast<uint32_t>(w.job)));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tfull[at]);
+            first = last;
+            w.next(a);
         }
     } else {
         // ======================= MMA issuer =======================
-        const uint32_t idesc_qk = idesc_f16_f32(128, N, false, false);
-        const uint32_t idesc_rope = R == 432 ? idesc_bf16_f32(128, N, false, false) : idesc_qk;
+        const uint32_t idesc_qk = idesc_f16_f32(64, N, false, false);
+        const uint32_t idesc_rope = R == 432 ? idesc_bf16_f32(64, N, false, false) : idesc_qk;
         const uint32_t idesc_pv = idesc_f16_f32(128, N, true, N == 64);
         const uint64_t kdesc0 = sdesc_sw128(sbase + S::kOffK, 16, 1024);          // K-major: keys x dims
-        const uint64_t qdesc0 = sdesc_sw128(sbase + S::kOffQ, 16, 1024);          // K-major: rows x dims
+        const uint64_t rdesc0 = sdesc_sw128(sbase + S::kOffRope, 16, 1024);       // K-major: keys x RoPE dims
+        const uint64_t qdesc0 = sdesc_sw128(sbase + kOffQ, 16, 1024);             // K-major: rows x dims
         const uint64_t vdesc0 = sdesc_sw128(sbase + S::kOffK, kSubBlk, 1024);     // MN-major: dims x keys
         // P^T: MN-major rows x keys (N = 64), K-major rows x keys (N = 16, 32)
-        const uint64_t pdesc0 = N == 64 ? sdesc_sw128(sbase + S::kOffP, kTile * 128, 1024) : sdesc_sw128(sbase + S::kOffP, 16, 1024);
+        const uint64_t pdesc0 = sdesc_sw128(sbase + S::kOffP, N == 64 ? S::kPBytes : 16, 1024);
+        constexpr int kPStep = N == 64 ? 2048 : 32;                               // 16 keys of P
         const bool leader = elect_one_in_warp();
         bool ok = true;
-        Walk<N> w;
-        w.start(a, ctl->job0, ctl->tile0, count);
-        int qk_slot = 0, qk_round = 0, pv_slot = 0, seg = 0;
-        bool first = true, prev_first = true;
-        auto qk_block = [&](int b, uint32_t d) {   // dims 128b .. 128b + 127 as soon as they are converted
-            ok = wait_warp(ctl, &ctl->kfull[qk_slot], qk_round & 1, a.status);
-            if (!ok) return;
-            tc_fence_after_sync();
-            if (leader) {
-                const uint64_t kd = kdesc0 + static_cast<uint64_t>((qk_slot * kBlk) >> 4);
-                const uint64_t qd = qdesc0 + static_cast<uint64_t>((2 * b * S::kQBlk) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(d, kd + static_cast<uint64_t>(((kk >> 2) * kSubBlk + (kk & 3) * 32) >> 4),
-                           qd + static_cast<uint64_t>(((kk >> 2) * S::kQBlk + (kk & 3) * 32) >> 4), idesc_qk,
-                           (b > 0 || kk > 0) ? 1u : 0u);
-            }
-            __syncwarp();
-            if (++qk_slot == S::kRing) {
-                qk_slot = 0;
-                ++qk_round;
-            }
-        };
-        auto pv = [&](int tile, bool fresh) {      // O^T += V^T P^T of a tile; its ring blocks are free then
-            ok = wait_warp(ctl, &ctl->pfull, tile & 1, a.status);
-            if (!ok) return;
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
+        int qi = 0, qb = 0, qk_slot = 0, qk_round = 0;   // the next QK block
+        int pi = 0, pv_slot = 0;                         // the next PV
+        int seg = 0;
+        uint32_t fresh = 0u;                             // bit t & 1: tile t is the first of its segment
+        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)); };
+        bool open = false;                               // tile qi's description is read and its queries are staged
+        uint32_t idle = 0;
+        uint64_t idle_since = 0;
+        while (pi < count) {
+            bool moved = false;
+            if (pi < qi && ready(&ctl->pfull[pi & 1], (pi >> 1) & 1)) {
+                // O^T += V^T P^T of tile pi; its ring blocks are free then
+                tc_fence_after_sync();
+                const bool first = ((fresh >> (pi & 1)) & 1u) != 0u;
                 if (leader) {
-                    const uint64_t vd = vdesc0 + static_cast<uint64_t>((pv_slot * kBlk) >> 4);
+                    const uint64_t pd = pdesc0 + static_cast<uint64_t>((S::kPBytes * (pi & 1)) >> 4);
+#pragma unroll 1
+                    for (int b = 0; b < 4; ++b) {
+                        const uint64_t vd = vdesc0 + static_cast<uint64_t>((pv_slot * kBlk) >> 4);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s)    // keys 16s .. 16s + 15
-                        mma_ss(tmem + S::kColO + N * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
-                               pdesc0 + static_cast<uint64_t>((N == 64 ? s * 2048 : (s >> 2) * (N * 128) + (s & 3) * 32) >> 4), idesc_pv,
-                               (!fresh || s > 0) ? 1u : 0u);
-                    mma_commit(&ctl->kfree[pv_slot]);
+                        for (int s = 0; s < 4; ++s)    // keys 16s .. 16s + 15
+                            mma_ss(tmem + S::kColO + N * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
+                                   pd + static_cast<uint64_t>((s * kPStep) >> 4), idesc_pv, (!first || s > 0) ? 1u : 0u);
+                        mma_commit(&ctl->kfree[pv_slot]);
+                        if (++pv_slot == S::kRing) pv_slot = 0;
+                    }
                 }
                 __syncwarp();
-                if (++pv_slot == S::kRing) pv_slot = 0;
-            }
-        };
-        for (int it = 0; it < count && ok; ++it) {
-            const uint32_t d = tmem + S::kColS + N * (it & 1);
-            if (first) {
-                // (the new queries are staged behind the epilogue of the old ones, which waits for this PV)
-                if (it > 0) pv(it - 1, prev_first);
-                if (ok) ok = wait_warp(ctl, &ctl->qready, seg & 1, a.status);
-                ++seg;
-            }
-#pragma unroll 1
-            for (int b = 0; b < S::kEarly && ok; ++b) qk_block(b, d);
-            if (ok && !first) pv(it - 1, prev_first);
-#pragma unroll 1
-            for (int b = S::kEarly; b < 4 && ok; ++b) qk_block(b, d);
-            if (ok) ok = wait_warp(ctl, &ctl->ropefull, it & 1, a.status);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (leader) {
+                ++pi;
+                moved = true;
+            } else if (qi < count && qi < pi + 2) {    // (score and P buffers of tile qi - 2 are free)
+                if (!open && ready(&ctl->tfull[qi % kAhead], (qi / kAhead) & 1)) {
+                    const bool first = (lds_u32(sbase + kOffTile + 16 * (qi % kAhead) + 8) & 1u) != 0u;
+                    if (!first || ready(&ctl->qready, seg & 1)) {
+                        __syncwarp();
+                        if (leader) mbar_arrive(&ctl->tfree[qi % kAhead]);
+                        fresh = (fresh & ~(1u << (qi & 1))) | ((first ? 1u : 0u) << (qi & 1));
+                        if (first) ++seg;
+                        open = true;
+                    }
+                }
+                if (open && ready(&ctl->kfull[qk_slot], qk_round & 1)) {
+                    // S^T (+)= K Q^T over dims 128 qb .. 128 qb + 127, the RoPE dims behind the last of them
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + S::kColS + N * (qi & 1);
+                    if (leader) {
+                        const uint64_t kd = kdesc0 + static_cast<uint64_t>((qk_slot * kBlk) >> 4);
+                        const uint64_t qd = qdesc0 + static_cast<uint64_t>((2 * qb * S::kQBlk) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)   // dims 512-575: K rows from tensor memory
-                    mma_ts(d, tmem + S::kColR + 8 * kk, qdesc0 + static_cast<uint64_t>((8 * S::kQBlk + kk * 32) >> 4), idesc_rope, 1u);
-                mma_commit(&ctl->sfull);
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ss(d, kd + static_cast<uint64_t>(((kk >> 2) * kSubBlk + (kk & 3) * 32) >> 4),
+                                   qd + static_cast<uint64_t>(((kk >> 2) * S::kQBlk + (kk & 3) * 32) >> 4), idesc_qk,
+                                   (qb > 0 || kk > 0) ? 1u : 0u);
+                        if (qb == 3) {
+                            const uint64_t rd = rdesc0 + static_cast<uint64_t>(((qi % S::kRopeRing) * kSubBlk) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss(d, rd + static_cast<uint64_t>((kk * 32) >> 4),
+                                       qdesc0 + static_cast<uint64_t>((8 * S::kQBlk + kk * 32) >> 4), idesc_rope, 1u);
+                            mma_commit(&ctl->sfull[qi & 1]);
+                        }
+                    }
+                    __syncwarp();
+                    if (++qk_slot == S::kRing) {
+                        qk_slot = 0;
+                        ++qk_round;
+                    }
+                    if (++qb == 4) {
+                        qb = 0;
+                        ++qi;
+                        open = false;
+                    }
+                    moved = true;
+                }
             }
-            __syncwarp();
-            prev_first = first;
-            first = w.last_of_segment();
-            w.next(a);
+            if (moved) {
+                idle = 0;
+            } else if ((++idle & 63u) == 0u) {   // nothing ready for a while: go on polling, for a second at most
+                const uint64_t now = __shfl_sync(0xffffffffu, global_ns(), 0);
+                if (idle == 64u) idle_since = now;
+                if (now - idle_since > kWaitLimitNs || __any_sync(0xffffffffu, aborted(ctl))) {
+                    ok = false;
+                    break;
+                }
+            }
         }
-        if (ok) pv(count - 1, prev_first);
+        if (!ok) set_abort(ctl, a.status);
         if (leader) mma_commit(&ctl->drain);
         __syncwarp();
         if (!mbar_wait(&ctl->drain, 0)) set_abort(ctl, a.status);
