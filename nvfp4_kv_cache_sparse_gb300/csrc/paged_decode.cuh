@@ -24,8 +24,7 @@
 // Pipeline. Shared memory holds a ring of kRing blocks (64 keys x 128 dims, 16 KB), two tiles and more:
 // a block is filled by the converters, read by the QK MMAs, and freed by the PV MMAs of its tile.
 // The conversion of one tile, the softmax of another and the MMAs of both run side by side (two
-// score buffers, two P buffers); the MMA issuer takes whichever of the next PV and the next QK block
-// is ready, PV first, as it frees the ring. Tiles of 64 keys, not 128: what a CTA can have in flight is
+// score buffers, two P buffers; QK and PV are issued by a warp each). Tiles of 64 keys, not 128: what a CTA can have in flight is
 // bounded by shared memory, and a tile of 128 keys (128 KB) left the ring half empty while its
 // softmax ran (16 rows, 352-byte records: 3.5 us per 128 keys with a ring of 1.5 such tiles).
 //
@@ -84,7 +83,7 @@ template <int N>
 struct Shape {
     static constexpr int kSoft = N == 16 ? 4 : 8;        // softmax warps
     static constexpr int kConv = 16;                     // converter warps: two groups, even and odd blocks
-    static constexpr int kThreads = 32 * (kSoft + kConv + 2);
+    static constexpr int kThreads = 32 * (kSoft + kConv + 3);   // and two MMA issuers and the look-up warp
     static constexpr int kCols = 4 * N / kSoft;          // rows (score columns) of a softmax warp
     static constexpr int kRing = N == 16 ? 10 : N == 32 ? 9 : 7;
     static constexpr int kRopeRing = N == 64 ? 2 : 3;    // tiles whose RoPE dims are held (see the converters)
@@ -106,9 +105,9 @@ struct Shape {
 struct __align__(8) Ctl {
     uint64_t qload;           // q boxes landed (TMA, tx-counted)
     uint64_t qready;          // softmax warps: q converted in shared memory
-    uint64_t kfull[10];       // converter warps of a group: a ring block is written
+    uint64_t kfull[4];        // converter warps, by tile mod 4: the tile's blocks and RoPE dims are written
     uint64_t kfree[10];       // PV commit: a ring block has been read
-    uint64_t sfull[2];        // QK commit, by tile parity: S^T ready (every MMA issued before completed too)
+    uint64_t sfull[2];        // QK commit, by tile parity: S^T ready
     uint64_t pfull[2];        // softmax warps, by tile parity: P^T written (and O^T rescaled)
     uint64_t tfull[kAhead];   // look-up warp: slots and description of a tile
     uint64_t tfree[kAhead];   // every other warp has taken them
@@ -321,7 +320,7 @@ template <int R, bool kBlkOrder, int N>
 __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ KernelArgs a) {
     using S = Shape<N>;
     constexpr int kSoftThreads = 32 * S::kSoft;
-    constexpr int kWarpMma = S::kSoft + S::kConv, kWarpLook = kWarpMma + 1;
+    constexpr int kWarpQk = S::kSoft + S::kConv, kWarpPv = kWarpQk + 1, kWarpLook = kWarpQk + 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Ctl* ctl = reinterpret_cast<Ctl*>(smem);
@@ -332,23 +331,21 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     if (threadIdx.x == 0) {
         mbar_init(&ctl->qload, 1);
         mbar_init(&ctl->qready, S::kSoft);
-        for (int s = 0; s < S::kRing; ++s) {
-            mbar_init(&ctl->kfull[s], S::kConv / 2);
-            mbar_init(&ctl->kfree[s], 1);
-        }
+        for (int s = 0; s < 4; ++s) mbar_init(&ctl->kfull[s], S::kConv);
+        for (int s = 0; s < S::kRing; ++s) mbar_init(&ctl->kfree[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->sfull[s], 1);
             mbar_init(&ctl->pfull[s], S::kSoft);
         }
         for (int s = 0; s < kAhead; ++s) {
             mbar_init(&ctl->tfull[s], 1);
-            mbar_init(&ctl->tfree[s], S::kSoft + S::kConv + 1);
+            mbar_init(&ctl->tfree[s], S::kSoft + S::kConv + 2);
         }
-        mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
         fence_barrier_init();
     }
-    if (warp == kWarpMma) {
+    if (warp == kWarpQk) {
         tmem_alloc(&ctl->tmem_base, S::kTmemCols);
         tmem_relinquish();
     }
@@ -565,6 +562,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             float tmax = -INFINITY;
             uint32_t nan0 = 0u, nan1 = 0u;
             // (the scores' MMAs were issued behind the waits for the blocks that the flags were written before)
+            if (ok && it >= 2) {   // the PV that read this P buffer
+                const int g = 4 * it - 5;
+                ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+            }
             if (ok) ok = wait_warp(ctl, &ctl->sfull[it & 1], (it >> 1) & 1, a.status);
             if (ok) {
                 if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             }
         }
         if (threadIdx.x == 0) a.hdr[blockIdx.x] = hdr;
-    } else if (warp < kWarpMma) {
+    } else if (warp < kWarpQk) {
         // ============ converters: two groups of eight warps, group g the 128-dim blocks g and g + 2 ============
         const int group = (warp - S::kSoft) >> 3;
         const int t = (threadIdx.x - 32 * S::kSoft) & 255;
@@ -836,9 +837,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 // The RoPE dims go to the buffer of kRopeRing tiles ago: the PV commit that freed this group's first
                 // block of the tile (or, before the ring's first round, no tile at all) came behind that QK
                 if (i == 0) sts_u128(sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk + swz(j, 2 * q + group), cur >= 0 ? raw.rope_values() : zero);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->kfull[slot]);
                 if (nxt >= 0) {
                     raw.load_codes(next_rec, q, group, i);
                     if (i == 0) raw.load_rope(next_rec, q, group);
@@ -850,6 +848,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 }
             }
             if (!ok) break;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->kfull[k & 3]);
             cur = nxt;
         }
     } else if (warp == kWarpLook) {
@@ -885,107 +886,84 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             first = last;
             w.next(a);
         }
-    } else {
-        // ======================= MMA issuer =======================
+    } else if (warp == kWarpQk) {
+        // ======================= QK issuer: S^T = K Q^T =======================
         const uint32_t idesc_qk = idesc_f16_f32(64, N, false, false);
         const uint32_t idesc_rope = R == 432 ? idesc_bf16_f32(64, N, false, false) : idesc_qk;
-        const uint32_t idesc_pv = idesc_f16_f32(128, N, true, N == 64);
         const uint64_t kdesc0 = sdesc_sw128(sbase + S::kOffK, 16, 1024);          // K-major: keys x dims
         const uint64_t rdesc0 = sdesc_sw128(sbase + S::kOffRope, 16, 1024);       // K-major: keys x RoPE dims
         const uint64_t qdesc0 = sdesc_sw128(sbase + kOffQ, 16, 1024);             // K-major: rows x dims
+        const bool leader = elect_one_in_warp();
+        bool ok = true;
+        int slot = 0, rslot = 0, seg = 0;
+        for (int it = 0; it < count && ok; ++it) {
+            ok = wait_warp(ctl, &ctl->tfull[it % kAhead], (it / kAhead) & 1, a.status);
+            const bool first = (lds_u32(sbase + kOffTile + 16 * (it % kAhead) + 8) & 1u) != 0u;
+            __syncwarp();
+            if (ok && leader) mbar_arrive(&ctl->tfree[it % kAhead]);
+            if (ok && first) ok = wait_warp(ctl, &ctl->qready, seg++ & 1, a.status);
+            // the score buffer: its scores of two tiles ago have been read
+            if (ok && it >= 2) ok = wait_warp(ctl, &ctl->pfull[it & 1], ((it - 2) >> 1) & 1, a.status);
+            if (ok) ok = wait_warp(ctl, &ctl->kfull[it & 3], (it >> 2) & 1, a.status);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + S::kColS + N * (it & 1);
+            // (short loops: straight-line code of 36 MMAs runs at the pace of the instruction fetch, 50 to 60 clk
+            // an MMA against 25)
+            if (leader) {
+#pragma unroll 1
+                for (int b = 0; b < 9; ++b) {   // 64 dims each, the RoPE dims last
+                    const uint64_t kd = b < 8 ? kdesc0 + static_cast<uint64_t>((slot * kBlk + (b & 1) * kSubBlk) >> 4)
+                                              : rdesc0 + static_cast<uint64_t>((rslot * kSubBlk) >> 4);
+                    const uint64_t qd = qdesc0 + static_cast<uint64_t>((b * S::kQBlk) >> 4);
+                    const uint32_t idesc = b < 8 ? idesc_qk : idesc_rope;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(d, kd + static_cast<uint64_t>((kk * 32) >> 4), qd + static_cast<uint64_t>((kk * 32) >> 4), idesc, (b | kk) != 0 ? 1u : 0u);
+                    if ((b & 1) && ++slot == S::kRing) slot = 0;
+                }
+                if (++rslot == S::kRopeRing) rslot = 0;
+            }
+            if (leader) mma_commit(&ctl->sfull[it & 1]);
+            __syncwarp();
+        }
+        if (leader) mma_commit(&ctl->drain);
+        __syncwarp();
+        if (!mbar_wait(&ctl->drain, 0)) set_abort(ctl, a.status);
+        __syncwarp();
+    } else {
+        // ======================= PV issuer: O^T += V^T P^T; the tile's ring blocks are free then =======================
+        const uint32_t idesc_pv = idesc_f16_f32(128, N, true, N == 64);
         const uint64_t vdesc0 = sdesc_sw128(sbase + S::kOffK, kSubBlk, 1024);     // MN-major: dims x keys
         // P^T: MN-major rows x keys (N = 64), K-major rows x keys (N = 16, 32)
         const uint64_t pdesc0 = sdesc_sw128(sbase + S::kOffP, N == 64 ? S::kPBytes : 16, 1024);
         constexpr int kPStep = N == 64 ? 2048 : 32;                               // 16 keys of P
         const bool leader = elect_one_in_warp();
         bool ok = true;
-        int qi = 0, qb = 0, qk_slot = 0, qk_round = 0;   // the next QK block
-        int pi = 0, pv_slot = 0;                         // the next PV
-        int seg = 0;
-        uint32_t fresh = 0u;                             // bit t & 1: tile t is the first of its segment
-        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)); };
-        bool open = false;                               // tile qi's description is read and its queries are staged
-        uint32_t idle = 0;
-        uint64_t idle_since = 0;
-        while (pi < count) {
-            bool moved = false;
-            if (pi < qi && ready(&ctl->pfull[pi & 1], (pi >> 1) & 1)) {
-                // O^T += V^T P^T of tile pi; its ring blocks are free then
-                tc_fence_after_sync();
-                const bool first = ((fresh >> (pi & 1)) & 1u) != 0u;
-                if (leader) {
-                    const uint64_t pd = pdesc0 + static_cast<uint64_t>((S::kPBytes * (pi & 1)) >> 4);
+        int slot = 0;
+        for (int it = 0; it < count && ok; ++it) {
+            ok = wait_warp(ctl, &ctl->tfull[it % kAhead], (it / kAhead) & 1, a.status);
+            const bool first = (lds_u32(sbase + kOffTile + 16 * (it % kAhead) + 8) & 1u) != 0u;
+            __syncwarp();
+            if (ok && leader) mbar_arrive(&ctl->tfree[it % kAhead]);
+            if (ok) ok = wait_warp(ctl, &ctl->pfull[it & 1], (it >> 1) & 1, a.status);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t pd = pdesc0 + static_cast<uint64_t>((S::kPBytes * (it & 1)) >> 4);
+            if (leader) {
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        const uint64_t vd = vdesc0 + static_cast<uint64_t>((pv_slot * kBlk) >> 4);
+                for (int b = 0; b < 4; ++b) {
+                    const uint64_t vd = vdesc0 + static_cast<uint64_t>((slot * kBlk) >> 4);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)    // keys 16s .. 16s + 15
-                            mma_ss(tmem + S::kColO + N * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
-                                   pd + static_cast<uint64_t>((s * kPStep) >> 4), idesc_pv, (!first || s > 0) ? 1u : 0u);
-                        mma_commit(&ctl->kfree[pv_slot]);
-                        if (++pv_slot == S::kRing) pv_slot = 0;
-                    }
-                }
-                __syncwarp();
-                ++pi;
-                moved = true;
-            } else if (qi < count && qi < pi + 2) {    // (score and P buffers of tile qi - 2 are free)
-                if (!open && ready(&ctl->tfull[qi % kAhead], (qi / kAhead) & 1)) {
-                    const bool first = (lds_u32(sbase + kOffTile + 16 * (qi % kAhead) + 8) & 1u) != 0u;
-                    if (!first || ready(&ctl->qready, seg & 1)) {
-                        __syncwarp();
-                        if (leader) mbar_arrive(&ctl->tfree[qi % kAhead]);
-                        fresh = (fresh & ~(1u << (qi & 1))) | ((first ? 1u : 0u) << (qi & 1));
-                        if (first) ++seg;
-                        open = true;
-                    }
-                }
-                if (open && ready(&ctl->kfull[qk_slot], qk_round & 1)) {
-                    // S^T (+)= K Q^T over dims 128 qb .. 128 qb + 127, the RoPE dims behind the last of them
-                    tc_fence_after_sync();
-                    const uint32_t d = tmem + S::kColS + N * (qi & 1);
-                    if (leader) {
-                        const uint64_t kd = kdesc0 + static_cast<uint64_t>((qk_slot * kBlk) >> 4);
-                        const uint64_t qd = qdesc0 + static_cast<uint64_t>((2 * qb * S::kQBlk) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_ss(d, kd + static_cast<uint64_t>(((kk >> 2) * kSubBlk + (kk & 3) * 32) >> 4),
-                                   qd + static_cast<uint64_t>(((kk >> 2) * S::kQBlk + (kk & 3) * 32) >> 4), idesc_qk,
-                                   (qb > 0 || kk > 0) ? 1u : 0u);
-                        if (qb == 3) {
-                            const uint64_t rd = rdesc0 + static_cast<uint64_t>(((qi % S::kRopeRing) * kSubBlk) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_ss(d, rd + static_cast<uint64_t>((kk * 32) >> 4),
-                                       qdesc0 + static_cast<uint64_t>((8 * S::kQBlk + kk * 32) >> 4), idesc_rope, 1u);
-                            mma_commit(&ctl->sfull[qi & 1]);
-                        }
-                    }
-                    __syncwarp();
-                    if (++qk_slot == S::kRing) {
-                        qk_slot = 0;
-                        ++qk_round;
-                    }
-                    if (++qb == 4) {
-                        qb = 0;
-                        ++qi;
-                        open = false;
-                    }
-                    moved = true;
+                    for (int s = 0; s < 4; ++s)    // keys 16s .. 16s + 15
+                        mma_ss(tmem + S::kColO + N * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
+                               pd + static_cast<uint64_t>((s * kPStep) >> 4), idesc_pv, (!first || s > 0) ? 1u : 0u);
+                    mma_commit(&ctl->kfree[slot]);
+                    if (++slot == S::kRing) slot = 0;
                 }
             }
-            if (moved) {
-                idle = 0;
-            } else if ((++idle & 63u) == 0u) {   // nothing ready for a while: go on polling, for a second at most
-                const uint64_t now = __shfl_sync(0xffffffffu, global_ns(), 0);
-                if (idle == 64u) idle_since = now;
-                if (now - idle_since > kWaitLimitNs || __any_sync(0xffffffffu, aborted(ctl))) {
-                    ok = false;
-                    break;
-                }
-            }
+            __syncwarp();
         }
-        if (!ok) set_abort(ctl, a.status);
         if (leader) mma_commit(&ctl->drain);
         __syncwarp();
         if (!mbar_wait(&ctl->drain, 0)) set_abort(ctl, a.status);
@@ -994,7 +972,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kWarpMma) {
+    if (warp == kWarpQk) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, S::kTmemCols);
     }
