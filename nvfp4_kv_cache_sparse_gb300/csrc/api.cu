@@ -330,17 +330,19 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode(const void* q, const uint8_t* cache, in
     nvfp4mla::PagedDecodeArgs d;
     d.q = q;
     d.cache = cache;
-    d.num_pages = static_cast<int>(num_pages);
-    d.page_shift = page_shift_of(page_size);
     d.record_bytes = record_width(record_bytes);
     d.block_scales = block_scales(record_bytes);
-    d.page_table = page_table;
-    d.table_stride = table_stride;
-    d.capacity = max_pages << d.page_shift;
-    d.seq_lens = seq_lens;
-    d.batch = batch;
-    d.s_q = s_q;
-    d.h_q = h_q;
+    d.jobs.page_table = page_table;
+    d.jobs.table_stride = table_stride;
+    d.jobs.seq_lens = seq_lens;
+    d.jobs.num_pages = static_cast<int>(num_pages);
+    d.jobs.page_shift = page_shift_of(page_size);
+    d.jobs.capacity = max_pages << d.jobs.page_shift;
+    d.jobs.batch = batch;
+    d.jobs.s_q = s_q;
+    d.jobs.h_q = h_q;
+    d.jobs.rows_per_seq = static_cast<int>(rows_per_seq);
+    d.jobs.row_tiles = 0;
     d.sm_scale = sm_scale;
     d.attn_sink = attn_sink;
     d.out = out;

@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "paged_jobs.cuh"
+
 namespace nvfp4mla {
 
 // The fused producer stage ahead of the quantizer (nvfp4_mla_norm_rope_quantize_append).
@@ -79,32 +81,26 @@ cudaError_t launch_wait_timeout_probe(uint32_t* status, uint64_t* elapsed_ns, cu
 struct PagedDecodeArgs {
     const void* q;               // bf16 [batch, s_q, h_q, 576]
     const uint8_t* cache;        // [num_pages << page_shift, record_bytes]
-    int num_pages;
-    int page_shift;
     int record_bytes;            // 352 or 432
     bool block_scales;
-    const int32_t* page_table;   // [batch, max_pages], rows table_stride apart
-    int64_t table_stride;
-    int capacity;                // max_pages << page_shift
-    const int32_t* seq_lens;
-    int batch, s_q, h_q;
+    paged::Jobs jobs;            // page table, lengths, shapes (row_tiles set by the launchers)
     float sm_scale;
     const float* attn_sink;      // nullable [h_q]
     void* out;                   // bf16 [batch, s_q, h_q, 512]
     float* lse;
-    int ctas;                    // CTAs of the attention grid
+    int ctas;                    // runs that the tiles are cut into: the SMs (one CTA each, or two runs for a pair)
     uint16_t* part_out;          // workspace, see paged_workspace_bytes
     float* part_lse;
     int32_t* hdr;
     uint32_t* dev_status;
 };
 constexpr int kPagedMaxCtas = 160;               // no sm_103 device has more SMs
-int paged_row_tile(int64_t rows_per_seq);        // query rows that share a CTA's keys: 16, 32 or 64
+int paged_row_tile(int64_t rows_per_seq);        // query rows that share dequantized keys: 16, 32 (one CTA) or 128 (a pair)
 size_t paged_workspace_bytes(int row_tile);
 cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_decode_n16(const PagedDecodeArgs& d, cudaStream_t stream);
 cudaError_t launch_paged_decode_n32(const PagedDecodeArgs& d, cudaStream_t stream);
-cudaError_t launch_paged_decode_n64(const PagedDecodeArgs& d, cudaStream_t stream);
+cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, cudaStream_t stream);
 
 // ---- operations on pages (page_ops.cu)
 constexpr int kMaxCaches = 256;

@@ -88,8 +88,7 @@ paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict
 
 }  // namespace
 
-// The smallest row tile that holds a sequence's rows: a larger one only multiplies by padding.
-int paged_row_tile(int64_t rows_per_seq) { return rows_per_seq <= 16 ? 16 : rows_per_seq <= 32 ? 32 : 64; }
+int paged_row_tile(int64_t rows_per_seq) { return rows_per_seq <= 16 ? 16 : rows_per_seq <= 32 ? 32 : 128; }
 
 // f16 parts [2 CTAs, row tile, 512], their fp32 log-sum-exps, one int4 per CTA
 size_t paged_workspace_bytes(int row_tile) {
@@ -98,14 +97,14 @@ size_t paged_workspace_bytes(int row_tile) {
 }
 
 cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t stream) {
-    const int n = paged_row_tile(static_cast<int64_t>(d.s_q) * d.h_q);
+    const int n = paged_row_tile(d.jobs.rows_per_seq);
     const size_t parts = static_cast<size_t>(2 * kPagedMaxCtas) * n;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (d.ctas > kPagedMaxCtas) d.ctas = kPagedMaxCtas;
     d.part_out = reinterpret_cast<uint16_t*>(ws);
     d.part_lse = reinterpret_cast<float*>(ws + parts * 512 * sizeof(uint16_t));
     d.hdr = reinterpret_cast<int32_t*>(ws + parts * 512 * sizeof(uint16_t) + parts * sizeof(float));
-    cudaError_t err = n == 16 ? launch_paged_decode_n16(d, stream) : n == 32 ? launch_paged_decode_n32(d, stream) : launch_paged_decode_n64(d, stream);
+    cudaError_t err = n == 16 ? launch_paged_decode_n16(d, stream) : n == 32 ? launch_paged_decode_n32(d, stream) : launch_paged_decode_pair(d, stream);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(d.ctas), static_cast<unsigned>(n / kJoinRows));
@@ -117,7 +116,7 @@ cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, paged_join_kernel, static_cast<const uint16_t*>(d.part_out), static_cast<const float*>(d.part_lse),
-                             reinterpret_cast<const int4*>(d.hdr), d.attn_sink, d.h_q, n, static_cast<__nv_bfloat16*>(d.out), d.lse);
+                             reinterpret_cast<const int4*>(d.hdr), d.attn_sink, d.jobs.h_q, n, static_cast<__nv_bfloat16*>(d.out), d.lse);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

@@ -7,13 +7,11 @@
 //     z_j = sm_scale * q[b,i,h,:] . K_j,   out = sum_j e^{z_j} V_j / (sum_j e^{z_j} + e^{sink_h}),
 //     lse = ln sum_j e^{z_j},              V_j = K_j[0:512]
 //
-// Work split. The s_q * h_q query rows of a sequence lie one behind the other in q; N of them (16, 32
-// or 64: the kernel's row tile) share every key that is dequantized, so a job is (sequence, row tile)
-// and costs ceil(keys / 64) tiles of 64 keys. The tiles of all jobs, one job behind the other, are
-// cut into as many equal runs as there are CTAs (one per SM), whatever the lengths are: the lengths
-// are read on the device, so a captured call follows them. A job that lies in one run is finished by
-// its CTA; the parts of a job that was cut go to the workspace (at most two per CTA, f16 outputs
-// divided by their own sums, fp32 log-sum-exps) and a second kernel joins them.
+// Work split. N query rows of a sequence (16 or 32: the kernel's row tile) share every key that is
+// dequantized; the tiles of 64 keys of all such jobs are cut into equal runs, one per CTA (one CTA per
+// SM; paged_jobs.cuh). A job that lies in one run is finished by its CTA; the parts of a job that was cut
+// go to the workspace (at most two per CTA, f16 outputs divided by their own sums, fp32 log-sum-exps)
+// and a second kernel joins them.
 //
 // Contractions. As keys outnumber rows, both products have the keys or the value dims on the MMA's M
 // side: S^T [64 keys x N] = K Q^T and O^T [512 dims x N] += V^T P^T (four M = 128 MMAs per 16
@@ -53,6 +51,7 @@
 
 #include "dequant.cuh"
 #include "launch.h"
+#include "paged_jobs.cuh"
 #include "sm103_ptx.cuh"
 
 namespace nvfp4mla {
@@ -85,11 +84,11 @@ struct Shape {
     static constexpr int kConv = 16;                     // converter warps: two groups, even and odd blocks
     static constexpr int kThreads = 32 * (kSoft + kConv + 3);   // and two MMA issuers and the look-up warp
     static constexpr int kCols = 4 * N / kSoft;          // rows (score columns) of a softmax warp
-    static constexpr int kRing = N == 16 ? 10 : N == 32 ? 9 : 7;
-    static constexpr int kRopeRing = N == 64 ? 2 : 3;    // tiles whose RoPE dims are held (see the converters)
+    static constexpr int kRing = N == 16 ? 10 : 9;
+    static constexpr int kRopeRing = 3;                      // tiles whose RoPE dims are held (see the converters)
     // tensor memory columns: O^T four blocks, two score buffers
     static constexpr uint32_t kColO = 0, kColS = 4 * N;
-    static constexpr int kTmemCols = N == 16 ? 128 : N == 32 ? 256 : 512;
+    static constexpr int kTmemCols = N == 16 ? 128 : 256;
     static_assert(6 * N <= kTmemCols, "tensor memory");
     static constexpr int kQBlk = N * 128;                // N rows x 64 dims
     static constexpr int kOffK = kOffQ + 9 * kQBlk;
@@ -112,25 +111,15 @@ struct __align__(8) Ctl {
     uint64_t tfull[kAhead];   // look-up warp: slots and description of a tile
     uint64_t tfree[kAhead];   // every other warp has taken them
     uint64_t drain;           // every MMA issued completed
-    int64_t total;            // tiles of all jobs
     uint32_t tmem_base;
     uint32_t abort;
-    int32_t job0, tile0;      // where this CTA's run begins
 };
 static_assert(sizeof(Ctl) <= kOffCM, "control block");
 
 struct KernelArgs {
     CUtensorMap qmap;         // q as bf16 [batch * s_q * h_q, 576], box 64 dims x N rows, 128B swizzle
     const uint8_t* cache;
-    const int32_t* page_table;
-    int64_t table_stride;
-    const int32_t* seq_lens;
-    int num_pages;            // pages of the pool
-    int page_shift;
-    int capacity;             // tokens that a page table row can name
-    int batch, s_q, h_q;
-    int rows_per_seq;         // s_q * h_q
-    int row_tiles;            // ceil(rows_per_seq / N)
+    Jobs jobs;
     float sm_scale;
     const float* sink;
     __nv_bfloat16* out;       // [batch * rows_per_seq, 512]
@@ -142,59 +131,29 @@ struct KernelArgs {
     uint32_t* status;
 };
 
-struct Job {
-    int seq, row0, rows;      // rows row0 .. row0 + rows - 1 of sequence seq
-    int keys;                 // keys that some of them sees
-    int tiles;
-    int first_pos, first_tok; // position and token of row row0
-};
-
-template <int N>
-__device__ __forceinline__ Job job_info(const KernelArgs& a, int job) {
-    Job j;
-    j.seq = job / a.row_tiles;
-    j.row0 = (job - j.seq * a.row_tiles) * N;
-    j.rows = min(N, a.rows_per_seq - j.row0);
-    const int len = min(max(__ldg(a.seq_lens + j.seq), 0), a.capacity);
-    const int last_tok = (j.row0 + j.rows - 1) / a.h_q;
-    j.first_tok = j.row0 / a.h_q;
-    j.keys = max(0, len - a.s_q + last_tok + 1);
-    j.tiles = (j.keys + kTile - 1) / kTile;
-    j.first_pos = len - a.s_q + j.first_tok;
-    return j;
-}
-
 // A position in the run of tiles of a CTA.
 template <int N>
 struct Walk {
     Job j;
     int job, t, left;         // tile t of the job; tiles left in the run, this one included
-    __device__ __forceinline__ void start(const KernelArgs& a, int job0, int tile0, int count) {
+    __device__ __forceinline__ void start(const Jobs& a, int job0, int tile0, int count) {
         job = job0;
         t = tile0;
         left = count;
-        j = job_info<N>(a, job);
+        j = job_info<N, kTile>(a, job);
     }
-    __device__ __forceinline__ void next(const KernelArgs& a) {
+    __device__ __forceinline__ void next(const Jobs& a) {
         if (left <= 1) {
             left = 0;
             return;
         }
         --left;
         if (++t < j.tiles) return;
-        do j = job_info<N>(a, ++job);
+        do j = job_info<N, kTile>(a, ++job);
         while (j.tiles == 0);
         t = 0;
     }
     __device__ __forceinline__ bool last_of_segment() const { return left == 1 || t == j.tiles - 1; }
-    // slot of key `key` (0..63) of the tile; -1: no such key, -2: its page is outside the pool
-    __device__ __forceinline__ int slot(const KernelArgs& a, int key) const {
-        const int pos = kTile * t + key;
-        if (pos >= j.keys) return -1;
-        const int page = __ldg(a.page_table + j.seq * a.table_stride + (pos >> a.page_shift));
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) return -2;
-        return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-    }
 };
 
 __device__ __forceinline__ void set_abort(Ctl* ctl, uint32_t* status) {
@@ -358,61 +317,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    // ---- the run of this CTA: a prefix sum over the jobs' tiles, a contiguous piece of the jobs per thread
-    const int jobs = a.batch * a.row_tiles;
-    int count = 0;
-    {
-        const int per = (jobs + S::kThreads - 1) / S::kThreads;
-        const int ja = min(jobs, static_cast<int>(threadIdx.x) * per), jb = min(jobs, ja + per);
-        int64_t mine = 0;
-        for (int j = ja; j < jb; ++j) mine += job_info<N>(a, j).tiles;
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        int64_t* scan = reinterpret_cast<int64_t*>(smem + kOffScan);
-        if (lane == 31) scan[warp] = incl;
-        __syncthreads();
-        int64_t total = 0, before = incl - mine;
-        for (int w = 0; w < S::kThreads / 32; ++w) {
-            const int64_t v = scan[w];
-            if (w < warp) before += v;
-            total += v;
-        }
-        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-        const int64_t c = blockIdx.x;
-        if (c < ctas) {
-            const int64_t g0 = total * c / ctas;
-            count = static_cast<int>(total * (c + 1) / ctas - g0);
-            if (before <= g0 && g0 < before + mine) {
-                int64_t at = before;
-                int j = ja;
-                for (;; ++j) {
-                    const int nt = job_info<N>(a, j).tiles;
-                    if (g0 < at + nt) break;
-                    at += nt;
-                }
-                ctl->job0 = j;
-                ctl->tile0 = static_cast<int>(g0 - at);
-            }
-        }
-        if (threadIdx.x == 0) ctl->total = total;
-        __syncthreads();
-    }
-    // ---- jobs without a visible key: out = 0, lse = -inf
-    for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Job j = job_info<N>(a, job);
-        if (j.tiles > 0) continue;
-        const int64_t row = static_cast<int64_t>(j.seq) * a.rows_per_seq + j.row0;
-        uint4* o = reinterpret_cast<uint4*>(a.out + row * 512);
-        for (int e = threadIdx.x; e < j.rows * 64; e += S::kThreads) o[e] = make_uint4(0u, 0u, 0u, 0u);
-        for (int e = threadIdx.x; e < j.rows; e += S::kThreads) a.lse[row + e] = -INFINITY;
-    }
+    const Run run = find_run<N, kTile, S::kThreads>(a.jobs, reinterpret_cast<int64_t*>(smem + kOffScan), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
+    const int count = run.count;
+    write_empty_jobs<N, kTile, S::kThreads>(a.jobs, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), a.out, a.lse);
     if (blockIdx.x == 0 && a.status != nullptr)
-        for (int b = threadIdx.x; b < a.batch; b += S::kThreads)
-            if (__ldg(a.seq_lens + b) > a.capacity) atomicOr(a.status, 0x2u);
+        for (int b = threadIdx.x; b < a.jobs.batch; b += S::kThreads)
+            if (__ldg(a.jobs.seq_lens + b) > a.jobs.capacity) atomicOr(a.status, 0x2u);
     if (threadIdx.x == 0 && count == 0) a.hdr[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     if (count == 0) {
@@ -439,7 +349,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             if (threadIdx.x == 0) {
                 mbar_arrive_expect_tx(&ctl->qload, 9u * S::kQBlk);
                 for (int bx = 0; bx < 9; ++bx)
-                    tma_load_2d(sbase + kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.rows_per_seq + j.row0, &ctl->qload);
+                    tma_load_2d(sbase + kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.jobs.rows_per_seq + j.row0, &ctl->qload);
             }
         };
         // per-row prescale and f16 (bf16 RoPE for 432-byte records) in place; the rows' scales and positions
@@ -470,7 +380,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 // S' = 2^pre S and z = ch S'; a row that does not exist scores 0 throughout
                 sts_f32(ch_addr(r), r < j.rows ? a.sm_scale * kLog2e * __int_as_float((127 - pre) << 23) : 0.0f);
                 sts_f32(negm_addr(r), INFINITY);   // reference maximum -inf
-                const int tok = (j.row0 + min(r, j.rows - 1)) / a.h_q;
+                const int tok = (j.row0 + min(r, j.rows - 1)) / a.jobs.h_q;
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(pos_s + 4 * r), "r"(j.first_pos + tok - j.first_tok) : "memory");
             }
             if (ok) {
@@ -496,11 +406,11 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         };
 
         int seg = 0;
-        const Job first_job = job_info<N>(a, ctl->job0);
+        const Job first_job = job_info<N, kTile>(a.jobs, run.job);
         load_q(first_job);
         stage_q(first_job, seg);
         bool seg_first = true;
-        int seg_tile = ctl->tile0;             // the segment's first tile
+        int seg_tile = run.tile;               // the segment's first tile
         float l[kGroups][2];                   // this thread's share of its rows' sums of 2^(z - m)
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) l[g][0] = l[g][1] = 0.0f;
@@ -683,7 +593,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             seg_first = false;
 
             if (last_of_segment) {
-                const Job j = job_info<N>(a, static_cast<int>(tile.w));
+                const Job j = job_info<N, kTile>(a.jobs, static_cast<int>(tile.w));
                 const int t_end = pos0 / kTile;
                 const bool more = it + 1 < count;
                 Job next_job = j;
@@ -692,7 +602,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     if (ok) ok = wait_warp(ctl, &ctl->tfull[(it + 1) % kAhead], ((it + 1) / kAhead) & 1, a.status);
                     if (ok) {
                         const uint4 nt = lds_u128(sbase + kOffTile + 16 * ((it + 1) % kAhead));
-                        next_job = job_info<N>(a, static_cast<int>(nt.w));
+                        next_job = job_info<N, kTile>(a.jobs, static_cast<int>(nt.w));
                         next_tile = static_cast<int>(nt.x) / kTile;
                         load_q(next_job);   // every QK of this segment has completed
                     }
@@ -707,7 +617,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 }
                 const bool whole = seg_tile == 0 && t_end == j.tiles - 1;
                 const int slot = 2 * blockIdx.x + (seg_tile == 0 ? 1 : 0);
-                const int64_t row = static_cast<int64_t>(j.seq) * a.rows_per_seq + j.row0;
+                const int64_t row = static_cast<int64_t>(j.seq) * a.jobs.rows_per_seq + j.row0;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g)
 #pragma unroll
@@ -729,7 +639,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     float factor = 0.0f;
                     if (!empty) {
                         float denom = sum;
-                        if (whole && a.sink != nullptr && r < j.rows) denom += exp2f(__ldg(a.sink + (j.row0 + r) % a.h_q) * kLog2e - mref);
+                        if (whole && a.sink != nullptr && r < j.rows) denom += exp2f(__ldg(a.sink + (j.row0 + r) % a.jobs.h_q) * kLog2e - mref);
                         factor = 1.0f / denom;
                     }
                     sts_f32(alpha_s + 4 * r, factor);
@@ -765,11 +675,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 }
                 tc_fence_before_sync();
                 if (!whole && seg_tile == 0) {
-                    // the first part of a cut job: CTA c holds tile T of the run iff c = ((T + 1) CTAs - 1) / total
-                    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), ctl->total);
-                    const int64_t end = ctl->total * (static_cast<int64_t>(blockIdx.x) + 1) / ctas;   // behind this CTA's run
-                    const int64_t last = end - (t_end + 1) + j.tiles - 1;
-                    hdr = make_int4(static_cast<int>(row), j.rows, static_cast<int>(((last + 1) * ctas - 1) / ctl->total), j.row0 % a.h_q);
+                    // the first part of a cut job: its last tile lies (tiles - t_end - 1) behind the end of this run
+                    const int64_t end = run.total * (static_cast<int64_t>(blockIdx.x) + 1) / run.runs;
+                    hdr = make_int4(static_cast<int>(row), j.rows, run_of(run, end - (t_end + 1) + j.tiles - 1), j.row0 % a.jobs.h_q);
                 }
                 named_bar_sync(1, kSoftThreads);   // the factors and references have been read
                 if (more) {
@@ -856,21 +764,21 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     } else if (warp == kWarpLook) {
         // ============ look-up warp: the slots of the keys of every tile, and their records into L2 ============
         Walk<N> w;
-        w.start(a, ctl->job0, ctl->tile0, count);
+        w.start(a.jobs, run.job, run.tile, count);
         bool first = true;
         for (int it = 0; it < count; ++it) {
             const int at = it % kAhead;
             if (it >= kAhead && !wait_warp(ctl, &ctl->tfree[at], (it / kAhead - 1) & 1, a.status)) break;
             int slot[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) slot[e] = w.slot(a, 32 * e + lane);
+            for (int e = 0; e < 2; ++e) slot[e] = slot_of(a.jobs, w.j.seq, w.j.keys, kTile * w.t + 32 * e + lane);
             bool outside = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 outside = outside || slot[e] == -2;
                 sts_u32(sbase + kOffSlot + 4 * (kTile * at + 32 * e + lane), static_cast<uint32_t>(slot[e]));
                 // eight keys are one run of a page (of eight records or more)
-                if (a.page_shift >= 3) {
+                if (a.jobs.page_shift >= 3) {
                     if ((lane & 7) == 0 && slot[e] >= 0) prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[e]) * R, 8u * R);
                 } else if (slot[e] >= 0) {
                     prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[e]) * R, R);
@@ -884,7 +792,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->tfull[at]);
             first = last;
-            w.next(a);
+            w.next(a.jobs);
         }
     } else if (warp == kWarpQk) {
         // ======================= QK issuer: S^T = K Q^T =======================
@@ -1020,20 +928,11 @@ cudaError_t prepare_kernel() {
 template <int N>
 cudaError_t launch_rows(const PagedDecodeArgs& d, cudaStream_t stream) {
     KernelArgs a;
-    const int64_t rows = static_cast<int64_t>(d.batch) * d.s_q * d.h_q;
+    const int64_t rows = static_cast<int64_t>(d.jobs.batch) * d.jobs.rows_per_seq;
     if (!encode_q_map<N>(&a.qmap, d.q, rows)) return cudaErrorInvalidValue;
     a.cache = d.cache;
-    a.page_table = d.page_table;
-    a.table_stride = d.table_stride;
-    a.seq_lens = d.seq_lens;
-    a.num_pages = d.num_pages;
-    a.page_shift = d.page_shift;
-    a.capacity = d.capacity;
-    a.batch = d.batch;
-    a.s_q = d.s_q;
-    a.h_q = d.h_q;
-    a.rows_per_seq = d.s_q * d.h_q;
-    a.row_tiles = (a.rows_per_seq + N - 1) / N;
+    a.jobs = d.jobs;
+    a.jobs.row_tiles = (a.jobs.rows_per_seq + N - 1) / N;
     a.sm_scale = d.sm_scale;
     a.sink = d.attn_sink;
     a.out = static_cast<__nv_bfloat16*>(d.out);

@@ -1,0 +1,207 @@
+// paged_jobs.cuh -- how attention through a page table is cut into work: jobs (a sequence and a tile of its
+// query rows), their tiles of keys, and the runs of tiles that CTAs or CTA pairs take.
+//
+// The s_q * h_q query rows of a sequence lie one behind the other in q; rows row0 .. row0 + rows - 1 of a
+// job share every key that is dequantized. The tiles of all jobs, one job behind the other, are cut into
+// equal runs, whatever the lengths are: they are read on the device, so a captured call follows them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace nvfp4mla {
+namespace paged {
+
+struct Jobs {
+    const int32_t* page_table;
+    int64_t table_stride;
+    const int32_t* seq_lens;
+    int num_pages;            // pages of the pool
+    int page_shift;
+    int capacity;             // tokens that a page table row can name
+    int batch, s_q, h_q;
+    int rows_per_seq;         // s_q * h_q
+    int row_tiles;            // ceil(rows_per_seq / rows of a job)
+};
+
+struct Job {
+    int seq, row0, rows;      // rows row0 .. row0 + rows - 1 of sequence seq
+    int keys;                 // keys that some of them sees
+    int tiles;
+    int first_pos, first_tok; // position and token of row row0
+};
+
+// Job `job` of row tiles of kRows rows and key tiles of kKeys keys. (Not inlined: its divisions are long,
+// and it runs once per job, beside loops that should stay in the instruction cache.)
+template <int kRows, int kKeys>
+__device__ __noinline__ Job job_info(const Jobs& a, int job) {
+    Job j;
+    j.seq = job / a.row_tiles;
+    j.row0 = (job - j.seq * a.row_tiles) * kRows;
+    j.rows = min(kRows, a.rows_per_seq - j.row0);
+    const int len = min(max(__ldg(a.seq_lens + j.seq), 0), a.capacity);
+    const int last_tok = (j.row0 + j.rows - 1) / a.h_q;
+    j.first_tok = j.row0 / a.h_q;
+    j.keys = max(0, len - a.s_q + last_tok + 1);
+    j.tiles = (j.keys + kKeys - 1) / kKeys;
+    j.first_pos = len - a.s_q + j.first_tok;
+    return j;
+}
+
+// Slot of the token at position pos of a sequence; -1: none of the `keys` first, -2: its page is outside the pool.
+__device__ __forceinline__ int slot_of(const Jobs& a, int seq, int keys, int pos) {
+    if (pos >= keys) return -1;
+    const int page = __ldg(a.page_table + seq * a.table_stride + (pos >> a.page_shift));
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) return -2;
+    return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+}
+
+// Where run c of (at most) `runs` begins, its tiles, and the tiles of all jobs. The prefix sum over the jobs'
+// tiles takes a contiguous piece of the jobs per thread; scratch: int64 [33 + 2], shared. Block-collective.
+struct Run {
+    int64_t total, runs;      // tiles of all jobs; runs that are not empty
+    int job, tile, count;
+};
+// The run that holds tile t of all.
+__device__ __forceinline__ int run_of(const Run& r, int64_t t) { return static_cast<int>(((t + 1) * r.runs - 1) / r.total); }
+
+template <int kRows, int kKeys, int kThreads>
+__device__ __noinline__ Run find_run(const Jobs& a, int64_t* scratch, int runs, int c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int jobs = a.batch * a.row_tiles;
+    const int per = (jobs + kThreads - 1) / kThreads;
+    const int ja = min(jobs, static_cast<int>(threadIdx.x) * per), jb = min(jobs, ja + per);
+    int64_t mine = 0;
+    for (int j = ja; j < jb; ++j) mine += job_info<kRows, kKeys>(a, j).tiles;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    Run r;
+    r.total = 0;
+    int64_t before = incl - mine;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int64_t v = scratch[w];
+        if (w < warp) before += v;
+        r.total += v;
+    }
+    r.runs = min(static_cast<int64_t>(runs), r.total);
+    r.count = 0;
+    int* found = reinterpret_cast<int*>(scratch + 33);
+    if (c < r.runs) {
+        const int64_t g0 = r.total * c / r.runs;
+        r.count = static_cast<int>(r.total * (c + 1) / r.runs - g0);
+        if (before <= g0 && g0 < before + mine) {
+            int64_t at = before;
+            int j = ja;
+            for (;; ++j) {
+                const int nt = job_info<kRows, kKeys>(a, j).tiles;
+                if (g0 < at + nt) break;
+                at += nt;
+            }
+            found[0] = j;
+            found[1] = static_cast<int>(g0 - at);
+        }
+    }
+    __syncthreads();
+    r.job = found[0];
+    r.tile = found[1];
+    return r;
+}
+
+// Segment k: the pieces of jobs that lie in one run each, in order (a job's tiles in a run; a job that lies in
+// two runs has two). There are at most (jobs + runs) of them. Scratch: int64 [2 * 33 + 10], shared.
+struct Segment {
+    int32_t job, tile, tiles; // tiles tile .. tile + tiles - 1 of the job; tiles 0: there is no segment k
+    int32_t run;
+    int32_t ends_run;         // the last segment of its run
+    int32_t last_run;         // the run of the job's last tile
+};
+template <int kRows, int kKeys, int kThreads>
+__device__ __noinline__ Segment find_segment(const Jobs& a, int64_t* scratch, int runs, int k) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int jobs = a.batch * a.row_tiles;
+    const int per = (jobs + kThreads - 1) / kThreads;
+    const int ja = min(jobs, static_cast<int>(threadIdx.x) * per), jb = min(jobs, ja + per);
+    auto scan = [&](int64_t mine, int64_t* all, int64_t* total) {   // exclusive
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) all[warp] = incl;
+        __syncthreads();
+        int64_t before = incl - mine;
+        *total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int64_t v = all[w];
+            if (w < warp) before += v;
+            *total += v;
+        }
+        return before;
+    };
+    int64_t tiles = 0, pieces = 0, all_pieces;
+    for (int j = ja; j < jb; ++j) tiles += job_info<kRows, kKeys>(a, j).tiles;
+    Run r;
+    const int64_t first = scan(tiles, scratch, &r.total);
+    r.runs = min(static_cast<int64_t>(runs), r.total);
+    int64_t at = first;
+    for (int j = ja; j < jb; ++j) {
+        const int nt = job_info<kRows, kKeys>(a, j).tiles;
+        if (nt > 0) pieces += run_of(r, at + nt - 1) - run_of(r, at) + 1;
+        at += nt;
+    }
+    int64_t n = scan(pieces, scratch + 33, &all_pieces);
+    Segment* found = reinterpret_cast<Segment*>(scratch + 66);
+    if (threadIdx.x == 0 && k >= all_pieces) *found = Segment{};
+    if (k >= n && k < n + pieces) {
+        at = first;
+        for (int j = ja; j < jb; ++j) {
+            const int nt = job_info<kRows, kKeys>(a, j).tiles;
+            if (nt == 0) continue;
+            const int r0 = run_of(r, at), r1 = run_of(r, at + nt - 1);
+            if (k < n + r1 - r0 + 1) {
+                Segment s;
+                s.job = j;
+                s.run = r0 + static_cast<int>(k - n);
+                const int64_t g0 = r.total * s.run / r.runs, g1 = r.total * (s.run + 1) / r.runs;
+                const int64_t t0 = g0 > at ? g0 - at : 0, t1 = g1 < at + nt ? g1 - at : nt;
+                s.tile = static_cast<int>(t0);
+                s.tiles = static_cast<int>(t1 - t0);
+                s.ends_run = at + t1 == g1 ? 1 : 0;
+                s.last_run = r1;
+                *found = s;
+                break;
+            }
+            n += r1 - r0 + 1;
+            at += nt;
+        }
+    }
+    // (the caller reads it behind a barrier, and the runs that are empty from the number of those that are not)
+    if (threadIdx.x == 0) scratch[66 + 3] = r.runs;
+    __syncthreads();
+    return *found;
+}
+
+// Jobs without a visible key (block b of `blocks` takes every blocks-th job): out = 0, lse = -inf.
+template <int kRows, int kKeys, int kThreads>
+__device__ __noinline__ void write_empty_jobs(const Jobs& a, int b, int blocks, void* out, float* lse) {
+    const int jobs = a.batch * a.row_tiles;
+    for (int job = b; job < jobs; job += blocks) {
+        const Job j = job_info<kRows, kKeys>(a, job);
+        if (j.tiles > 0) continue;
+        const int64_t row = static_cast<int64_t>(j.seq) * a.rows_per_seq + j.row0;
+        uint4* o = static_cast<uint4*>(out) + row * 64;
+        for (int e = threadIdx.x; e < j.rows * 64; e += kThreads) o[e] = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = threadIdx.x; e < j.rows; e += kThreads) lse[row + e] = -INFINITY;
+    }
+}
+
+}  // namespace paged
+}  // namespace nvfp4mla
