@@ -302,7 +302,7 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s
     if (!bytes) return NVFP4_MLA_ERR_INVALID_ARG;
     const int st = check_paged_shape(batch, s_q, h_q);
     if (st != NVFP4_MLA_OK) return st;
-    *bytes = batch == 0 || s_q == 0 ? 0 : nvfp4mla::paged_workspace_bytes(nvfp4mla::paged_row_tile(static_cast<int64_t>(s_q) * h_q));
+    *bytes = batch == 0 || s_q == 0 ? 0 : nvfp4mla::paged_workspace_bytes(batch, static_cast<int64_t>(s_q) * h_q);
     return NVFP4_MLA_OK;
 }
 
@@ -323,7 +323,7 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode(const void* q, const uint8_t* cache, in
         !aligned(lse, 4) || !aligned(attn_sink, 4))
         return NVFP4_MLA_ERR_INVALID_ARG;
     const int64_t rows_per_seq = static_cast<int64_t>(s_q) * h_q;
-    st = check_workspace(workspace, workspace_bytes, nvfp4mla::paged_workspace_bytes(nvfp4mla::paged_row_tile(rows_per_seq)));
+    st = check_workspace(workspace, workspace_bytes, nvfp4mla::paged_workspace_bytes(batch, rows_per_seq));
     if (st != NVFP4_MLA_OK) return st;
     const int sms = device_sm_count(&st);
     if (sms <= 0) return st;
@@ -347,9 +347,8 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode(const void* q, const uint8_t* cache, in
     d.attn_sink = attn_sink;
     d.out = out;
     d.lse = lse;
-    d.ctas = sms;
     d.dev_status = dev_status;
-    const cudaError_t e = nvfp4mla::launch_paged_decode(d, workspace, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = nvfp4mla::launch_paged_decode(d, workspace, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
 }
 

@@ -47,14 +47,16 @@
 // drains what it issued and returns.
 //
 // kPaged. The rows are up to 128 query rows of one sequence (tokens x heads), the keys the tokens of the
-// sequence up to the last row's position, found through its page table (paged_jobs.cuh). The tiles of all
-// jobs are cut into equal runs, and a pair takes one job's share of one run, so that long sequences are
-// spread over pairs; the parts of a job that was cut go to the workspace and a second kernel joins them. Masks differ: a row does not see the keys behind its own position, and a NaN in a record
-// or a query has to reach the rows that see it and no others. So a key that is not there has zero K and
-// V rows, dims of V with a NaN scale are zeros, and the softmax sets the scores of keys that a row does
-// not see to -inf (each softmax warp looks up the pages of its 32 keys itself); tiles that every row sees
-// whole take the same path as the sparse decode's. The idle PV warp of CTA 1 brings the records
-// kPrefetch tiles ahead into L2.
+// sequence up to the last row's position, found through its page table. A pair takes one of the segments
+// that paged_decode_pair.cu cuts the jobs into; the parts of jobs that were cut go to the workspace and a
+// second kernel joins them. (One pair for several segments, in a loop over them, leaves the softmax without
+// the registers that it needs: 276 against 184 us for 32 sequences x 2 tokens x 128 heads.) Masks differ: a
+// row does not see the keys behind its own position, and a NaN in a record or a query has to reach the rows
+// that see it and no others. So a key that is not there has zero K and V rows, dims of V with a NaN scale
+// are zeros, and the softmax sets the scores of keys that a row does not see to -inf; a tile that every row
+// sees whole takes the same path as the sparse decode's. A page outside the pool (an error that is reported)
+// is announced to the softmax two tiles ahead; only then does it look up the pages of its keys itself (looked
+// up for every tile: 1320 against 1241 us for 2 chunks of 256 tokens x 64 heads).
 #pragma once
 
 #include <cuda.h>
@@ -89,7 +91,6 @@ constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kPrefetch = 4;               // tiles ahead that records go into L2 (kPaged)
 
 // Shared memory (offsets from a 1024-byte aligned base)
 constexpr int kBlk = 8192;                 // 64 rows x 128 B (one 64-wide 16-bit block)
@@ -139,19 +140,21 @@ struct __align__(8) Ctl {
     uint64_t drain;           // CTA 0: both issuers' MMAs completed
     uint32_t tmem_base;
     uint32_t abort;
-    uint32_t progress;        // kPaged: tiles scored so far (paces the prefetch)
+    uint32_t outside;         // kPaged: some key's page lies outside the pool
     uint32_t sig_sink;        // target of the 4-byte st.async signals (the value is never read)
 };
 static_assert(sizeof(Ctl) <= 256, "control block");
 
-// What a pair works on (kPaged): a run's share of one job.
-struct Segment {
+// What a pair works on (kPaged): consecutive tiles of a job. 48 bytes, read as three int4.
+struct alignas(16) Segment {
     int32_t seq, row0, rows;  // query rows row0 .. row0 + rows - 1 of sequence seq
     int32_t keys;             // keys that some row sees
-    int32_t key_begin, tiles; // first key and tiles of this segment
+    int32_t key_begin, tiles; // first key and tiles of this segment; tiles 0: none
     int32_t first_pos, first_tok;   // position and token of row row0
-    int32_t whole, part;      // whole: all of the job's tiles; else the part's slot in the workspace
+    int32_t part;             // slot of the partial result in the workspace; -1: the job is not cut
+    int32_t pad[3];
 };
+static_assert(sizeof(Segment) == 48, "three int4");
 constexpr int kOffSeg = 256;
 static_assert(kOffSeg + sizeof(Segment) <= kOffXmax, "control block");
 
@@ -170,9 +173,8 @@ struct KernelArgs {
     uint16_t* part_out;       // f16 partial outputs [rows, splits, 128, 512]
     float* part_lse;          // log2 domain
     uint32_t* status;
-    paged::Jobs jobs;         // kPaged: the sequences; part_out is then [2 runs, 128, 512], and hdr [runs] names the
-    int4* hdr;                // cut job that begins in a run (see paged_decode.cu)
-    int runs;                 // equal parts that all tiles are cut into
+    paged::Jobs jobs;         // kPaged: the sequences; part_out is then [parts, 128, 512]
+    const Segment* segments;  // kPaged: [pairs of the grid]
     int merge;                // 1: the row's splits share a cluster (pair p = ranks 2p, 2p + 1) and pair 0
                               // merges their partials into out and lse after the whole cluster is done
 };
@@ -300,38 +302,6 @@ __device__ __forceinline__ void merge_splits(const KernelArgs& a, int row) {
     }
 }
 
-// The pair's segment (its k-th of all; both CTAs find the same one). Block-collective.
-static __device__ __noinline__ void open_segment(const KernelArgs& a, uint8_t* smem, int k, bool leader) {
-    int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffXmax);
-    const paged::Segment g = paged::find_segment<128, kTile, kThreads>(a.jobs, scratch, a.runs, k);
-    if (threadIdx.x == 0) {
-        Segment s = {};
-        if (g.tiles > 0) {
-            const paged::Job j = paged::job_info<128, kTile>(a.jobs, g.job);
-            s.seq = j.seq;
-            s.row0 = j.row0;
-            s.rows = j.rows;
-            s.keys = j.keys;
-            s.key_begin = g.tile * kTile;
-            s.tiles = g.tiles;
-            s.first_pos = j.first_pos;
-            s.first_tok = j.first_tok;
-            s.whole = g.tiles == j.tiles ? 1 : 0;
-            s.part = 2 * g.run + (g.tile == 0 ? 1 : 0);
-            // the join's list: the cut job that begins in this run and goes on behind it, if there is one
-            if (leader && g.ends_run) {
-                const bool cut = g.tile == 0 && g.last_run > g.run;
-                a.hdr[g.run] = cut ? make_int4(j.seq * a.jobs.rows_per_seq + j.row0, j.rows, g.last_run, j.row0 % a.jobs.h_q) : make_int4(0, 0, 0, 0);
-            }
-        }
-        *reinterpret_cast<Segment*>(smem + kOffSeg) = s;
-    }
-    // runs without a tile
-    if (leader && k == 0)
-        for (int r = static_cast<int>(scratch[69]) + threadIdx.x; r < a.runs; r += kThreads) a.hdr[r] = make_int4(0, 0, 0, 0);
-    __syncthreads();
-}
-
 // Launched in clusters of two CTAs per split pair (one pair, or all splits of a row when they merge
 // in the kernel), or (kPaged) per segment.
 template <int R, bool kBlkOrder, bool kPaged>
@@ -374,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ctl->qload, 1);
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
-        ctl->progress = 0u;
+        ctl->outside = 0u;
         fence_barrier_init();
     }
     if (warp == kWarpQK) {
@@ -390,11 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if constexpr (kPaged) {
-        open_segment(a, smem, pair, crank == 0);
-        paged::write_empty_jobs<128, kTile, kThreads>(a.jobs, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), a.out, a.lse);
-        if (blockIdx.x == 0 && a.status != nullptr)
-            for (int b = threadIdx.x; b < a.jobs.batch; b += kThreads)
-                if (__ldg(a.jobs.seq_lens + b) > a.jobs.capacity) atomicOr(a.status, 0x2u);
+        if (threadIdx.x < 3)
+            reinterpret_cast<int4*>(smem + kOffSeg)[threadIdx.x] = __ldcg(reinterpret_cast<const int4*>(a.segments + pair) + threadIdx.x);
+        __syncthreads();
         key_begin = seg.key_begin;
         key_end = seg.keys;
         n_tiles = seg.tiles;
@@ -436,6 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         xmax[slot * 64 + hl] = qmax;
+        if (kPaged && warp >= kWarpV) {   // the keys of the first two tiles (see the softmax)
+            const int key = key_begin + static_cast<int>(threadIdx.x) - 32 * kWarpV;
+            if (paged::slot_of(a.jobs, seg.seq, key_end, key) == -2) ctl->outside = 1u;
+        }
         named_bar_sync(2, 512);
 #pragma unroll
         for (int k = 0; k < 8; ++k) qmax = fmaxf(qmax, xmax[k * 64 + hl]);
@@ -507,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // kPaged: the last position that this thread's row sees; the first of the warp's 32 keys of tile 0
         const int last_pos = kPaged ? seg.first_pos - seg.first_tok + (seg.row0 + min(64 * crank + hl, seg.rows - 1)) / a.jobs.h_q : 0;
         const int warp_key = key_begin + (upper ? kOwn : 0) + 32 * h2;
-        bool there_n = kPaged && paged::slot_of(a.jobs, seg.seq, key_end, warp_key + lane) >= 0;
         const uint32_t p_row = sbase + kOffP + (upper ? kBlk : 0);
         // Every softmax warp takes part in every named barrier below, also after a wait ran out
         // (then it only passes the barriers), so no warp can be left waiting on a missing one.
@@ -517,10 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mul = ch;
             uint32_t seen = 0xffffffffu;   // kPaged: which of the warp's keys this row sees
             if constexpr (kPaged) {
-                seen = __ballot_sync(0xffffffffu, there_n);
-                const int n = last_pos + 1 - (warp_key + kTile * i);   // keys up to the row's position
-                if (n < 32) seen &= n > 0 ? (1u << n) - 1u : 0u;
-                there_n = i + 1 < n_tiles && paged::slot_of(a.jobs, seg.seq, key_end, warp_key + kTile * (i + 1) + lane) >= 0;
+                const int pos = warp_key + kTile * i;
+                const int n = last_pos + 1 - pos;   // keys up to the row's position
+                if (n < 32) seen = n > 0 ? (1u << n) - 1u : 0u;
+                // (a tile's flag is set ahead of the vfull arrivals of two tiles earlier, and the P of the last tile waited
+                // for that PV)
+                if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&ctl->outside) != 0u))
+                    seen &= __ballot_sync(0xffffffffu, paged::slot_of(a.jobs, seg.seq, key_end, pos + lane) >= 0);
             }
             if (ok) ok = wait_warp(ctl, &ctl->qkdone, i & 1, a.status);
             if (ok) {
@@ -555,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mul = 1.0f;
                 }
             }
-            if (kPaged && threadIdx.x == 0) ctl->progress = static_cast<uint32_t>(i + 1);
             // ---- does any head of this CTA need a new reference? (one barrier reduction)
             if (bar_red_or(1, 256, mx > m_ref + kRescaleThreshold)) {
                 xmax[qi * 64 + hl] = mx;
@@ -651,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (have_o) tc_fence_after_sync();
         }
         const int head = 64 * crank + hl;      // (kPaged: row of the job)
-        const bool single = kPaged ? seg.whole != 0 : a.splits == 1;
+        const bool single = kPaged ? seg.part < 0 : a.splits == 1;
         const bool empty = kPaged ? lt == 0.0f : !(lt > 0.0f);
         const float lse2 = empty ? -INFINITY : m_ref + log2f(lt);
         float factor = 0.0f;
@@ -849,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage_v(1, ib0);
             int32_t ia2 = index_at(2, j), ib2 = index_at(2, kOwn + j);
             for (int k = 0; k < n_tiles; ++k) {
+                if (kPaged && (ia2 == -2 || ib2 == -2)) ctl->outside = 1u;
 #pragma unroll
                 for (int hv = 0; hv < 2; ++hv) {   // V rows 64 hv + j: CTA hv's keys
                     cp_async_wait<1>();
@@ -965,23 +939,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (leader) mma_commit_cg2(&ctl->drain, 0x1u << pb);
             __syncwarp();
-        } else if constexpr (kPaged) {
-            // records into L2, kPrefetch tiles ahead of the softmax: eight keys are one run of a page (of eight records or more)
-            const volatile uint32_t* progress = &ctl->progress;
-            for (int i = 0; i < n_tiles; ++i) {
-                const uint64_t t0 = global_ns();
-                while (__any_sync(0xffffffffu, static_cast<int>(*progress) + kPrefetch < i)) {
-                    __nanosleep(200);
-                    if (__any_sync(0xffffffffu, aborted(ctl) || global_ns() - t0 > kWaitLimitNs)) break;
-                }
-                const int step = a.jobs.page_shift >= 3 ? 8 : 1;
-                for (int key = step * lane; key < kTile; key += 32 * step) {
-                    const int slot = paged::slot_of(a.jobs, seg.seq, key_end, key_begin + kTile * i + key);
-                    if (slot >= 0)
-                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.cache + static_cast<int64_t>(slot) * R), "r"(step * R) : "memory");
-                }
-                __syncwarp();
-            }
         }
     }
 

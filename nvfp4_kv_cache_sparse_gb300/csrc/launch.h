@@ -88,19 +88,23 @@ struct PagedDecodeArgs {
     const float* attn_sink;      // nullable [h_q]
     void* out;                   // bf16 [batch, s_q, h_q, 512]
     float* lse;
-    int ctas;                    // runs that the tiles are cut into: the SMs (one CTA each, or two runs for a pair)
-    uint16_t* part_out;          // workspace, see paged_workspace_bytes
+    int runs;                    // one CTA each: equal runs that all tiles are cut into
+    int pairs;                   // CTA pairs that run at once
+    void* segments;              // workspace, see PagedWorkspace
+    uint16_t* part_out;
     float* part_lse;
     int32_t* hdr;
     uint32_t* dev_status;
 };
-constexpr int kPagedMaxCtas = 160;               // no sm_103 device has more SMs
+constexpr int kPagedMaxSms = 160;                // no sm_103 device has more SMs
 int paged_row_tile(int64_t rows_per_seq);        // query rows that share dequantized keys: 16, 32 (one CTA) or 128 (a pair)
-size_t paged_workspace_bytes(int row_tile);
-cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t stream);
+size_t paged_workspace_bytes(int64_t batch, int64_t rows_per_seq);
+int64_t paged_max_segments(int64_t jobs, int pairs);
+cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, int sms, cudaStream_t stream);
+int paged_pairs(int sms);
 cudaError_t launch_paged_decode_n16(const PagedDecodeArgs& d, cudaStream_t stream);
 cudaError_t launch_paged_decode_n32(const PagedDecodeArgs& d, cudaStream_t stream);
-cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, cudaStream_t stream);
+cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, int max_segments, int headers, cudaStream_t stream);
 
 // ---- operations on pages (page_ops.cu)
 constexpr int kMaxCaches = 256;

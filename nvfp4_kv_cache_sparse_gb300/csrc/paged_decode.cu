@@ -15,24 +15,24 @@ constexpr int kJoinRows = 4;      // rows of a join CTA, four warps each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The cut job that begins in CTA c's run has its parts in slots 2c + 1, 2(c + 1), ..., 2 last. With
-// part lse L_s (log2) and f16 output O_s (divided by its own sum): w_s = 2^(L_s - m),
-// out = sum_s w_s O_s / (sum_s w_s + 2^(sink - m)), lse = (m + log2 sum_s w_s) ln 2. Four warps take
-// the parts of a row in turn and add up their fp32 sums through shared memory, in warp order. A NaN
-// L_s makes the row NaN; a row without any key gets out = 0, lse = -inf.
+// Entry c of hdr names a job that was cut: first output row, rows (0: there is none), parts n, slot f of the
+// first part; the others lie in slots next(c), next(c) + step, ... With part lse L_s (log2) and f16 output
+// O_s (divided by its own sum): w_s = 2^(L_s - m), out = sum_s w_s O_s / (sum_s w_s + 2^(sink - m)),
+// lse = (m + log2 sum_s w_s) ln 2. Four warps take the parts of a row in turn and add up their fp32 sums
+// through shared memory, in warp order. A NaN L_s makes the row NaN; a row without any key gets out = 0,
+// lse = -inf.
 __global__ void __launch_bounds__(128 * kJoinRows)
 paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict__ part_lse, const int4* __restrict__ hdr,
-                  const float* __restrict__ sink, int h_q, int row_tile, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+                  const float* __restrict__ sink, int h_q, int row_tile, int step, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
     __shared__ float acc_s[kJoinRows][4][512];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x;
-    const int4 h = hdr[c];   // first output row, rows, last CTA, first head
+    const int4 h = hdr[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = blockIdx.y * kJoinRows;
     if (r0 >= h.y) return;
     const int r = r0 + (warp >> 2), sub = warp & 3;
-    const int parts = h.z - c + 1;
-    auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * row_tile + r; };
+    const int parts = h.z;
+    auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? h.w : h.w + 1 + (s - 1) * step) * row_tile + r; };
     float m = -INFINITY, tot = 0.0f;
     if (r < h.y) {
         for (int s = lane; s < parts; s += 32) m = fmaxf(m, part_lse[slot(s)]);
@@ -71,7 +71,7 @@ paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict
     }
     __syncthreads();
     if (r >= h.y) return;
-    const float den = tot + (sink != nullptr ? exp2f(sink[(h.w + r) % h_q] * kLog2e - m) : 0.0f);
+    const float den = tot + (sink != nullptr ? exp2f(sink[(h.x + r) % h_q] * kLog2e - m) : 0.0f);
     const float f = tot == 0.0f ? 0.0f : 1.0f / den;
     const int d = 128 * sub + 4 * lane;
     float v[4];
@@ -90,24 +90,54 @@ paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict
 
 int paged_row_tile(int64_t rows_per_seq) { return rows_per_seq <= 16 ? 16 : rows_per_seq <= 32 ? 32 : 128; }
 
-// f16 parts [2 CTAs, row tile, 512], their fp32 log-sum-exps, one int4 per CTA
-size_t paged_workspace_bytes(int row_tile) {
-    const size_t n = static_cast<size_t>(2 * kPagedMaxCtas) * row_tile;
-    return n * 512 * sizeof(uint16_t) + n * sizeof(float) + kPagedMaxCtas * 4 * sizeof(int32_t);
-}
+namespace {
 
-cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t stream) {
+// f16 parts [parts, row tile, 512], their fp32 log-sum-exps, one int4 per job that may be cut, and for CTA pairs the
+// segments. One CTA each: two slots per run. CTA pairs: the segments are at most (jobs + 2 pairs), so there are
+// at most 2 pairs cuts, 2 pairs jobs that are cut and 4 pairs parts.
+struct PagedWorkspace {
+    size_t parts, headers, segments;
+    size_t at_lse, at_hdr, at_segments, bytes;
+    PagedWorkspace(int64_t batch, int64_t rows_per_seq) {
+        const int n = paged_row_tile(rows_per_seq);
+        parts = 2 * kPagedMaxSms;
+        headers = kPagedMaxSms;
+        segments = n < 128 ? 0 : static_cast<size_t>(batch * ((rows_per_seq + 127) / 128) + kPagedMaxSms);
+        at_lse = parts * n * 512 * sizeof(uint16_t);
+        at_hdr = at_lse + parts * n * sizeof(float);
+        at_segments = at_hdr + headers * 4 * sizeof(int32_t);
+        bytes = at_segments + segments * 12 * sizeof(int32_t);
+    }
+};
+
+}  // namespace
+
+size_t paged_workspace_bytes(int64_t batch, int64_t rows_per_seq) { return PagedWorkspace(batch, rows_per_seq).bytes; }
+
+cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, int sms, cudaStream_t stream) {
     const int n = paged_row_tile(d.jobs.rows_per_seq);
-    const size_t parts = static_cast<size_t>(2 * kPagedMaxCtas) * n;
+    const PagedWorkspace w(d.jobs.batch, d.jobs.rows_per_seq);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (d.ctas > kPagedMaxCtas) d.ctas = kPagedMaxCtas;
+    if (sms > kPagedMaxSms) sms = kPagedMaxSms;
+    d.runs = sms;
     d.part_out = reinterpret_cast<uint16_t*>(ws);
-    d.part_lse = reinterpret_cast<float*>(ws + parts * 512 * sizeof(uint16_t));
-    d.hdr = reinterpret_cast<int32_t*>(ws + parts * 512 * sizeof(uint16_t) + parts * sizeof(float));
-    cudaError_t err = n == 16 ? launch_paged_decode_n16(d, stream) : n == 32 ? launch_paged_decode_n32(d, stream) : launch_paged_decode_pair(d, stream);
+    d.part_lse = reinterpret_cast<float*>(ws + w.at_lse);
+    d.hdr = reinterpret_cast<int32_t*>(ws + w.at_hdr);
+    int headers = sms;
+    cudaError_t err;
+    if (n == 128) {
+        d.pairs = paged_pairs(sms);
+        d.segments = ws + w.at_segments;
+        const int64_t jobs = static_cast<int64_t>(d.jobs.batch) * ((d.jobs.rows_per_seq + 127) / 128);
+        const int64_t most = paged_max_segments(jobs, d.pairs);
+        headers = static_cast<int>(jobs < 2 * d.pairs ? jobs : 2 * d.pairs);
+        err = launch_paged_decode_pair(d, static_cast<int>(most), headers, stream);
+    } else {
+        err = n == 16 ? launch_paged_decode_n16(d, stream) : launch_paged_decode_n32(d, stream);
+    }
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(d.ctas), static_cast<unsigned>(n / kJoinRows));
+    cfg.gridDim = dim3(static_cast<unsigned>(headers), static_cast<unsigned>(n / kJoinRows));
     cfg.blockDim = dim3(128 * kJoinRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -116,7 +146,8 @@ cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, paged_join_kernel, static_cast<const uint16_t*>(d.part_out), static_cast<const float*>(d.part_lse),
-                             reinterpret_cast<const int4*>(d.hdr), d.attn_sink, d.jobs.h_q, n, static_cast<__nv_bfloat16*>(d.out), d.lse);
+                             reinterpret_cast<const int4*>(d.hdr), d.attn_sink, d.jobs.h_q, n, n == 128 ? 1 : 2,
+                             static_cast<__nv_bfloat16*>(d.out), d.lse);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

@@ -126,8 +126,8 @@ struct KernelArgs {
     float* lse;
     uint16_t* part_out;       // f16 [2 * CTAs, N, 512]
     float* part_lse;          // [2 * CTAs, N], log2 domain
-    int4* hdr;                // [CTAs]: the cut job that begins in the CTA's run: first output row, rows,
-                              // last CTA with a part of it, first head; rows 0: none
+    int4* hdr;                // [CTAs]: the cut job that begins in the CTA's run: first output row, rows
+                              // (0: none), parts, slot of the first part (the others: 2 (CTA + 1), 2 (CTA + 2), ...)
     uint32_t* status;
 };
 
@@ -320,9 +320,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     const Run run = find_run<N, kTile, S::kThreads>(a.jobs, reinterpret_cast<int64_t*>(smem + kOffScan), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
     const int count = run.count;
     write_empty_jobs<N, kTile, S::kThreads>(a.jobs, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), a.out, a.lse);
-    if (blockIdx.x == 0 && a.status != nullptr)
-        for (int b = threadIdx.x; b < a.jobs.batch; b += S::kThreads)
-            if (__ldg(a.jobs.seq_lens + b) > a.jobs.capacity) atomicOr(a.status, 0x2u);
+    if (blockIdx.x == 0) check_lengths(a.jobs, static_cast<int>(threadIdx.x), S::kThreads, a.status);
     if (threadIdx.x == 0 && count == 0) a.hdr[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     if (count == 0) {
@@ -677,7 +675,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 if (!whole && seg_tile == 0) {
                     // the first part of a cut job: its last tile lies (tiles - t_end - 1) behind the end of this run
                     const int64_t end = run.total * (static_cast<int64_t>(blockIdx.x) + 1) / run.runs;
-                    hdr = make_int4(static_cast<int>(row), j.rows, run_of(run, end - (t_end + 1) + j.tiles - 1), j.row0 % a.jobs.h_q);
+                    hdr = make_int4(static_cast<int>(row), j.rows, run_of(run, end - (t_end + 1) + j.tiles - 1) - static_cast<int>(blockIdx.x) + 1,
+                                    2 * static_cast<int>(blockIdx.x) + 1);
                 }
                 named_bar_sync(1, kSoftThreads);   // the factors and references have been read
                 if (more) {
@@ -949,7 +948,7 @@ cudaError_t launch_rows(const PagedDecodeArgs& d, cudaStream_t stream) {
                                             : prepare_kernel<352, false, N>();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(d.ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>(d.runs));
     cfg.blockDim = dim3(Shape<N>::kThreads);
     cfg.dynamicSmemBytes = Shape<N>::kSmemAlloc;
     cfg.stream = stream;

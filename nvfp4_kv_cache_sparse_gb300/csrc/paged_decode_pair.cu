@@ -2,14 +2,182 @@
 // CTA pair (decode_pair.cuh with kPaged).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "decode_pair.cuh"
 #include "launch.h"
 
 namespace nvfp4mla {
+namespace {
 
-cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, cudaStream_t stream) {
+using pairdec::Segment;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanClasses = 8;
+constexpr int kPlanEmpty = 31;   // CTAs of the plan that write the rows without a key
+
+// Segments for n jobs that have a key: one per pair if that leaves each job four or more, else a whole wave of
+// pairs more than the jobs fill. (For 32 sequences x 2 tokens x 128 heads, lengths 1000 to 8192, on 76 pairs: a
+// model of the waves gives 1.17 of the even share, against 1.68 with one wave, 1.25 and 1.33 with 3 and 4.)
+__host__ __device__ __forceinline__ int64_t waves(int64_t jobs, int64_t pairs) {
+    return 4 * jobs <= pairs ? 1 : (jobs + pairs - 1) / pairs + 1;
+}
+
+// Cuts the jobs into segments for the pairs. With m = waves(jobs), T is the smallest number of tiles such that
+// jobs cut evenly into ceil(tiles / T) segments make at most m * pairs; the segments are then put in the order
+// of eight classes of length, the longest first, so that short ones fill the gaps at the end. (In the jobs'
+// order the model gives 1.3 instead of 1.17.) One CTA: sums over the jobs, each thread a contiguous piece of
+// them. The other CTAs write the rows of jobs without a key.
+__global__ void __launch_bounds__(kPlanThreads, 1)
+paged_plan_kernel(const paged::Jobs a, int pairs, int max_segments, int headers, Segment* __restrict__ segments,
+                  int4* __restrict__ hdr, void* out, float* lse, uint32_t* status) {
+    constexpr int kRows = 128, kKeys = pairdec::kTile;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x > 0) {
+        paged::write_empty_jobs<kRows, kKeys, kPlanThreads>(a, static_cast<int>(blockIdx.x) - 1, kPlanEmpty, out, lse);
+        return;
+    }
+    paged::check_lengths(a, static_cast<int>(threadIdx.x), kPlanThreads, status);
+    __shared__ int64_t sums[2 + kPlanClasses + 1][32];
+    __shared__ int64_t counts[2][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int jobs = a.batch * a.row_tiles;
+    const int per = (jobs + kPlanThreads - 1) / kPlanThreads;
+    const int ja = min(jobs, static_cast<int>(threadIdx.x) * per), jb = min(jobs, ja + per);
+    // the block's exclusive prefix sums (rows of scratch are used once, or in turn by calls with a barrier in between)
+    auto scan = [&](int64_t mine, int64_t* row, int64_t* total) {
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) row[warp] = incl;
+        __syncthreads();
+        const int64_t w = row[lane];
+        int64_t upto = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        *total = __shfl_sync(0xffffffffu, upto, 31);
+        return __shfl_sync(0xffffffffu, upto - w, warp) + incl - mine;
+    };
+    // tiles of the thread's first job stay in a register (most calls have no more jobs than threads)
+    const int first_tiles = ja < jb ? paged::job_info<kRows, kKeys>(a, ja).tiles : 0;
+    auto tiles_of = [&](int j) { return j == ja ? first_tiles : paged::job_info<kRows, kKeys>(a, j).tiles; };
+    int64_t mine = 0, mine_n = 0, total, n;
+    for (int j = ja; j < jb; ++j) {
+        const int nt = tiles_of(j);
+        mine += nt;
+        mine_n += nt > 0 ? 1 : 0;
+    }
+    (void)scan(mine, sums[0], &total);
+    (void)scan(mine_n, sums[1], &n);
+    const int64_t limit = n > 0 ? waves(n, pairs) * pairs : 0;
+    // total / limit <= T; and sum ceil(t / T) < total / T + n, so T = ceil(total / (limit - n)) is enough if that is
+    // positive (limit >= n always; with equality one segment per job, T the longest, is)
+    int64_t lo = 1, hi = 1;
+    if (n > 0) {
+        lo = max(int64_t(1), (total + limit - 1) / limit);
+        hi = limit > n ? (total + limit - n - 1) / (limit - n) : total;
+        hi = max(lo, hi);
+    }
+    for (int turn = 0; lo < hi; turn ^= 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        int64_t c = 0, all;
+        for (int j = ja; j < jb; ++j) c += (tiles_of(j) + mid - 1) / mid;
+        (void)scan(c, counts[turn], &all);
+        if (all <= limit)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    const int T = static_cast<int>(min(lo, static_cast<int64_t>(INT32_MAX)));
+    auto pieces_of = [&](int nt) { return nt / T + (nt % T != 0 ? 1 : 0); };
+    auto class_of = [&](int nt, int np) { return static_cast<int>((static_cast<int64_t>((nt + np - 1) / np - 1) * kPlanClasses) / T); };
+    // slots of the parts and numbers of the jobs that are cut
+    int64_t cuts = 0, all;
+    for (int j = ja; j < jb; ++j) {
+        const int np = pieces_of(tiles_of(j));
+        if (np > 1) cuts += (static_cast<int64_t>(np) << 32) + 1;
+    }
+    cuts = scan(cuts, sums[2], &all);
+    const int cut_jobs = static_cast<int>(all & 0xffffffff);
+    int64_t begin = 0;
+#pragma unroll 1
+    for (int cl = kPlanClasses - 1; cl >= 0; --cl) {
+        int64_t own = 0, in_class;
+        for (int j = ja; j < jb; ++j) {
+            const int nt = tiles_of(j), np = pieces_of(nt);
+            if (nt > 0 && class_of(nt, np) == cl) own += np;
+        }
+        int64_t at = begin + scan(own, sums[3 + cl], &in_class);
+        begin += in_class;
+        int64_t cut = cuts;
+        for (int j = ja; j < jb && own > 0; ++j) {
+            const int nt = tiles_of(j), np = pieces_of(nt);
+            if (nt == 0) continue;
+            if (class_of(nt, np) == cl) {
+                const paged::Job job = paged::job_info<kRows, kKeys>(a, j);
+                if (np > 1 && static_cast<int>(cut & 0xffffffff) < headers)
+                    hdr[cut & 0xffffffff] = make_int4(job.seq * a.rows_per_seq + job.row0, job.rows, np, static_cast<int>(cut >> 32));
+                for (int p = 0; p < np; ++p, ++at) {
+                    if (at >= max_segments) break;
+                    const int t0 = static_cast<int>(static_cast<int64_t>(nt) * p / np), t1 = static_cast<int>(static_cast<int64_t>(nt) * (p + 1) / np);
+                    int4* s = reinterpret_cast<int4*>(segments + at);
+                    s[0] = make_int4(job.seq, job.row0, job.rows, job.keys);
+                    s[1] = make_int4(t0 * kKeys, t1 - t0, job.first_pos, job.first_tok);
+                    s[2] = make_int4(np > 1 ? static_cast<int>(cut >> 32) + p : -1, 0, 0, 0);
+                }
+            }
+            if (np > 1) cut += (static_cast<int64_t>(np) << 32) + 1;
+        }
+    }
+    for (int64_t k = begin + threadIdx.x; k < max_segments; k += kPlanThreads)
+        reinterpret_cast<int4*>(segments + k)[1] = make_int4(0, 0, 0, 0);
+    for (int k = cut_jobs + static_cast<int>(threadIdx.x); k < headers; k += kPlanThreads) hdr[k] = make_int4(0, 0, 0, 0);
+}
+
+}  // namespace
+
+// Segments at most, whatever the lengths are.
+int64_t paged_max_segments(int64_t jobs, int pairs) { return waves(jobs, pairs) * pairs; }
+
+// How many pairs of this kernel run at once on the current device, asked once per device (every record format
+// leaves one CTA per SM).
+int paged_pairs(int sms) {
+    using namespace pairdec;
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return sms / 2;
+    }
+    int pairs = known[dev].load(std::memory_order_relaxed);
+    if (pairs > 0) return pairs;
+    if (prepare_kernel<432, false, true>() == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemAlloc<432>;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&pairs, decode_pair_kernel<432, false, true>, &cfg) != cudaSuccess) pairs = 0;
+    }
+    (void)cudaGetLastError();
+    if (pairs < 1 || pairs > sms / 2) pairs = sms / 2;
+    known[dev].store(pairs, std::memory_order_relaxed);
+    return pairs;
+}
+
+cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, int max_segments, int headers, cudaStream_t stream) {
     using namespace pairdec;
     KernelArgs a = {};
     if (!encode_q_map(&a.qmap, d.q, static_cast<int64_t>(d.jobs.batch) * d.jobs.rows_per_seq)) return cudaErrorInvalidValue;
@@ -24,8 +192,7 @@ cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, cudaStream_t stre
     a.status = d.dev_status;
     a.jobs = d.jobs;
     a.jobs.row_tiles = (a.jobs.rows_per_seq + 127) / 128;
-    a.hdr = reinterpret_cast<int4*>(d.hdr);
-    a.runs = d.ctas;
+    a.segments = static_cast<const Segment*>(d.segments);
     const auto kernel = d.record_bytes == 432 ? decode_pair_kernel<432, false, true>
                         : d.block_scales      ? decode_pair_kernel<352, true, true>
                                               : decode_pair_kernel<352, false, true>;
@@ -34,14 +201,21 @@ cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, cudaStream_t stre
                                             : prepare_kernel<352, false, true>();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    // a pair per segment: at most one for each job and each cut (those behind the last one leave at once)
-    cfg.gridDim = dim3(2u * (static_cast<unsigned>(d.jobs.batch) * static_cast<unsigned>(a.jobs.row_tiles) + static_cast<unsigned>(d.ctas)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = d.record_bytes == 432 ? kSmemAlloc<432> : kSmemAlloc<352>;
-    cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddepcontrol.wait
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(1 + kPlanEmpty);
+    cfg.blockDim = dim3(kPlanThreads);
+    err = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a.jobs, d.pairs, max_segments, headers, static_cast<Segment*>(d.segments),
+                             reinterpret_cast<int4*>(d.hdr), d.out, d.lse, d.dev_status);
+    if (err != cudaSuccess) return err;
+    // a pair per segment (those behind the last one leave at once)
+    cfg.gridDim = dim3(2u * static_cast<unsigned>(max_segments));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = d.record_bytes == 432 ? kSmemAlloc<432> : kSmemAlloc<352>;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;

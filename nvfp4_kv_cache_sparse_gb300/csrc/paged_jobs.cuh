@@ -114,81 +114,6 @@ __device__ __noinline__ Run find_run(const Jobs& a, int64_t* scratch, int runs, 
     return r;
 }
 
-// Segment k: the pieces of jobs that lie in one run each, in order (a job's tiles in a run; a job that lies in
-// two runs has two). There are at most (jobs + runs) of them. Scratch: int64 [2 * 33 + 10], shared.
-struct Segment {
-    int32_t job, tile, tiles; // tiles tile .. tile + tiles - 1 of the job; tiles 0: there is no segment k
-    int32_t run;
-    int32_t ends_run;         // the last segment of its run
-    int32_t last_run;         // the run of the job's last tile
-};
-template <int kRows, int kKeys, int kThreads>
-__device__ __noinline__ Segment find_segment(const Jobs& a, int64_t* scratch, int runs, int k) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int jobs = a.batch * a.row_tiles;
-    const int per = (jobs + kThreads - 1) / kThreads;
-    const int ja = min(jobs, static_cast<int>(threadIdx.x) * per), jb = min(jobs, ja + per);
-    auto scan = [&](int64_t mine, int64_t* all, int64_t* total) {   // exclusive
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) all[warp] = incl;
-        __syncthreads();
-        int64_t before = incl - mine;
-        *total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const int64_t v = all[w];
-            if (w < warp) before += v;
-            *total += v;
-        }
-        return before;
-    };
-    int64_t tiles = 0, pieces = 0, all_pieces;
-    for (int j = ja; j < jb; ++j) tiles += job_info<kRows, kKeys>(a, j).tiles;
-    Run r;
-    const int64_t first = scan(tiles, scratch, &r.total);
-    r.runs = min(static_cast<int64_t>(runs), r.total);
-    int64_t at = first;
-    for (int j = ja; j < jb; ++j) {
-        const int nt = job_info<kRows, kKeys>(a, j).tiles;
-        if (nt > 0) pieces += run_of(r, at + nt - 1) - run_of(r, at) + 1;
-        at += nt;
-    }
-    int64_t n = scan(pieces, scratch + 33, &all_pieces);
-    Segment* found = reinterpret_cast<Segment*>(scratch + 66);
-    if (threadIdx.x == 0 && k >= all_pieces) *found = Segment{};
-    if (k >= n && k < n + pieces) {
-        at = first;
-        for (int j = ja; j < jb; ++j) {
-            const int nt = job_info<kRows, kKeys>(a, j).tiles;
-            if (nt == 0) continue;
-            const int r0 = run_of(r, at), r1 = run_of(r, at + nt - 1);
-            if (k < n + r1 - r0 + 1) {
-                Segment s;
-                s.job = j;
-                s.run = r0 + static_cast<int>(k - n);
-                const int64_t g0 = r.total * s.run / r.runs, g1 = r.total * (s.run + 1) / r.runs;
-                const int64_t t0 = g0 > at ? g0 - at : 0, t1 = g1 < at + nt ? g1 - at : nt;
-                s.tile = static_cast<int>(t0);
-                s.tiles = static_cast<int>(t1 - t0);
-                s.ends_run = at + t1 == g1 ? 1 : 0;
-                s.last_run = r1;
-                *found = s;
-                break;
-            }
-            n += r1 - r0 + 1;
-            at += nt;
-        }
-    }
-    // (the caller reads it behind a barrier, and the runs that are empty from the number of those that are not)
-    if (threadIdx.x == 0) scratch[66 + 3] = r.runs;
-    __syncthreads();
-    return *found;
-}
-
 // Jobs without a visible key (block b of `blocks` takes every blocks-th job): out = 0, lse = -inf.
 template <int kRows, int kKeys, int kThreads>
 __device__ __noinline__ void write_empty_jobs(const Jobs& a, int b, int blocks, void* out, float* lse) {
@@ -201,6 +126,13 @@ __device__ __noinline__ void write_empty_jobs(const Jobs& a, int b, int blocks, 
         for (int e = threadIdx.x; e < j.rows * 64; e += kThreads) o[e] = make_uint4(0u, 0u, 0u, 0u);
         for (int e = threadIdx.x; e < j.rows; e += kThreads) lse[row + e] = -INFINITY;
     }
+}
+
+// Lengths beyond the page table are reported (and read as its capacity).
+__device__ __forceinline__ void check_lengths(const Jobs& a, int thread, int threads, uint32_t* status) {
+    if (status == nullptr) return;
+    for (int b = thread; b < a.batch; b += threads)
+        if (__ldg(a.seq_lens + b) > a.capacity) atomicOr(status, 0x2u);
 }
 
 }  // namespace paged
