@@ -21,7 +21,7 @@ from . import D_QK, D_V, RECORD_BYTES, _check, _need, _ptr, _record_code, load
 
 def _stream_of(dev: int, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream builds an object for it (1 us more)
     _need(stream.device_index == dev, "the stream belongs to another device than the tensors")
     return stream.cuda_stream
 
@@ -42,15 +42,12 @@ def _call(name: str, dev: int, *args) -> None:
             _check(name, getattr(load(), name)(*args))
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, dev: int, stream) -> torch.Tensor:
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev: int, stream) -> Tuple[torch.Tensor, int]:
+    """(workspace, its bytes)"""
     if workspace is None:
-        return _empty(need, torch.uint8, dev, stream)
+        return _empty(need, torch.uint8, dev, stream), need
     _need(workspace.get_device() == dev and workspace.is_contiguous(), "workspace: contiguous, on the tensors' device")
-    return workspace
-
-
-def _bytes(t: torch.Tensor) -> int:
-    return t.numel() * t.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _table(page_table: torch.Tensor, seq_lens: torch.Tensor, name: str = "page_table") -> Tuple[int, int, int]:
@@ -73,25 +70,29 @@ def _refs(page_refs: torch.Tensor) -> int:
 def _pool(caches: Sequence[torch.Tensor], num_pages: Optional[int], page_size: int, dev: Optional[int]):
     """(host array of the caches' pointers, number, pages, record bytes, device)"""
     _need(page_size > 0, "page_size is a power of two")
-    ptrs, width, slots = [], 0, 0
+    shape, ptrs = None, []
     for c in caches:
-        _need(c.dtype == torch.uint8 and c.dim() == 2 and c.is_contiguous() and c.shape[1] in RECORD_BYTES,
-              "caches: uint8 [num_slots, 352|432|656] contiguous")
-        if not ptrs:
-            slots, width = c.shape
+        if shape is None:
+            _need(c.dtype == torch.uint8 and c.dim() == 2 and c.is_contiguous() and c.shape[1] in RECORD_BYTES,
+                  "caches: uint8 [num_slots, 352|432|656] contiguous")
+            shape = c.shape
             if num_pages is None:
-                num_pages = slots // page_size
+                num_pages = shape[0] // page_size
             if dev is None:
                 dev = c.get_device()
-            _need(slots >= num_pages * page_size, "caches hold fewer pages than page_refs counts")
-        _need(c.shape[1] == width and c.shape[0] == slots, "caches: one shape for all")
-        _need(dev >= 0 and c.get_device() == dev, "all tensors on the same CUDA device")
+            _need(shape[0] >= num_pages * page_size, "caches hold fewer pages than page_refs counts")
+        elif c.dtype != torch.uint8 or c.shape != shape or not c.is_contiguous():
+            raise ValueError("caches: contiguous uint8 tensors of one shape")
+        if c.get_device() != dev or dev < 0:
+            raise ValueError("all tensors on the same CUDA device")
         ptrs.append(c.data_ptr())
-    return (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), num_pages, width or 352, dev
+    return (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), num_pages, 352 if shape is None else shape[1], dev
 
 
 def _same_device(dev: int, *tensors: Optional[torch.Tensor]) -> None:
-    _need(dev >= 0 and all(t is None or t.get_device() == dev for t in tensors), "all tensors on the same CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError("all tensors on the same CUDA device")
 
 
 def _status(dev_status: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
@@ -144,14 +145,16 @@ def paged_mla_decode(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     _same_device(dev, cache, page_table, seq_lens, attn_sink, out, lse, _status(dev_status))
     if out is None:
         out = _empty((B, s_q, h_q, D_V), torch.bfloat16, dev, stream)
+    else:
+        _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (B, s_q, h_q, D_V), "out bf16 [B,s_q,h_q,512]")
     if lse is None:
         lse = _empty((B, s_q, h_q), torch.float32, dev, stream)
-    _need(out.dtype == torch.bfloat16 and out.is_contiguous() and tuple(out.shape) == (B, s_q, h_q, D_V), "out bf16 [B,s_q,h_q,512]")
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (B, s_q, h_q), "lse fp32 [B,s_q,h_q]")
-    ws = _workspace(workspace, paged_workspace_size(B, s_q, h_q), dev, stream)
+    else:
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (B, s_q, h_q), "lse fp32 [B,s_q,h_q]")
+    ws, ws_bytes = _workspace(workspace, paged_workspace_size(B, s_q, h_q), dev, stream)
     _call("nvfp4_paged_mla_decode", dev, q.data_ptr(), cache.data_ptr(), cache.shape[0] // page_size, page_size, code,
           page_table.data_ptr(), stride, width, seq_lens.data_ptr(), B, s_q, h_q, float(sm_scale), _ptr(attn_sink),
-          out.data_ptr(), lse.data_ptr(), ws.data_ptr(), _bytes(ws), _ptr(dev_status), _stream_of(dev, stream))
+          out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws_bytes, _ptr(dev_status), _stream_of(dev, stream))
     return out, lse
 
 
@@ -178,9 +181,9 @@ def fork_sequences(page_table: torch.Tensor, seq_lens: torch.Tensor, page_refs: 
     n = _pairs(src, dst)
     dev = page_table.get_device()
     _same_device(dev, seq_lens, page_refs, src, dst, _status(dev_status))
-    ws = _workspace(workspace, pages_workspace_size(b, width, pages, n), dev, stream)
+    ws, ws_bytes = _workspace(workspace, pages_workspace_size(b, width, pages, n), dev, stream)
     _call("nvfp4_mla_fork_sequences", dev, page_table.data_ptr(), stride, width, seq_lens.data_ptr(), b, page_refs.data_ptr(),
-          pages, page_size, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), _bytes(ws), _ptr(dev_status), _stream_of(dev, stream))
+          pages, page_size, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), ws_bytes, _ptr(dev_status), _stream_of(dev, stream))
 
 
 def resize_sequences(caches: Sequence[torch.Tensor], page_table: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor,
@@ -201,10 +204,11 @@ def resize_sequences(caches: Sequence[torch.Tensor], page_table: torch.Tensor, s
     _same_device(dev, seq_lens, page_refs, new_lens, slots, _status(dev_status))
     if slots is None:
         slots = _empty((b, max_new), torch.int64, dev, stream)
-    _need(slots.dtype == torch.int64 and slots.is_contiguous() and tuple(slots.shape) == (b, max_new), "slots int64 [batch, max_new]")
-    ws = _workspace(workspace, pages_workspace_size(b, width, pages), dev, stream)
+    else:
+        _need(slots.dtype == torch.int64 and slots.is_contiguous() and slots.shape == (b, max_new), "slots int64 [batch, max_new]")
+    ws, ws_bytes = _workspace(workspace, pages_workspace_size(b, width, pages), dev, stream)
     _call("nvfp4_mla_resize_sequences", dev, page_table.data_ptr(), stride, width, seq_lens.data_ptr(), new_lens.data_ptr(), b,
-          page_refs.data_ptr(), pages, page_size, arr, num, rec, slots.data_ptr(), max_new, ws.data_ptr(), _bytes(ws),
+          page_refs.data_ptr(), pages, page_size, arr, num, rec, slots.data_ptr(), max_new, ws.data_ptr(), ws_bytes,
           _ptr(dev_status), _stream_of(dev, stream))
     return slots
 
@@ -220,19 +224,25 @@ def compact_pages(caches: Sequence[torch.Tensor], page_table: torch.Tensor, seq_
     pages = _refs(page_refs)
     table_out = page_table if table_out is None else table_out
     refs_out = page_refs if refs_out is None else refs_out
-    ob, ow, ostride = _table(table_out, seq_lens, "table_out")
-    _need((ob, ow) == (b, width) and _refs(refs_out) == pages, "table_out, refs_out: as page_table, page_refs")
+    ostride = stride
+    if table_out is not page_table:
+        ob, ow, ostride = _table(table_out, seq_lens, "table_out")
+        _need(ob == b and ow == width, "table_out, refs_out: as page_table, page_refs")
+    if refs_out is not page_refs:
+        _need(_refs(refs_out) == pages, "table_out, refs_out: as page_table, page_refs")
     dev = page_table.get_device()
     arr, num, _, rec, _ = _pool(caches, pages, page_size, dev)
     _same_device(dev, seq_lens, page_refs, table_out, refs_out, page_map, live, _status(dev_status))
     if page_map is None:
         page_map = _empty((pages,), torch.int32, dev, stream)
+    else:
+        _need(page_map.dtype == torch.int32 and page_map.is_contiguous() and page_map.shape == (pages,), "page_map int32 [num_pages]")
     if live is None:
         live = _empty((1,), torch.int32, dev, stream)
-    _need(page_map.dtype == torch.int32 and page_map.is_contiguous() and tuple(page_map.shape) == (pages,), "page_map int32 [num_pages]")
-    _need(live.dtype == torch.int32 and tuple(live.shape) == (1,), "live int32 [1]")
-    ws = _workspace(workspace, pages_workspace_size(b, width, pages), dev, stream)
+    else:
+        _need(live.dtype == torch.int32 and live.shape == (1,), "live int32 [1]")
+    ws, ws_bytes = _workspace(workspace, pages_workspace_size(b, width, pages), dev, stream)
     _call("nvfp4_mla_compact_pages", dev, arr, num, rec, page_table.data_ptr(), stride, table_out.data_ptr(), ostride, width,
           seq_lens.data_ptr(), b, page_refs.data_ptr(), refs_out.data_ptr(), pages, page_size, page_map.data_ptr(), live.data_ptr(),
-          ws.data_ptr(), _bytes(ws), _ptr(dev_status), _stream_of(dev, stream))
+          ws.data_ptr(), ws_bytes, _ptr(dev_status), _stream_of(dev, stream))
     return table_out, refs_out, page_map, live

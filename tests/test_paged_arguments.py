@@ -70,7 +70,7 @@ def test_page_call_refusals():
 
 def test_workspace_sizes(cdll):
     n16, n32, n64 = lib.paged_workspace_size(3, 1, 16), lib.paged_workspace_size(1, 2, 16), lib.paged_workspace_size(7, 1, 33)
-    assert 0 < n16 < n32 < n64 == lib.paged_workspace_size(1, 500, 128)
+    assert 0 < n16 < n32 < n64 < lib.paged_workspace_size(1, 500, 128)   # (grows with the 128-row tiles)
     assert lib.paged_workspace_size(0, 1, 16) == 0 and lib.paged_workspace_size(1, 0, 16) == 0
     assert lib.pages_workspace_size(2, 4, 100) >= 4 * 108
     assert lib.pages_workspace_size(2, 1000, 100, 50) >= 4 * 50 * 1001
