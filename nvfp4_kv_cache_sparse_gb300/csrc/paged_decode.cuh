@@ -65,25 +65,26 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kSubBlk = 8192;              // 64 keys x 64 dims
 constexpr int kBlk = 16384;                // 64 keys x 128 dims
 constexpr int kAhead = 8;                  // tiles whose keys' slots are looked up ahead
+constexpr int kLook = 2;                   // of them at a time
 // Shared memory (offsets from a 1024-byte aligned base)
 constexpr int kOffCM = 512;                // float [N/2][4]: per row pair {ch_a, ch_b, -m_a, -m_b}: the score scale
                                            // sm_scale log2(e) 2^-pre and the negated reference maximum
 constexpr int kOffAlpha = 1024;            // float [N]: rescale factors, then 1 / l
-constexpr int kOffXmax = 1280;             // float [N][4]: per-row values of the four key quadrants
+constexpr int kOffXmax = 1280;             // float [N][8]: per-row values of the four key quadrants, of two groups
 constexpr int kOffPos = 2304;              // int [N]: each row's position (its last visible key)
 constexpr int kOffNan = 2560;              // uint8 [4][2][64]: keys with a NaN scale, by tile and converter group
 constexpr int kOffScan = 3072;             // int64 [32]
-constexpr int kOffTile = 3328;             // int4 [kAhead]: first key position, row 0's position, flags, job
+constexpr int kOffTile = 3328;             // int4 [kAhead]: first key position, row 0's position, 2 x (tiles left of the
+                                           // segment) + (its first one), job
 constexpr int kOffSlot = 3456;             // int [kAhead][64]: the keys' slots; -1: no key, -2: its page is outside the pool
 constexpr int kOffQ = 6144;
 static_assert(kOffSlot + kAhead * kTile * 4 <= kOffQ, "control area");
 
 template <int N>
 struct Shape {
-    static constexpr int kSoft = N == 16 ? 4 : 8;        // softmax warps
+    static constexpr int kSoft = 8;                      // softmax warps: two groups of four, even and odd tiles
     static constexpr int kConv = 16;                     // converter warps: two groups, even and odd blocks
     static constexpr int kThreads = 32 * (kSoft + kConv + 3);   // and two MMA issuers and the look-up warp
-    static constexpr int kCols = 4 * N / kSoft;          // rows (score columns) of a softmax warp
     static constexpr int kRing = N == 16 ? 10 : 9;
     static constexpr int kRopeRing = 3;                      // tiles whose RoPE dims are held (see the converters)
     // tensor memory columns: O^T four blocks, two score buffers
@@ -103,11 +104,12 @@ struct Shape {
 
 struct __align__(8) Ctl {
     uint64_t qload;           // q boxes landed (TMA, tx-counted)
-    uint64_t qready;          // softmax warps: q converted in shared memory
+    uint64_t qready;          // four softmax warps: q converted in shared memory
     uint64_t kfull[4];        // converter warps, by tile mod 4: the tile's blocks and RoPE dims are written
     uint64_t kfree[10];       // PV commit: a ring block has been read
     uint64_t sfull[2];        // QK commit, by tile parity: S^T ready
     uint64_t pfull[2];        // softmax warps, by tile parity: P^T written (and O^T rescaled)
+    uint64_t voted[2];        // softmax warps, by tile parity: the references are those of the next tile
     uint64_t tfull[kAhead];   // look-up warp: slots and description of a tile
     uint64_t tfree[kAhead];   // every other warp has taken them
     uint64_t drain;           // every MMA issued completed
@@ -153,7 +155,6 @@ struct Walk {
         while (j.tiles == 0);
         t = 0;
     }
-    __device__ __forceinline__ bool last_of_segment() const { return left == 1 || t == j.tiles - 1; }
 };
 
 __device__ __forceinline__ void set_abort(Ctl* ctl, uint32_t* status) {
@@ -278,7 +279,7 @@ __device__ __forceinline__ bool has_nan_e4m3(uint32_t w) { return __vcmpeq4(w & 
 template <int R, bool kBlkOrder, int N>
 __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ KernelArgs a) {
     using S = Shape<N>;
-    constexpr int kSoftThreads = 32 * S::kSoft;
+    constexpr int kSoftThreads = 32 * S::kSoft, kGroupWarps = 4, kGroupThreads = 128;
     constexpr int kWarpQk = S::kSoft + S::kConv, kWarpPv = kWarpQk + 1, kWarpLook = kWarpQk + 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -289,16 +290,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
 
     if (threadIdx.x == 0) {
         mbar_init(&ctl->qload, 1);
-        mbar_init(&ctl->qready, S::kSoft);
+        mbar_init(&ctl->qready, kGroupWarps);
         for (int s = 0; s < 4; ++s) mbar_init(&ctl->kfull[s], S::kConv);
         for (int s = 0; s < S::kRing; ++s) mbar_init(&ctl->kfree[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->sfull[s], 1);
-            mbar_init(&ctl->pfull[s], S::kSoft);
+            mbar_init(&ctl->pfull[s], kGroupWarps);
+            mbar_init(&ctl->voted[s], kGroupWarps);
         }
         for (int s = 0; s < kAhead; ++s) {
             mbar_init(&ctl->tfull[s], 1);
-            mbar_init(&ctl->tfree[s], S::kSoft + S::kConv + 2);
+            mbar_init(&ctl->tfree[s], kGroupWarps + S::kConv + 2);
         }
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
@@ -326,13 +328,16 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     if (count == 0) {
         // nothing to do in this CTA
     } else if (warp < S::kSoft) {
-        // ======================= softmax warps =======================
-        constexpr int kGroups = S::kCols / 8;
+        // ======================= softmax warps: two groups of four, group g the tiles of parity g =======================
+        constexpr int kGroups = N / 8;        // groups of eight rows
+        const int grp = warp >> 2;
         const int qd = warp & 3;              // TMEM lane quadrant: keys 16 qd .. 16 qd + 15 of a tile, and 128 dims' share of O^T
-        const int rb = S::kCols * (warp >> 2);   // rows rb .. rb + kCols - 1
         const int k0 = 16 * qd + (lane >> 2); // this thread's keys: k0 and k0 + 8; its rows: c0 + 8g, c0 + 8g + 1
-        const int c0 = rb + 2 * (lane & 3);
+        const int c0 = 2 * (lane & 3);
+        const uint32_t bar_grp = 1u + static_cast<uint32_t>(grp), bar_all = 3u;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * qd) << 16);
+        const uint32_t s_col = lane_base + S::kColS + N * grp;
+        const uint32_t p_s = sbase + S::kOffP + S::kPBytes * grp;
         const uint32_t cm_s = sbase + kOffCM;
         const uint32_t alpha_s = sbase + kOffAlpha;
         const uint32_t xmax_s = sbase + kOffXmax;
@@ -341,18 +346,16 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         auto negm_addr = [&](int r) { return cm_s + 16 * (r >> 1) + 8 + 4 * (r & 1); };
 
         bool ok = true;
-        // q of a job's rows into shared memory (TMA); rows behind the sequence's last one are those of the
+        // q of a job: rows row0 .. row0 + N - 1 of its sequence (thread 0); rows behind the job's last one are the
         // next sequence or zeros, and reach columns that nothing reads
         auto load_q = [&](const Job& j) {
-            if (threadIdx.x == 0) {
-                mbar_arrive_expect_tx(&ctl->qload, 9u * S::kQBlk);
-                for (int bx = 0; bx < 9; ++bx)
-                    tma_load_2d(sbase + kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.jobs.rows_per_seq + j.row0, &ctl->qload);
-            }
+            mbar_arrive_expect_tx(&ctl->qload, 9u * S::kQBlk);
+            for (int bx = 0; bx < 9; ++bx)
+                tma_load_2d(sbase + kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.jobs.rows_per_seq + j.row0, &ctl->qload);
         };
-        // per-row prescale and f16 (bf16 RoPE for 432-byte records) in place; the rows' scales and positions
+        // group 0: per-row prescale and f16 (bf16 RoPE for 432-byte records) in place; the rows' scales and positions
         auto stage_q = [&](const Job& j, int seg) {
-            constexpr int kTpr = kSoftThreads / N, kChunks = 72 / kTpr;   // threads of a row, chunks of 8 dims of a thread
+            constexpr int kTpr = kGroupThreads / N, kChunks = 72 / kTpr;   // threads of a row, chunks of 8 dims of a thread
             if (ok) ok = wait_warp(ctl, &ctl->qload, seg & 1, a.status);
             const int r = threadIdx.x / kTpr, part = threadIdx.x % kTpr;
             float qmax = 0.0f;
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 sts_f32(ch_addr(r), r < j.rows ? a.sm_scale * kLog2e * __int_as_float((127 - pre) << 23) : 0.0f);
                 sts_f32(negm_addr(r), INFINITY);   // reference maximum -inf
                 const int tok = (j.row0 + min(r, j.rows - 1)) / a.jobs.h_q;
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(pos_s + 4 * r), "r"(j.first_pos + tok - j.first_tok) : "memory");
+                sts_u32(pos_s + 4 * r, static_cast<uint32_t>(j.first_pos + tok - j.first_tok));
             }
             if (ok) {
 #pragma unroll 3
@@ -400,107 +403,122 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->qready);
-            named_bar_sync(1, kSoftThreads);   // the rows' scales, references and positions are written
         };
 
-        int seg = 0;
-        const Job first_job = job_info<N, kTile>(a.jobs, run.job);
-        load_q(first_job);
-        stage_q(first_job, seg);
-        bool seg_first = true;
-        int seg_tile = run.tile;               // the segment's first tile
-        float l[kGroups][2];                   // this thread's share of its rows' sums of 2^(z - m)
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) l[g][0] = l[g][1] = 0.0f;
+        if (threadIdx.x == 0) load_q(job_info<N, kTile>(a.jobs, run.job));
+        float l[kGroups][2], lnm[kGroups][2];  // this thread's share of its rows' sums of 2^(z - m), and the -m that they are for
         int4 hdr = make_int4(0, 0, 0, 0);
+        int seg = 0;
+        // the sums for references that have moved since (also by the other group)
+        auto move_sum = [&](int g, float nm0, float nm1) {
+            if (nm0 != lnm[g][0]) {
+                l[g][0] *= ex2_approx(nm0 - lnm[g][0]);
+                lnm[g][0] = nm0;
+            }
+            if (nm1 != lnm[g][1]) {
+                l[g][1] *= ex2_approx(nm1 - lnm[g][1]);
+                lnm[g][1] = nm1;
+            }
+        };
 
-        // Every softmax warp takes part in every named barrier below, also after a wait ran out in it, until
-        // the next vote, where all leave together: no warp is left waiting on a missing one. Tensor-memory loads
-        // and stores are warp-collective: masks change values only.
-        for (int it = 0; it < count; ++it) {
-            const int at = it % kAhead;
-            if (ok) ok = wait_warp(ctl, &ctl->tfull[at], (it / kAhead) & 1, a.status);
-            const uint32_t slot_s = sbase + kOffSlot + 4 * kTile * at;
-            const bool there0 = ok && static_cast<int>(lds_u32(slot_s + 4 * k0)) >= 0;
-            const bool there1 = ok && static_cast<int>(lds_u32(slot_s + 4 * k0 + 32)) >= 0;
-            const uint4 tile = lds_u128(sbase + kOffTile + 16 * at);
-            const int pos0 = static_cast<int>(tile.x), pos = pos0 + k0;
-            const bool last_of_segment = (tile.z & 2u) != 0u || it + 1 == count;
-            const bool full = pos0 + kTile - 1 <= static_cast<int>(tile.y);   // every row sees every key of the tile
-            const uint32_t s_col = lane_base + S::kColS + N * (it & 1) + rb;
-            float z[kGroups][4];
-            // z - m of this thread's scores (-inf for a row that does not see the key); returns the largest
-            auto load_z = [&]() -> float {
-                uint32_t sv[4 * kGroups];
-                tmem_ld_16x256<kGroups>(s_col, sv);
-                tmem_wait_ld();
-                float tmax = -INFINITY;
+        // Every warp of a group takes part in each of the group's barriers below, also after a wait ran out in it,
+        // until the next vote, where the group leaves its tiles together; both groups then meet at the segment's end,
+        // and leave together. No warp is left waiting on a missing one. Tensor-memory loads and stores are
+        // warp-collective: masks change values only.
+        for (int s0 = 0; s0 < count; ++seg) {
+            if (ok) ok = wait_warp(ctl, &ctl->tfull[s0 % kAhead], (s0 / kAhead) & 1, a.status);
+            const uint4 head = ok ? lds_u128(sbase + kOffTile + 16 * (s0 % kAhead)) : make_uint4(0u, 0u, 2u, static_cast<uint32_t>(run.job));
+            const Job j = job_info<N, kTile>(a.jobs, static_cast<int>(head.w));
+            const int s1 = s0 + static_cast<int>(head.z >> 1);
+            const int seg_tile = static_cast<int>(head.x) / kTile;
+            if (grp == 0) stage_q(j, seg);
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const uint4 c = lds_u128(cm_s + 8 * (c0 + 8 * g));
-                    const uint64_t ch = f32x2_pack(__uint_as_float(c.x), __uint_as_float(c.y));
-                    const uint64_t nm = f32x2_pack(__uint_as_float(c.z), __uint_as_float(c.w));
-                    const float2 a0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g]), __uint_as_float(sv[4 * g + 1])), ch, nm));
-                    const float2 a1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g + 2]), __uint_as_float(sv[4 * g + 3])), ch, nm));
-                    z[g][0] = a0.x;
-                    z[g][1] = a0.y;
-                    z[g][2] = a1.x;
-                    z[g][3] = a1.y;
-                }
-                if (!full) {
+            for (int g = 0; g < kGroups; ++g) {
+                l[g][0] = l[g][1] = 0.0f;
+                lnm[g][0] = lnm[g][1] = INFINITY;
+            }
+            if (bar_red_or(bar_all, kSoftThreads, !ok)) break;   // the rows' scales, references and positions are written
+
+            for (int it = s0 + ((s0 ^ grp) & 1); it < s1; it += 2) {
+                const int at = it % kAhead;
+                if (ok) ok = wait_warp(ctl, &ctl->tfull[at], (it / kAhead) & 1, a.status);
+                const uint32_t slot_s = sbase + kOffSlot + 4 * kTile * at;
+                const bool there0 = ok && static_cast<int>(lds_u32(slot_s + 4 * k0)) >= 0;
+                const bool there1 = ok && static_cast<int>(lds_u32(slot_s + 4 * k0 + 32)) >= 0;
+                const int pos0 = kTile * (seg_tile + it - s0), pos = pos0 + k0;
+                const bool full = pos0 + kTile - 1 <= j.first_pos;   // every row sees every key of the tile
+                uint32_t sv[4 * kGroups];
+                float z[kGroups][4];
+                // z - m of this thread's scores (-inf for a row that does not see the key); returns the largest
+                auto load_z = [&]() -> float {
+                    float tmax = -INFINITY;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        const uint2 qp = lds_u64(pos_s + 4 * (c0 + 8 * g));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (pos + 8 * (e >> 1) > static_cast<int>((e & 1) ? qp.y : qp.x)) z[g][e] = -INFINITY;
+                        const uint4 c = lds_u128(cm_s + 8 * (c0 + 8 * g));
+                        move_sum(g, __uint_as_float(c.z), __uint_as_float(c.w));
+                        const uint64_t ch = f32x2_pack(__uint_as_float(c.x), __uint_as_float(c.y));
+                        const uint64_t nm = f32x2_pack(__uint_as_float(c.z), __uint_as_float(c.w));
+                        const float2 a0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g]), __uint_as_float(sv[4 * g + 1])), ch, nm));
+                        const float2 a1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g + 2]), __uint_as_float(sv[4 * g + 3])), ch, nm));
+                        z[g][0] = a0.x;
+                        z[g][1] = a0.y;
+                        z[g][2] = a1.x;
+                        z[g][3] = a1.y;
                     }
-                }
-                if (!there0 || !there1) {
+                    if (!full) {
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
+                        for (int g = 0; g < kGroups; ++g) {
+                            const uint2 qp = lds_u64(pos_s + 4 * (c0 + 8 * g));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!(e < 2 ? there0 : there1)) z[g][e] = -INFINITY;
-                }
+                            for (int e = 0; e < 4; ++e)
+                                if (pos + 8 * (e >> 1) > static_cast<int>((e & 1) ? qp.y : qp.x)) z[g][e] = -INFINITY;
+                        }
+                    }
+                    if (!there0 || !there1) {
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) tmax = fmax3(fmax3(tmax, z[g][0], z[g][1]), z[g][2], z[g][3]);
-                return tmax;
-            };
-            float tmax = -INFINITY;
-            uint32_t nan0 = 0u, nan1 = 0u;
-            // (the scores' MMAs were issued behind the waits for the blocks that the flags were written before)
-            if (ok && it >= 2) {   // the PV that read this P buffer
-                const int g = 4 * it - 5;
-                ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
-            }
-            if (ok) ok = wait_warp(ctl, &ctl->sfull[it & 1], (it >> 1) & 1, a.status);
-            if (ok) {
-                if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
-                tc_fence_after_sync();
-                const uint32_t nan_s = sbase + kOffNan + 128 * (it & 3) + k0;
-                nan0 = lds_u8(nan_s) | lds_u8(nan_s + 64);
-                nan1 = lds_u8(nan_s + 8) | lds_u8(nan_s + 72);
-                tmax = load_z();
-            }
-            // ---- does any row need a new reference? (one barrier reduction; also entered where a wait ran out,
-            // and then left by every softmax warp at once)
-            if (bar_red_or(1, kSoftThreads, tmax > kRescaleThreshold || !ok)) {
-                // O^T stands still once the PV of the tile before has completed
-                if (ok && !seg_first) {
-                    const int g = 4 * it - 1;
-                    ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!(e < 2 ? there0 : there1)) z[g][e] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) tmax = fmax3(fmax3(tmax, z[g][0], z[g][1]), z[g][2], z[g][3]);
+                    return tmax;
+                };
+                float tmax = -INFINITY;
+                uint32_t nan0 = 0u, nan1 = 0u;
+                if (ok) ok = wait_warp(ctl, &ctl->sfull[grp], (it >> 1) & 1, a.status);
+                if (ok) {
+                    if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
                     tc_fence_after_sync();
-                }
-                if (bar_red_or(1, kSoftThreads, !ok)) {
-                    ok = false;
-                    break;
-                }
-                // per row: the tile's largest z over the 64 keys (a thread's two, the warp's, then the four quadrants)
-                {
-                    uint32_t sv[4 * kGroups];
                     tmem_ld_16x256<kGroups>(s_col, sv);
+                    // (the scores' MMAs were issued behind the waits for the blocks that the flags were written before)
+                    const uint32_t nan_s = sbase + kOffNan + 128 * (it & 3) + k0;
+                    nan0 = lds_u8(nan_s) | lds_u8(nan_s + 64);
+                    nan1 = lds_u8(nan_s + 8) | lds_u8(nan_s + 72);
                     tmem_wait_ld();
+                }
+                if (ok && it >= 2) {   // the PV that read this P buffer
+                    const int g = 4 * it - 5;
+                    ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                }
+                // the other group's tile before this one has its references
+                if (ok && it > s0) ok = wait_warp(ctl, &ctl->voted[grp ^ 1], ((it - 1) >> 1) & 1, a.status);
+                if (ok) tmax = load_z();
+                // ---- does any row need a new reference? (one barrier reduction; also entered where a wait ran out,
+                // and then left by the whole group at once)
+                if (bar_red_or(bar_grp, kGroupThreads, tmax > kRescaleThreshold || !ok)) {
+                    // O^T stands still once the PV of the tile before has completed
+                    if (ok && it > s0) {
+                        const int g = 4 * it - 1;
+                        ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                        tc_fence_after_sync();
+                    }
+                    if (bar_red_or(bar_grp, kGroupThreads, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    // per row: the tile's largest z over the 64 keys (a thread's two, the warp's, then the four quadrants)
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
@@ -513,179 +531,152 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                             if (there1 && pos + 8 <= last) m = fmaxf(m, __uint_as_float(sv[4 * g + 2 + e]) * ch);
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            if (lane < 4) sts_f32(xmax_s + 16 * r + 4 * qd, m);
+                            if (lane < 4) sts_f32(xmax_s + 32 * r + 4 * qd, m);
                         }
-                }
-                named_bar_sync(1, kSoftThreads);
-                if (qd == 0 && lane < S::kCols) {   // one thread per row: the new reference and the rescale factor
-                    const int r = rb + lane;
-                    const uint4 x = lds_u128(xmax_s + 16 * r);
-                    const float zt = fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
-                                           fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
-                    const float mo = -lds_f32(negm_addr(r));
-                    float al = 1.0f;
-                    if (zt > mo + kRescaleThreshold) {
-                        al = mo == -INFINITY ? 0.0f : ex2_approx(mo - zt);
-                        sts_f32(negm_addr(r), -zt);
+                    named_bar_sync(bar_grp, kGroupThreads);
+                    if (qd == 0 && lane < N) {   // one thread per row: the new reference and the rescale factor
+                        const uint4 x = lds_u128(xmax_s + 32 * lane);
+                        const float zt = fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
+                                               fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+                        const float mo = -lds_f32(negm_addr(lane));
+                        float al = 1.0f;
+                        if (zt > mo + kRescaleThreshold) {
+                            al = mo == -INFINITY ? 0.0f : ex2_approx(mo - zt);
+                            sts_f32(negm_addr(lane), -zt);
+                        }
+                        sts_f32(alpha_s + 4 * lane, al);
                     }
-                    sts_f32(alpha_s + 4 * r, al);
-                }
-                named_bar_sync(1, kSoftThreads);
-                if (!seg_first) {
-                    // O^T (this warp's 32 lanes of each block of dims, its rows) *= alpha
+                    named_bar_sync(bar_grp, kGroupThreads);
+                    if (it > s0) {
+                        // O^T (this warp's 32 lanes of each block of dims) *= alpha
 #pragma unroll 1
-                    for (int c = 0; c < 4 * (S::kCols / 16); ++c) {
-                        const int r0 = rb + 16 * (c % (S::kCols / 16));
-                        const uint32_t col = lane_base + S::kColO + N * (c / (S::kCols / 16)) + r0;
-                        uint32_t o[16];
-                        tmem_ld16(col, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < 4 * (N / 16); ++c) {
+                            const int r0 = 16 * (c % (N / 16));
+                            const uint32_t col = lane_base + S::kColO + N * (c / (N / 16)) + r0;
+                            uint32_t o[16];
+                            tmem_ld16(col, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha_s + 4 * (r0 + e)));
-                        tmem_st16(col, o);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha_s + 4 * (r0 + e)));
+                            tmem_st16(col, o);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
+                    (void)load_z();   // against the moved references
+                    __syncwarp();
                 }
+                if (lane == 0) mbar_arrive(&ctl->voted[grp]);   // (the barrier's vote put every lane's reads before)
+                if ((nan0 | nan1) != 0u) {   // a NaN key: NaN for the rows that see it
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((e < 2 ? nan0 : nan1) != 0u && z[g][e] != -INFINITY) z[g][e] = NAN;
+                }
+                // P^T in shared memory: row = query row, 64 keys across (K-major B operand)
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    l[g][0] *= lds_f32(alpha_s + 4 * (c0 + 8 * g));
-                    l[g][1] *= lds_f32(alpha_s + 4 * (c0 + 8 * g) + 4);
-                }
-                (void)load_z();   // against the moved references
-            }
-            if ((nan0 | nan1) != 0u) {   // a NaN key: NaN for the rows that see it
+                    const int c = c0 + 8 * g;
+                    float p[4];
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((e < 2 ? nan0 : nan1) != 0u && z[g][e] != -INFINITY) z[g][e] = NAN;
-            }
-            // P^T in shared memory. N = 64: row = key, 64 rows of the tile across (MN-major B operand); N = 16, 32:
-            // row = query row, 64 keys across (K-major B operand)
-            const uint32_t p_s = sbase + S::kOffP + S::kPBytes * (it & 1);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int c = c0 + 8 * g;
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(z[g][e]);
-                l[g][0] += p[0] + p[2];
-                l[g][1] += p[1] + p[3];
-                const uint32_t w0 = pack_f16x2(p[0], p[1]), w1 = pack_f16x2(p[2], p[3]);
-                if constexpr (N == 64) {
-                    sts_u32(p_s + swz(k0, c >> 3) + 2 * (c & 7), w0);
-                    sts_u32(p_s + swz(k0 + 8, c >> 3) + 2 * (c & 7), w1);
-                } else {
+                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(z[g][e]);
+                    l[g][0] += p[0] + p[2];
+                    l[g][1] += p[1] + p[3];
+                    const uint32_t w0 = pack_f16x2(p[0], p[1]), w1 = pack_f16x2(p[2], p[3]);
                     const uint32_t x = p_s + 2 * (k0 & 7);
                     sts_u16(x + swz(c, k0 >> 3), static_cast<uint16_t>(w0));
                     sts_u16(x + swz(c + 1, k0 >> 3), static_cast<uint16_t>(w0 >> 16));
                     sts_u16(x + swz(c, (k0 >> 3) + 1), static_cast<uint16_t>(w1));
                     sts_u16(x + swz(c + 1, (k0 >> 3) + 1), static_cast<uint16_t>(w1 >> 16));
                 }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->pfull[it & 1]);
-            seg_first = false;
-
-            if (last_of_segment) {
-                const Job j = job_info<N, kTile>(a.jobs, static_cast<int>(tile.w));
-                const int t_end = pos0 / kTile;
-                const bool more = it + 1 < count;
-                Job next_job = j;
-                int next_tile = 0;
-                if (more) {
-                    if (ok) ok = wait_warp(ctl, &ctl->tfull[(it + 1) % kAhead], ((it + 1) / kAhead) & 1, a.status);
-                    if (ok) {
-                        const uint4 nt = lds_u128(sbase + kOffTile + 16 * ((it + 1) % kAhead));
-                        next_job = job_info<N, kTile>(a.jobs, static_cast<int>(nt.w));
-                        next_tile = static_cast<int>(nt.x) / kTile;
-                        load_q(next_job);   // every QK of this segment has completed
-                    }
-                }
-                // ---- row sums, O^T / l, out (or the job's part) and lse
-                bool have_o = false;
-                if (ok) {
-                    const int g = 4 * it + 3;
-                    have_o = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
-                    ok = have_o;
-                    if (have_o) tc_fence_after_sync();
-                }
-                const bool whole = seg_tile == 0 && t_end == j.tiles - 1;
-                const int slot = 2 * blockIdx.x + (seg_tile == 0 ? 1 : 0);
-                const int64_t row = static_cast<int64_t>(j.seq) * a.jobs.rows_per_seq + j.row0;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v = l[g][e];
-                        l[g][e] = 0.0f;
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                        if (lane < 4) sts_f32(xmax_s + 16 * (c0 + 8 * g + e) + 4 * qd, v);
-                    }
-                named_bar_sync(1, kSoftThreads);
-                if (qd == 0 && lane < S::kCols) {
-                    const int r = rb + lane;
-                    const uint4 x = lds_u128(xmax_s + 16 * r);
-                    const float sum = (__uint_as_float(x.x) + __uint_as_float(x.y)) + (__uint_as_float(x.z) + __uint_as_float(x.w));
-                    const float mref = -lds_f32(negm_addr(r));
-                    const bool empty = sum == 0.0f;   // the row sees no key of this segment
-                    const float lse2 = empty ? -INFINITY : mref + log2f(sum);
-                    float factor = 0.0f;
-                    if (!empty) {
-                        float denom = sum;
-                        if (whole && a.sink != nullptr && r < j.rows) denom += exp2f(__ldg(a.sink + (j.row0 + r) % a.jobs.h_q) * kLog2e - mref);
-                        factor = 1.0f / denom;
-                    }
-                    sts_f32(alpha_s + 4 * r, factor);
-                    if (r < j.rows) {
-                        if (whole)
-                            a.lse[row + r] = lse2 * kLn2;
-                        else
-                            a.part_lse[static_cast<int64_t>(slot) * N + r] = lse2;
-                    }
-                }
-                named_bar_sync(1, kSoftThreads);
-                // O^T block b: this thread's lane is dim 128b + 32qd + lane; a warp store covers 32 consecutive
-                // dims of one row (64 bytes)
-                uint16_t* dst = whole ? reinterpret_cast<uint16_t*>(a.out) + row * 512
-                                      : a.part_out + static_cast<int64_t>(slot) * N * 512;
-#pragma unroll 1
-                for (int c = 0; c < 4 * (S::kCols / 16); ++c) {
-                    const int b = c / (S::kCols / 16), r0 = rb + 16 * (c % (S::kCols / 16));
-                    uint32_t o[16];
-                    if (have_o) {
-                        tmem_ld16(lane_base + S::kColO + N * b + r0, o);
-                        tmem_wait_ld();
-                    }
-                    uint16_t* p = dst + static_cast<int64_t>(r0) * 512 + 128 * b + 32 * qd + lane;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if (r0 + e < j.rows) {
-                            const float f = lds_f32(alpha_s + 4 * (r0 + e));
-                            const float v = have_o && f != 0.0f ? __uint_as_float(o[e]) * f : 0.0f;
-                            p[e * 512] = whole ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-                        }
-                    }
-                }
+                fence_proxy_async_smem();
                 tc_fence_before_sync();
-                if (!whole && seg_tile == 0) {
-                    // the first part of a cut job: its last tile lies (tiles - t_end - 1) behind the end of this run
-                    const int64_t end = run.total * (static_cast<int64_t>(blockIdx.x) + 1) / run.runs;
-                    hdr = make_int4(static_cast<int>(row), j.rows, run_of(run, end - (t_end + 1) + j.tiles - 1) - static_cast<int>(blockIdx.x) + 1,
-                                    2 * static_cast<int>(blockIdx.x) + 1);
-                }
-                named_bar_sync(1, kSoftThreads);   // the factors and references have been read
-                if (more) {
-                    ++seg;
-                    stage_q(next_job, seg);
-                    seg_first = true;
-                    seg_tile = next_tile;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->pfull[grp]);
+            }
+
+            // ---- the segment's end: row sums, O^T / l, out (or the job's part) and lse
+            const int t_end = seg_tile + s1 - s0 - 1;
+            if (ok) {
+                const int g = 4 * s1 - 1;
+                ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                tc_fence_after_sync();
+            }
+            if (bar_red_or(bar_all, kSoftThreads, !ok)) break;   // the references are final, every QK of the segment has completed
+            if (warp == 0 && s1 < count) {
+                ok = wait_warp(ctl, &ctl->tfull[s1 % kAhead], (s1 / kAhead) & 1, a.status);
+                if (ok && lane == 0) load_q(job_info<N, kTile>(a.jobs, static_cast<int>(lds_u32(sbase + kOffTile + 16 * (s1 % kAhead) + 12))));
+                __syncwarp();
+            }
+            const bool whole = seg_tile == 0 && t_end == j.tiles - 1;
+            const int slot = 2 * blockIdx.x + (seg_tile == 0 ? 1 : 0);
+            const int64_t row = static_cast<int64_t>(j.seq) * a.jobs.rows_per_seq + j.row0;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const uint4 c = lds_u128(cm_s + 8 * (c0 + 8 * g));
+                move_sum(g, __uint_as_float(c.z), __uint_as_float(c.w));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = l[g][e];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    if (lane < 4) sts_f32(xmax_s + 32 * (c0 + 8 * g + e) + 16 * grp + 4 * qd, v);
                 }
             }
+            named_bar_sync(bar_all, kSoftThreads);
+            if (warp == 0 && lane < N) {
+                const int r = lane;
+                const uint4 x = lds_u128(xmax_s + 32 * r), y = lds_u128(xmax_s + 32 * r + 16);
+                const float sum = ((__uint_as_float(x.x) + __uint_as_float(x.y)) + (__uint_as_float(x.z) + __uint_as_float(x.w))) +
+                                  ((__uint_as_float(y.x) + __uint_as_float(y.y)) + (__uint_as_float(y.z) + __uint_as_float(y.w)));
+                const float mref = -lds_f32(negm_addr(r));
+                const bool empty = sum == 0.0f;   // the row sees no key of this segment
+                const float lse2 = empty ? -INFINITY : mref + log2f(sum);
+                float factor = 0.0f;
+                if (!empty) {
+                    float denom = sum;
+                    if (whole && a.sink != nullptr && r < j.rows) denom += exp2f(__ldg(a.sink + (j.row0 + r) % a.jobs.h_q) * kLog2e - mref);
+                    factor = 1.0f / denom;
+                }
+                sts_f32(alpha_s + 4 * r, factor);
+                if (r < j.rows) {
+                    if (whole)
+                        a.lse[row + r] = lse2 * kLn2;
+                    else
+                        a.part_lse[static_cast<int64_t>(slot) * N + r] = lse2;
+                }
+            }
+            named_bar_sync(bar_all, kSoftThreads);
+            // O^T blocks 2 grp, 2 grp + 1: this thread's lane is dim 128b + 32qd + lane; a warp store covers 32 consecutive
+            // dims of one row (64 bytes)
+            uint16_t* dst = whole ? reinterpret_cast<uint16_t*>(a.out) + row * 512
+                                  : a.part_out + static_cast<int64_t>(slot) * N * 512;
+#pragma unroll 1
+            for (int c = 0; c < 2 * (N / 16); ++c) {
+                const int b = 2 * grp + c / (N / 16), r0 = 16 * (c % (N / 16));
+                uint32_t o[16];
+                tmem_ld16(lane_base + S::kColO + N * b + r0, o);
+                tmem_wait_ld();
+                uint16_t* p = dst + static_cast<int64_t>(r0) * 512 + 128 * b + 32 * qd + lane;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (r0 + e < j.rows) {
+                        const float f = lds_f32(alpha_s + 4 * (r0 + e));
+                        const float v = f != 0.0f ? __uint_as_float(o[e]) * f : 0.0f;
+                        p[e * 512] = whole ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            if (!whole && seg_tile == 0) {
+                // the first part of a cut job: its last tile lies (tiles - t_end - 1) behind the end of this run
+                const int64_t end = run.total * (static_cast<int64_t>(blockIdx.x) + 1) / run.runs;
+                hdr = make_int4(static_cast<int>(row), j.rows, run_of(run, end - (t_end + 1) + j.tiles - 1) - static_cast<int>(blockIdx.x) + 1,
+                                2 * static_cast<int>(blockIdx.x) + 1);
+            }
+            named_bar_sync(bar_all, kSoftThreads);   // the factors and references have been read
+            s0 = s1;
         }
         if (threadIdx.x == 0) a.hdr[blockIdx.x] = hdr;
     } else if (warp < kWarpQk) {
@@ -762,36 +753,49 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         }
     } else if (warp == kWarpLook) {
         // ============ look-up warp: the slots of the keys of every tile, and their records into L2 ============
+        // kLook tiles at a time: their loads from the page table are in flight together (one tile after the other, the
+        // loads' latency alone took 1.3 us a tile)
         Walk<N> w;
         w.start(a.jobs, run.job, run.tile, count);
-        bool first = true;
-        for (int it = 0; it < count; ++it) {
-            const int at = it % kAhead;
-            if (it >= kAhead && !wait_warp(ctl, &ctl->tfree[at], (it / kAhead - 1) & 1, a.status)) break;
-            int slot[2];
+        bool first = true, ok = true;
+        for (int it0 = 0; it0 < count && ok; it0 += kLook) {
+            int slot[kLook][2];
+            uint4 tile[kLook];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) slot[e] = slot_of(a.jobs, w.j.seq, w.j.keys, kTile * w.t + 32 * e + lane);
-            bool outside = false;
+            for (int u = 0; u < kLook; ++u) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                outside = outside || slot[e] == -2;
-                sts_u32(sbase + kOffSlot + 4 * (kTile * at + 32 * e + lane), static_cast<uint32_t>(slot[e]));
-                // eight keys are one run of a page (of eight records or more)
-                if (a.jobs.page_shift >= 3) {
-                    if ((lane & 7) == 0 && slot[e] >= 0) prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[e]) * R, 8u * R);
-                } else if (slot[e] >= 0) {
-                    prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[e]) * R, R);
+                for (int e = 0; e < 2; ++e) slot[u][e] = it0 + u < count ? slot_of(a.jobs, w.j.seq, w.j.keys, kTile * w.t + 32 * e + lane) : -1;
+                const int left = min(w.left, w.j.tiles - w.t);
+                tile[u] = make_uint4(static_cast<uint32_t>(kTile * w.t), static_cast<uint32_t>(w.j.first_pos), (first ? 1u : 0u) | static_cast<uint32_t>(left << 1),
+                                     static_cast<uint32_t>(w.job));
+                first = left == 1;
+                w.next(a.jobs);
+            }
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (slot[u][e] == -2 && a.status != nullptr) atomicOr(a.status, 0x2u);
+                    // eight keys are one run of a page (of eight records or more)
+                    if (a.jobs.page_shift >= 3) {
+                        if ((lane & 7) == 0 && slot[u][e] >= 0) prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[u][e]) * R, 8u * R);
+                    } else if (slot[u][e] >= 0) {
+                        prefetch_l2_bulk(a.cache + static_cast<int64_t>(slot[u][e]) * R, R);
+                    }
                 }
             }
-            if (outside && a.status != nullptr) atomicOr(a.status, 0x2u);
-            const bool last = w.last_of_segment();
-            if (lane == 0)
-                sts_u128(sbase + kOffTile + 16 * at, make_uint4(static_cast<uint32_t>(kTile * w.t), static_cast<uint32_t>(w.j.first_pos),
-                                                                (first ? 1u : 0u) | (last ? 2u : 0u), static_cast<uint32_t>(w.job)));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->tfull[at]);
-            first = last;
-            w.next(a.jobs);
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                const int it = it0 + u, at = it % kAhead;
+                if (it >= count) break;
+                if (ok && it >= kAhead) ok = wait_warp(ctl, &ctl->tfree[at], (it / kAhead - 1) & 1, a.status);
+                if (!ok) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sts_u32(sbase + kOffSlot + 4 * (kTile * at + 32 * e + lane), static_cast<uint32_t>(slot[u][e]));
+                if (lane == 0) sts_u128(sbase + kOffTile + 16 * at, tile[u]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->tfull[at]);
+            }
         }
     } else if (warp == kWarpQk) {
         // ======================= QK issuer: S^T = K Q^T =======================
@@ -840,11 +844,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         __syncwarp();
     } else {
         // ======================= PV issuer: O^T += V^T P^T; the tile's ring blocks are free then =======================
-        const uint32_t idesc_pv = idesc_f16_f32(128, N, true, N == 64);
+        const uint32_t idesc_pv = idesc_f16_f32(128, N, true, false);
         const uint64_t vdesc0 = sdesc_sw128(sbase + S::kOffK, kSubBlk, 1024);     // MN-major: dims x keys
-        // P^T: MN-major rows x keys (N = 64), K-major rows x keys (N = 16, 32)
-        const uint64_t pdesc0 = sdesc_sw128(sbase + S::kOffP, N == 64 ? S::kPBytes : 16, 1024);
-        constexpr int kPStep = N == 64 ? 2048 : 32;                               // 16 keys of P
+        const uint64_t pdesc0 = sdesc_sw128(sbase + S::kOffP, 16, 1024);          // K-major: rows x keys
         const bool leader = elect_one_in_warp();
         bool ok = true;
         int slot = 0;
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
 #pragma unroll
                     for (int s = 0; s < 4; ++s)    // keys 16s .. 16s + 15
                         mma_ss(tmem + S::kColO + N * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
-                               pd + static_cast<uint64_t>((s * kPStep) >> 4), idesc_pv, (!first || s > 0) ? 1u : 0u);
+                               pd + static_cast<uint64_t>((s * 32) >> 4), idesc_pv, (!first || s > 0) ? 1u : 0u);
                     mma_commit(&ctl->kfree[slot]);
                     if (++slot == S::kRing) slot = 0;
                 }
