@@ -207,11 +207,6 @@ __device__ __forceinline__ uint32_t ldg_stream2(const void* p) {
     asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
     return r;
 }
-__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
 __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
@@ -219,8 +214,8 @@ __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
 }
 
 // What a converter thread reads of one key: of the two 128-dim blocks c = group, group + 2 the record
-// bytes 64c + 16q .. + 15 (the codes of 16-dim blocks 8c + 2q and 8c + 2q + 1) and their scales, and RoPE
-// dims 16q + 8 group .. + 7.
+// bytes 64c + 16q .. + 15 (the codes of 16-dim blocks 8c + 2q and 8c + 2q + 1) and their scales, and, for half of the
+// keys, RoPE dims 16q .. 16q + 15.
 template <int R, bool kBlkOrder>
 struct HalfRecord {
     // 352-byte records place block s's scale at 320 + 8 (s & 3) + (s >> 2): the thread's four scales lie in
@@ -228,7 +223,7 @@ struct HalfRecord {
     static constexpr bool kPermuted = R == 352 && !kBlkOrder;
     uint4 codes[2];
     uint32_t sc[kPermuted ? 4 : 2];
-    uint32_t rope[R == 352 ? 2 : 4];
+    uint32_t rope[R == 352 ? 4 : 8];
 
     __device__ __forceinline__ void load_codes(const uint8_t* rec, int q, int group, int i) { codes[i] = ldg_stream16(rec + 64 * (group + 2 * i) + 16 * q); }
     __device__ __forceinline__ void load_scales(const uint8_t* rec, int q, int group) {
@@ -241,13 +236,11 @@ struct HalfRecord {
             sc[1] = ldg_stream2(p + 16);
         }
     }
-    __device__ __forceinline__ void load_rope(const uint8_t* rec, int q, int group) {
-        if constexpr (R == 352) {
-            const uint2 x = ldg_stream8(rec + 256 + 16 * q + 8 * group);
-            rope[0] = x.x; rope[1] = x.y;
-        } else {
-            const uint4 x = ldg_stream16(rec + 304 + 32 * q + 16 * group);
-            rope[0] = x.x; rope[1] = x.y; rope[2] = x.z; rope[3] = x.w;
+    __device__ __forceinline__ void load_rope(const uint8_t* rec, int q) {
+#pragma unroll
+        for (int e = 0; e < (R == 352 ? 1 : 2); ++e) {
+            const uint4 x = ldg_stream16(rec + (R == 352 ? 256 + 16 * q : 304 + 32 * q + 16 * e));
+            rope[4 * e] = x.x; rope[4 * e + 1] = x.y; rope[4 * e + 2] = x.z; rope[4 * e + 3] = x.w;
         }
     }
     // the scales of the 16-dim blocks of 128-dim block group + 2i: low byte 8c + 2q, next byte 8c + 2q + 1
@@ -259,13 +252,13 @@ struct HalfRecord {
             return sc[i];
         }
     }
-    // RoPE dims as 16-bit values (f16; the bf16 of 432-byte records as they are)
-    __device__ __forceinline__ uint4 rope_values() const {
+    // RoPE dims 16q + 8e .. + 7 as 16-bit values (f16; the bf16 of 432-byte records as they are)
+    __device__ __forceinline__ uint4 rope_values(int e) const {
         if constexpr (R == 352) {
-            const uint2 a = e4m3x4_to_f16(rope[0]), b = e4m3x4_to_f16(rope[1]);
+            const uint2 a = e4m3x4_to_f16(rope[2 * e]), b = e4m3x4_to_f16(rope[2 * e + 1]);
             return make_uint4(a.x, a.y, b.x, b.y);
         } else {
-            return make_uint4(rope[0], rope[1], rope[2], rope[3]);
+            return make_uint4(rope[4 * e], rope[4 * e + 1], rope[4 * e + 2], rope[4 * e + 3]);
         }
     }
 };
@@ -355,18 +348,23 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         };
         // group 0: per-row prescale and f16 (bf16 RoPE for 432-byte records) in place; the rows' scales and positions
         auto stage_q = [&](const Job& j, int seg) {
-            constexpr int kTpr = kGroupThreads / N, kChunks = 72 / kTpr;   // threads of a row, chunks of 8 dims of a thread
+            constexpr int kTpr = kGroupThreads / N, kPer = 8 / kTpr;   // threads of a row; blocks of 64 dims, and chunks of 8 RoPE dims, of a thread
             if (ok) ok = wait_warp(ctl, &ctl->qload, seg & 1, a.status);
             const int r = threadIdx.x / kTpr, part = threadIdx.x % kTpr;
+            auto chunk_at = [&](int bx, int c) { return sbase + kOffQ + bx * S::kQBlk + swz(r, c); };
             float qmax = 0.0f;
-            if (ok) {
-#pragma unroll 3
-                for (int k = kChunks * part; k < kChunks * part + kChunks; ++k) {
-                    const uint4 x = lds_u128(sbase + kOffQ + (k >> 3) * S::kQBlk + swz(r, k & 7));
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            auto take_max = [&](uint4 x) {
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        qmax = fmax3(qmax, fabsf(__uint_as_float(w[m] << 16)), fabsf(__uint_as_float(w[m] & 0xFFFF0000u)));
+                for (int m = 0; m < 4; ++m)
+                    qmax = fmax3(qmax, fabsf(__uint_as_float(w[m] << 16)), fabsf(__uint_as_float(w[m] & 0xFFFF0000u)));
+            };
+            if (ok) {
+#pragma unroll 1
+                for (int m = 0; m < kPer; ++m) {
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) take_max(lds_u128(chunk_at(part + kTpr * m, (i + part) & 7)));
+                    take_max(lds_u128(chunk_at(8, part + kTpr * m)));
                 }
             }
 #pragma unroll
@@ -384,20 +382,30 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 const int tok = (j.row0 + min(r, j.rows - 1)) / a.jobs.h_q;
                 sts_u32(pos_s + 4 * r, static_cast<uint32_t>(j.first_pos + tok - j.first_tok));
             }
-            if (ok) {
-#pragma unroll 3
-                for (int k = kChunks * part; k < kChunks * part + kChunks; ++k) {
-                    const bool bf = R == 432 && k >= 64;   // bf16 RoPE of 432-byte records
-                    const uint32_t addr = sbase + kOffQ + (k >> 3) * S::kQBlk + swz(r, k & 7);
-                    const uint4 x = lds_u128(addr);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[4];
+            auto scaled = [&](uint4 x, bool bf) {
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const float lo = __uint_as_float(w[m] << 16) * fpre, hi = __uint_as_float(w[m] & 0xFFFF0000u) * fpre;
-                        y[m] = bf ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+                for (int m = 0; m < 4; ++m) {
+                    const float lo = __uint_as_float(w[m] << 16) * fpre, hi = __uint_as_float(w[m] & 0xFFFF0000u) * fpre;
+                    y[m] = bf ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+                }
+                return make_uint4(y[0], y[1], y[2], y[3]);
+            };
+            if (ok) {
+                // (odd blocks with the chunks of each pair swapped, as the converters store K)
+#pragma unroll 1
+                for (int m = 0; m < kPer; ++m) {
+                    const int bx = part + kTpr * m;
+#pragma unroll 2
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = 2 * ((i + part) & 3);
+                        const uint4 x = lds_u128(chunk_at(bx, c)), y = lds_u128(chunk_at(bx, c + 1));
+                        sts_u128(chunk_at(bx, c ^ (bx & 1)), scaled(x, false));
+                        sts_u128(chunk_at(bx, (c + 1) ^ (bx & 1)), scaled(y, false));
                     }
-                    sts_u128(addr, make_uint4(y[0], y[1], y[2], y[3]));
+                    const uint32_t rope = chunk_at(8, part + kTpr * m);
+                    sts_u128(rope, scaled(lds_u128(rope), R == 432));   // bf16 RoPE of 432-byte records
                 }
             }
             fence_proxy_async_smem();
@@ -487,6 +495,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 };
                 float tmax = -INFINITY;
                 uint32_t nan0 = 0u, nan1 = 0u;
+                if (ok && it >= 2) {   // the PV that read this P buffer
+                    const int g = 4 * it - 5;
+                    ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                }
+                // the other group's tile before this one has its references
+                if (ok && it > s0) ok = wait_warp(ctl, &ctl->voted[grp ^ 1], ((it - 1) >> 1) & 1, a.status);
                 if (ok) ok = wait_warp(ctl, &ctl->sfull[grp], (it >> 1) & 1, a.status);
                 if (ok) {
                     if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
@@ -498,12 +512,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     nan1 = lds_u8(nan_s + 8) | lds_u8(nan_s + 72);
                     tmem_wait_ld();
                 }
-                if (ok && it >= 2) {   // the PV that read this P buffer
-                    const int g = 4 * it - 5;
-                    ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
-                }
-                // the other group's tile before this one has its references
-                if (ok && it > s0) ok = wait_warp(ctl, &ctl->voted[grp ^ 1], ((it - 1) >> 1) & 1, a.status);
                 if (ok) tmax = load_z();
                 // ---- does any row need a new reference? (one barrier reduction; also entered where a wait ran out,
                 // and then left by the whole group at once)
@@ -648,8 +656,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 }
             }
             named_bar_sync(bar_all, kSoftThreads);
-            // O^T blocks 2 grp, 2 grp + 1: this thread's lane is dim 128b + 32qd + lane; a warp store covers 32 consecutive
-            // dims of one row (64 bytes)
+            // O^T blocks 2 grp, 2 grp + 1: this thread's lane is dim 128b + 32qd + lane (in the second half of a block with
+            // the chunks of each pair swapped); a warp store covers 32 consecutive dims of one row (64 bytes)
+            const int dim = 32 * qd + (qd >= 2 ? lane ^ 8 : lane);
             uint16_t* dst = whole ? reinterpret_cast<uint16_t*>(a.out) + row * 512
                                   : a.part_out + static_cast<int64_t>(slot) * N * 512;
 #pragma unroll 1
@@ -658,7 +667,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 uint32_t o[16];
                 tmem_ld16(lane_base + S::kColO + N * b + r0, o);
                 tmem_wait_ld();
-                uint16_t* p = dst + static_cast<int64_t>(r0) * 512 + 128 * b + 32 * qd + lane;
+                uint16_t* p = dst + static_cast<int64_t>(r0) * 512 + 128 * b + dim;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     if (r0 + e < j.rows) {
@@ -683,12 +692,15 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         // ============ converters: two groups of eight warps, group g the 128-dim blocks g and g + 2 ============
         const int group = (warp - S::kSoft) >> 3;
         const int t = (threadIdx.x - 32 * S::kSoft) & 255;
-        // lane l of a group's warp w: key 8w + (l & 7), quarter q = l >> 3: the eight lanes of a quarter-warp
-        // store to eight bank slots, and the four quarters of a key load one 64-byte run
-        const int q = (t >> 3) & 3;
-        const int j = (t & 7) + 8 * (t >> 5);
+        // Lane l of a group's warp w: quarter q = l & 3 of key j, so that four lanes load one 64-byte run, and a quarter-warp
+        // the runs of keys j and j + 2, which lie in different banks of the load's data stage: 6 of its cycles a load,
+        // against 17.6 with the eight keys of a quarter-warp in lanes beside one another. Its eight stores go to
+        // eight bank slots as the chunks of each pair are swapped in the second half of a block (q >> 1).
+        const int q = t & 3;
+        const int j = 8 * (t >> 5) + ((t >> 3) & 1) + 2 * ((t >> 2) & 1) + 4 * ((t >> 4) & 1);
+        const bool with_rope = (t >> 7) == group;     // group 0 the RoPE dims of keys 0-31, group 1 of keys 32-63
         const uint32_t row_s = sbase + S::kOffK + (q >> 1) * kSubBlk;
-        const int ch0 = 4 * (q & 1);
+        const int ch0 = 4 * (q & 1), odd = q >> 1;
         bool ok = true;
         HalfRecord<R, kBlkOrder> raw;
         int cur = -1, nxt = -1;                       // slots of this thread's key in this tile, in the next
@@ -707,7 +719,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             raw.load_codes(rec, q, group, 0);
             raw.load_codes(rec, q, group, 1);
             raw.load_scales(rec, q, group);
-            raw.load_rope(rec, q, group);
+            if (with_rope) raw.load_rope(rec, q);
         }
         int slot = group, round = 0;                  // ring slot of this group's next block, times around the ring
         for (int k = 0; k < count; ++k) {
@@ -716,7 +728,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             const uint32_t sp0 = raw.scale_pair(q, group, 0), sp1 = raw.scale_pair(q, group, 1);
             // dims with a NaN scale become zeros, and the key's scores NaN
             const uint32_t nan = __ballot_sync(0xffffffffu, cur >= 0 && has_nan_e4m3(sp0 | (sp1 << 16)));
-            const bool bad = ((nan >> (lane & 7)) & 0x01010101u) != 0u;
+            const bool bad = ((nan >> (lane & 28)) & 0xFu) != 0u;
             const bool v = cur >= 0 && !bad;
             if (q == 0) sts_u8(sbase + kOffNan + 128 * (k & 3) + 64 * group + j, bad ? 1u : 0u);
             if (nxt >= 0) raw.load_scales(next_rec, q, group);
@@ -728,16 +740,20 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                 const uint32_t sp = i == 0 ? sp0 : sp1;
                 const __half2 sa = scale_half2(sp & 0xFFu), sb = scale_half2(sp >> 8);
-                sts_u128(blk + swz(j, ch0), v ? dq8(raw.codes[i].x, sa) : zero);
-                sts_u128(blk + swz(j, ch0 + 1), v ? dq8(raw.codes[i].y, sa) : zero);
-                sts_u128(blk + swz(j, ch0 + 2), v ? dq8(raw.codes[i].z, sb) : zero);
-                sts_u128(blk + swz(j, ch0 + 3), v ? dq8(raw.codes[i].w, sb) : zero);
+                sts_u128(blk + swz(j, ch0 ^ odd), v ? dq8(raw.codes[i].x, sa) : zero);
+                sts_u128(blk + swz(j, (ch0 + 1) ^ odd), v ? dq8(raw.codes[i].y, sa) : zero);
+                sts_u128(blk + swz(j, (ch0 + 2) ^ odd), v ? dq8(raw.codes[i].z, sb) : zero);
+                sts_u128(blk + swz(j, (ch0 + 3) ^ odd), v ? dq8(raw.codes[i].w, sb) : zero);
                 // The RoPE dims go to the buffer of kRopeRing tiles ago: the PV commit that freed this group's first
                 // block of the tile (or, before the ring's first round, no tile at all) came behind that QK
-                if (i == 0) sts_u128(sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk + swz(j, 2 * q + group), cur >= 0 ? raw.rope_values() : zero);
+                if (i == 0 && with_rope) {
+                    const uint32_t rope = sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk;
+                    sts_u128(rope + swz(j, 2 * q), cur >= 0 ? raw.rope_values(0) : zero);
+                    sts_u128(rope + swz(j, 2 * q + 1), cur >= 0 ? raw.rope_values(1) : zero);
+                }
                 if (nxt >= 0) {
                     raw.load_codes(next_rec, q, group, i);
-                    if (i == 0) raw.load_rope(next_rec, q, group);
+                    if (i == 0 && with_rope) raw.load_rope(next_rec, q);
                 }
                 slot += 2;
                 if (slot >= S::kRing) {
