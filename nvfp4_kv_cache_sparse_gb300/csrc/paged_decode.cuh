@@ -111,8 +111,9 @@ struct __align__(8) Ctl {
     uint64_t pfull[2];        // softmax warps, by tile parity: P^T written (and O^T rescaled)
     uint64_t voted[2];        // softmax warps, by tile parity: the references are those of the next tile
     uint64_t tfull[kAhead];   // look-up warp: slots and description of a tile
-    uint64_t tfree[kAhead];   // every other warp has taken them
+    uint64_t tfree[kAhead];   // converters and softmax warps have taken them
     uint64_t drain;           // every MMA issued completed
+    uint32_t pfirst[2];       // by tile parity, behind pfull: the tile is the first one of its segment
     uint32_t tmem_base;
     uint32_t abort;
 };
@@ -170,6 +171,38 @@ __device__ __forceinline__ bool wait_warp(Ctl* ctl, uint64_t* bar, uint32_t pari
         if (!ok) set_abort(ctl, status);
     }
     return __all_sync(0xffffffffu, ok);
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(Ctl* ctl, uint64_t* bar, uint32_t parity, uint32_t* status) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok && !aborted(ctl)) {
+        ok = mbar_wait(bar, parity);
+        if (!ok) set_abort(ctl, status);
+    }
+    return ok;
+}
+
+// Which of three phases have completed, without waiting for them (bits 0, 1, 2; the tests are in flight together).
+__device__ __forceinline__ uint32_t test_three(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2) {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p, q, r;\n"
+        "  .reg .b32 x, y;\n"
+        "  mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+        "  mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 q, [%3], %4;\n"
+        "  mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 r, [%5], %6;\n"
+        "  selp.b32 %0, 1, 0, p;\n"
+        "  selp.b32 x, 2, 0, q;\n"
+        "  selp.b32 y, 4, 0, r;\n"
+        "  or.b32 %0, %0, x;\n"
+        "  or.b32 %0, %0, y;\n"
+        "}\n"
+        : "=&r"(r)
+        : "r"(smem_addr(b0)), "r"(p0), "r"(smem_addr(b1)), "r"(p1), "r"(smem_addr(b2)), "r"(p2)
+        : "memory");
+    return r;
 }
 
 __device__ __forceinline__ float lds_f32(uint32_t a) {
@@ -293,7 +326,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         }
         for (int s = 0; s < kAhead; ++s) {
             mbar_init(&ctl->tfull[s], 1);
-            mbar_init(&ctl->tfree[s], kGroupWarps + S::kConv + 2);
+            mbar_init(&ctl->tfree[s], kGroupWarps + S::kConv);
         }
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
@@ -598,6 +631,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     sts_u16(x + swz(c, (k0 >> 3) + 1), static_cast<uint16_t>(w1));
                     sts_u16(x + swz(c + 1, (k0 >> 3) + 1), static_cast<uint16_t>(w1 >> 16));
                 }
+                if (qd == 0 && lane == 0) ctl->pfirst[grp] = it == s0 ? 1u : 0u;
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -699,21 +733,23 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         const int q = t & 3;
         const int j = 8 * (t >> 5) + ((t >> 3) & 1) + 2 * ((t >> 2) & 1) + 4 * ((t >> 4) & 1);
         const bool with_rope = (t >> 7) == group;     // group 0 the RoPE dims of keys 0-31, group 1 of keys 32-63
-        const uint32_t row_s = sbase + S::kOffK + (q >> 1) * kSubBlk;
-        const int ch0 = 4 * (q & 1), odd = q >> 1;
+        // the thread's four chunks of a block are 16-byte slots x, x ^ 1, x ^ 2, x ^ 3 of row j of its half (128B swizzle)
+        const uint32_t store0 = sbase + S::kOffK + (q >> 1) * kSubBlk + 128 * j + (((4 * (q & 1)) ^ (q >> 1) ^ (j & 7)) << 4);
         bool ok = true;
         HalfRecord<R, kBlkOrder> raw;
-        int cur = -1, nxt = -1;                       // slots of this thread's key in this tile, in the next
-        auto take = [&](int k) {
-            nxt = -1;
-            if (k >= count) return;
-            if (ok) ok = wait_warp(ctl, &ctl->tfull[k % kAhead], (k / kAhead) & 1, a.status);
-            if (ok) nxt = static_cast<int>(lds_u32(sbase + kOffSlot + 4 * kTile * (k % kAhead) + 4 * j));
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&ctl->tfree[k % kAhead]);
+        auto slot_at = [&](int k) { return static_cast<int>(lds_u32(sbase + kOffSlot + 4 * kTile * (k % kAhead) + 4 * j)); };
+        auto tile_bar = [&](int k) { return &ctl->tfull[k % kAhead]; };
+        auto taken = [&](int k) {   // behind a __syncwarp()
+            if (lane == 0) mbar_arrive(&ctl->tfree[k % kAhead]);
         };
-        take(0);
-        cur = nxt;
+        int cur = -1, nxt = -1;                       // slots of this thread's key in this tile, in the next
+#pragma unroll 1
+        for (int k = 0; k < min(count, 2); ++k) {
+            if (ok) ok = wait_warp(ctl, tile_bar(k), 0, a.status);
+            if (ok) (k == 0 ? cur : nxt) = slot_at(k);
+            __syncwarp();
+            if (ok) taken(k);
+        }
         if (cur >= 0) {
             const uint8_t* rec = a.cache + static_cast<int64_t>(cur) * R;
             raw.load_codes(rec, q, group, 0);
@@ -722,32 +758,40 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             if (with_rope) raw.load_rope(rec, q);
         }
         int slot = group, round = 0;                  // ring slot of this group's next block, times around the ring
-        for (int k = 0; k < count; ++k) {
-            take(k + 1);
+        for (int k = 0; k < count && ok; ++k) {
+            // the tile's three barriers are asked ahead of the work that does not need them
+            const bool more = k + 2 < count;
+            const int slot1 = slot + 2 >= S::kRing ? slot + 2 - S::kRing : slot + 2, round1 = round + (slot + 2 >= S::kRing ? 1 : 0);
+            uint32_t ready = test_three(&ctl->kfree[slot], (round - 1) & 1, &ctl->kfree[slot1], (round1 - 1) & 1, tile_bar(k + 2), ((k + 2) / kAhead) & 1);
+            if (round == 0) ready |= 1u;
+            if (round1 == 0) ready |= 2u;
+            ready = __reduce_and_sync(0xffffffffu, ready);
             const uint8_t* next_rec = a.cache + static_cast<int64_t>(max(nxt, 0)) * R;
-            const uint32_t sp0 = raw.scale_pair(q, group, 0), sp1 = raw.scale_pair(q, group, 1);
-            // dims with a NaN scale become zeros, and the key's scores NaN
-            const uint32_t nan = __ballot_sync(0xffffffffu, cur >= 0 && has_nan_e4m3(sp0 | (sp1 << 16)));
+            uint32_t sp[2] = {raw.scale_pair(q, group, 0), raw.scale_pair(q, group, 1)};
+            // dims with a NaN scale become zeros, and the key's scores NaN; a key that is not there is zeros: scales 0
+            const uint32_t nan = __ballot_sync(0xffffffffu, cur >= 0 && has_nan_e4m3(sp[0] | (sp[1] << 16)));
             const bool bad = ((nan >> (lane & 28)) & 0xFu) != 0u;
-            const bool v = cur >= 0 && !bad;
+            if (cur < 0 || bad) sp[0] = sp[1] = 0u;
             if (q == 0) sts_u8(sbase + kOffNan + 128 * (k & 3) + 64 * group + j, bad ? 1u : 0u);
             if (nxt >= 0) raw.load_scales(next_rec, q, group);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (ok && round > 0) ok = wait_warp(ctl, &ctl->kfree[slot], (round - 1) & 1, a.status);
-                if (!ok) break;
-                const uint32_t blk = row_s + slot * kBlk;
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t sp = i == 0 ? sp0 : sp1;
-                const __half2 sa = scale_half2(sp & 0xFFu), sb = scale_half2(sp >> 8);
-                sts_u128(blk + swz(j, ch0 ^ odd), v ? dq8(raw.codes[i].x, sa) : zero);
-                sts_u128(blk + swz(j, (ch0 + 1) ^ odd), v ? dq8(raw.codes[i].y, sa) : zero);
-                sts_u128(blk + swz(j, (ch0 + 2) ^ odd), v ? dq8(raw.codes[i].z, sb) : zero);
-                sts_u128(blk + swz(j, (ch0 + 3) ^ odd), v ? dq8(raw.codes[i].w, sb) : zero);
+                if ((ready & (1u << i)) == 0u &&
+                    !wait_warp(ctl, &ctl->kfree[i == 0 ? slot : slot1], ((i == 0 ? round : round1) - 1) & 1, a.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = store0 + (i == 0 ? slot : slot1) * kBlk;
+                const __half2 sa = scale_half2(sp[i] & 0xFFu), sb = scale_half2(sp[i] >> 8);
+                sts_u128(at, dq8(raw.codes[i].x, sa));
+                sts_u128(at ^ 16u, dq8(raw.codes[i].y, sa));
+                sts_u128(at ^ 32u, dq8(raw.codes[i].z, sb));
+                sts_u128(at ^ 48u, dq8(raw.codes[i].w, sb));
                 // The RoPE dims go to the buffer of kRopeRing tiles ago: the PV commit that freed this group's first
                 // block of the tile (or, before the ring's first round, no tile at all) came behind that QK
                 if (i == 0 && with_rope) {
                     const uint32_t rope = sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     sts_u128(rope + swz(j, 2 * q), cur >= 0 ? raw.rope_values(0) : zero);
                     sts_u128(rope + swz(j, 2 * q + 1), cur >= 0 ? raw.rope_values(1) : zero);
                 }
@@ -755,17 +799,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     raw.load_codes(next_rec, q, group, i);
                     if (i == 0 && with_rope) raw.load_rope(next_rec, q);
                 }
-                slot += 2;
-                if (slot >= S::kRing) {
-                    slot -= S::kRing;
-                    ++round;
-                }
             }
             if (!ok) break;
+            if (more && (ready & 4u) == 0u) ok = wait_warp(ctl, tile_bar(k + 2), ((k + 2) / kAhead) & 1, a.status);
+            cur = nxt;
+            nxt = more && ok ? slot_at(k + 2) : -1;
+            slot = slot1 + 2 >= S::kRing ? slot1 + 2 - S::kRing : slot1 + 2;
+            round = round1 + (slot1 + 2 >= S::kRing ? 1 : 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->kfull[k & 3]);
-            cur = nxt;
+            if (more && ok) taken(k + 2);
         }
     } else if (warp == kWarpLook) {
         // ============ look-up warp: the slots of the keys of every tile, and their records into L2 ============
@@ -821,24 +865,27 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         const uint64_t rdesc0 = sdesc_sw128(sbase + S::kOffRope, 16, 1024);       // K-major: keys x RoPE dims
         const uint64_t qdesc0 = sdesc_sw128(sbase + kOffQ, 16, 1024);             // K-major: rows x dims
         const bool leader = elect_one_in_warp();
-        bool ok = true;
-        int slot = 0, rslot = 0, seg = 0;
-        for (int it = 0; it < count && ok; ++it) {
-            ok = wait_warp(ctl, &ctl->tfull[it % kAhead], (it / kAhead) & 1, a.status);
-            const bool first = (lds_u32(sbase + kOffTile + 16 * (it % kAhead) + 8) & 1u) != 0u;
-            __syncwarp();
-            if (ok && leader) mbar_arrive(&ctl->tfree[it % kAhead]);
-            if (ok && first) ok = wait_warp(ctl, &ctl->qready, seg++ & 1, a.status);
-            // the score buffer: its scores of two tiles ago have been read
-            if (ok && it >= 2) ok = wait_warp(ctl, &ctl->pfull[it & 1], ((it - 2) >> 1) & 1, a.status);
-            if (ok) ok = wait_warp(ctl, &ctl->kfull[it & 3], (it >> 2) & 1, a.status);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t d = tmem + S::kColS + N * (it & 1);
-            // (short loops: straight-line code of 36 MMAs runs at the pace of the instruction fetch, 50 to 60 clk
-            // an MMA against 25)
-            if (leader) {
-#pragma unroll 1
+        if (leader) {
+            bool ok = true;
+            int slot = 0, rslot = 0, seg = 0, s1 = 0;
+            for (int it = 0; it < count; ++it) {
+                if (it == s1) {   // a segment begins: its length, its rows
+                    ok = wait_one(ctl, &ctl->tfull[it % kAhead], (it / kAhead) & 1, a.status);
+                    if (!ok) break;
+                    s1 = it + static_cast<int>(lds_u32(sbase + kOffTile + 16 * (it % kAhead) + 8) >> 1);
+                    ok = wait_one(ctl, &ctl->qready, seg++ & 1, a.status);
+                }
+                // the score buffer (its scores of two tiles ago have been read) and the keys
+                const bool free = it < 2 || mbar_test_wait(&ctl->pfull[it & 1], ((it - 2) >> 1) & 1);
+                const bool full = mbar_test_wait(&ctl->kfull[it & 3], (it >> 2) & 1);
+                if (ok && !free) ok = wait_one(ctl, &ctl->pfull[it & 1], ((it - 2) >> 1) & 1, a.status);
+                if (ok && !full) ok = wait_one(ctl, &ctl->kfull[it & 3], (it >> 2) & 1, a.status);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem + S::kColS + N * (it & 1);
+                // (short loops: straight-line code of 36 MMAs runs at the pace of the instruction fetch, 50 to 60 clk
+                // an MMA against 25)
+#pragma unroll 3
                 for (int b = 0; b < 9; ++b) {   // 64 dims each, the RoPE dims last
                     const uint64_t kd = b < 8 ? kdesc0 + static_cast<uint64_t>((slot * kBlk + (b & 1) * kSubBlk) >> 4)
                                               : rdesc0 + static_cast<uint64_t>((rslot * kSubBlk) >> 4);
@@ -850,10 +897,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     if ((b & 1) && ++slot == S::kRing) slot = 0;
                 }
                 if (++rslot == S::kRopeRing) rslot = 0;
+                mma_commit(&ctl->sfull[it & 1]);
             }
-            if (leader) mma_commit(&ctl->sfull[it & 1]);
-            __syncwarp();
         }
+        __syncwarp();
         if (leader) mma_commit(&ctl->drain);
         __syncwarp();
         if (!mbar_wait(&ctl->drain, 0)) set_abort(ctl, a.status);
@@ -864,18 +911,13 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         const uint64_t vdesc0 = sdesc_sw128(sbase + S::kOffK, kSubBlk, 1024);     // MN-major: dims x keys
         const uint64_t pdesc0 = sdesc_sw128(sbase + S::kOffP, 16, 1024);          // K-major: rows x keys
         const bool leader = elect_one_in_warp();
-        bool ok = true;
-        int slot = 0;
-        for (int it = 0; it < count && ok; ++it) {
-            ok = wait_warp(ctl, &ctl->tfull[it % kAhead], (it / kAhead) & 1, a.status);
-            const bool first = (lds_u32(sbase + kOffTile + 16 * (it % kAhead) + 8) & 1u) != 0u;
-            __syncwarp();
-            if (ok && leader) mbar_arrive(&ctl->tfree[it % kAhead]);
-            if (ok) ok = wait_warp(ctl, &ctl->pfull[it & 1], (it >> 1) & 1, a.status);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t pd = pdesc0 + static_cast<uint64_t>((S::kPBytes * (it & 1)) >> 4);
-            if (leader) {
+        if (leader) {
+            int slot = 0;
+            for (int it = 0; it < count; ++it) {
+                if (!wait_one(ctl, &ctl->pfull[it & 1], (it >> 1) & 1, a.status)) break;
+                tc_fence_after_sync();
+                const bool first = *reinterpret_cast<volatile uint32_t*>(&ctl->pfirst[it & 1]) != 0u;
+                const uint64_t pd = pdesc0 + static_cast<uint64_t>((S::kPBytes * (it & 1)) >> 4);
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     const uint64_t vd = vdesc0 + static_cast<uint64_t>((slot * kBlk) >> 4);
@@ -887,8 +929,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     if (++slot == S::kRing) slot = 0;
                 }
             }
-            __syncwarp();
         }
+        __syncwarp();
         if (leader) mma_commit(&ctl->drain);
         __syncwarp();
         if (!mbar_wait(&ctl->drain, 0)) set_abort(ctl, a.status);
