@@ -211,7 +211,6 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
     return v;
 }
 __device__ __forceinline__ void sts_f32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-__device__ __forceinline__ void sts_u16(uint32_t a, uint16_t v) { asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory"); }
 __device__ __forceinline__ void sts_u8(uint32_t a, uint32_t v) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
     uint32_t v;
@@ -437,8 +436,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                         sts_u128(chunk_at(bx, c ^ (bx & 1)), scaled(x, false));
                         sts_u128(chunk_at(bx, (c + 1) ^ (bx & 1)), scaled(y, false));
                     }
-                    const uint32_t rope = chunk_at(8, part + kTpr * m);
-                    sts_u128(rope, scaled(lds_u128(rope), R == 432));   // bf16 RoPE of 432-byte records
+                    const int c = part + kTpr * m;   // RoPE chunks 1 and 2 of four are swapped (the threads of four lie in one warp)
+                    const uint4 x = scaled(lds_u128(chunk_at(8, c)), R == 432);   // bf16 RoPE of 432-byte records
+                    __syncwarp();
+                    sts_u128(chunk_at(8, (c & 4) | ((c & 1) << 1) | ((c >> 1) & 1)), x);
                 }
             }
             fence_proxy_async_smem();
@@ -615,7 +616,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                         for (int e = 0; e < 4; ++e)
                             if ((e < 2 ? nan0 : nan1) != 0u && z[g][e] != -INFINITY) z[g][e] = NAN;
                 }
-                // P^T in shared memory: row = query row, 64 keys across (K-major B operand)
+                // P^T in shared memory: row = query row, 64 keys across (K-major B operand). Lanes of neighbouring keys
+                // exchange a row each, so that a store is one wavefront of whole words.
+                const bool odd_key = (lane & 4) != 0;
+                const uint32_t perm = odd_key ? 0x3276u : 0x5410u;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     const int c = c0 + 8 * g;
@@ -625,11 +629,11 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     l[g][0] += p[0] + p[2];
                     l[g][1] += p[1] + p[3];
                     const uint32_t w0 = pack_f16x2(p[0], p[1]), w1 = pack_f16x2(p[2], p[3]);
-                    const uint32_t x = p_s + 2 * (k0 & 7);
-                    sts_u16(x + swz(c, k0 >> 3), static_cast<uint16_t>(w0));
-                    sts_u16(x + swz(c + 1, k0 >> 3), static_cast<uint16_t>(w0 >> 16));
-                    sts_u16(x + swz(c, (k0 >> 3) + 1), static_cast<uint16_t>(w1));
-                    sts_u16(x + swz(c + 1, (k0 >> 3) + 1), static_cast<uint16_t>(w1 >> 16));
+                    const uint32_t v0 = __byte_perm(w0, __shfl_xor_sync(0xffffffffu, w0, 4), perm);
+                    const uint32_t v1 = __byte_perm(w1, __shfl_xor_sync(0xffffffffu, w1, 4), perm);
+                    const int r = c + (odd_key ? 1 : 0);
+                    sts_u32(p_s + 4 * ((k0 & 7) >> 1) + swz(r, k0 >> 3), v0);
+                    sts_u32(p_s + 4 * ((k0 & 7) >> 1) + swz(r, (k0 >> 3) + 1), v1);
                 }
                 if (qd == 0 && lane == 0) ctl->pfirst[grp] = it == s0 ? 1u : 0u;
                 fence_proxy_async_smem();
@@ -792,8 +796,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 if (i == 0 && with_rope) {
                     const uint32_t rope = sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk;
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                    sts_u128(rope + swz(j, 2 * q), cur >= 0 ? raw.rope_values(0) : zero);
-                    sts_u128(rope + swz(j, 2 * q + 1), cur >= 0 ? raw.rope_values(1) : zero);
+                    const int c = 4 * (q >> 1) + (q & 1);   // chunks 1 and 2 of four swapped, for eight bank slots here too
+                    sts_u128(rope + swz(j, c), cur >= 0 ? raw.rope_values(0) : zero);
+                    sts_u128(rope + swz(j, c + 2), cur >= 0 ? raw.rope_values(1) : zero);
                 }
                 if (nxt >= 0) {
                     raw.load_codes(next_rec, q, group, i);
