@@ -18,70 +18,58 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Entry c of hdr names a job that was cut: first output row, rows (0: there is none), parts n, slot f of the
 // first part; the others lie in slots next(c), next(c) + step, ... With part lse L_s (log2) and f16 output
 // O_s (divided by its own sum): w_s = 2^(L_s - m), out = sum_s w_s O_s / (sum_s w_s + 2^(sink - m)),
-// lse = (m + log2 sum_s w_s) ln 2. Four warps take the parts of a row in turn and add up their fp32 sums
-// through shared memory, in warp order. A NaN L_s makes the row NaN; a row without any key gets out = 0,
-// lse = -inf.
+// lse = (m + log2 sum_s w_s) ln 2, in fp32. A warp per row and 128 dims: its lanes weigh the parts (one each, in
+// turns of 32), then the warp adds the parts up in their order, eight loads in flight. A NaN L_s makes the
+// row NaN; a row without any key gets out = 0, lse = -inf.
 __global__ void __launch_bounds__(128 * kJoinRows)
 paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict__ part_lse, const int4* __restrict__ hdr,
                   const float* __restrict__ sink, int h_q, int row_tile, int step, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-    __shared__ float acc_s[kJoinRows][4][512];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 h = hdr[blockIdx.x];
+    const int4 h = __ldcg(hdr + blockIdx.x);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r0 = blockIdx.y * kJoinRows;
-    if (r0 >= h.y) return;
-    const int r = r0 + (warp >> 2), sub = warp & 3;
+    const int r = blockIdx.y * kJoinRows + (warp >> 2), sub = warp & 3;
+    if (r >= h.y) return;
     const int parts = h.z;
+    const int64_t row = static_cast<int64_t>(h.x) + r;
+    const float sk = sink != nullptr ? __ldg(sink + row % h_q) * kLog2e : -INFINITY;
     auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? h.w : h.w + 1 + (s - 1) * step) * row_tile + r; };
-    float m = -INFINITY, tot = 0.0f;
-    if (r < h.y) {
-        for (int s = lane; s < parts; s += 32) m = fmaxf(m, part_lse[slot(s)]);
+    auto lse_of = [&](int s) { return s < parts ? __ldcg(part_lse + slot(s)) : -INFINITY; };
+    const float first = lse_of(lane);
+    float m = first, tot;
+    for (int s = 32 + lane; s < parts; s += 32) m = fmaxf(m, lse_of(s));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (m == -INFINITY) m = 0.0f;
-        for (int s = lane; s < parts; s += 32) tot += exp2f(part_lse[slot(s)] - m);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0f;
+    tot = exp2f(first - m);
+    for (int s = 32 + lane; s < parts; s += 32) tot += exp2f(lse_of(s) - m);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-        float acc[16];
+    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    const int d = 128 * sub + 4 * lane;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int base = 0; base < parts; base += 32) {
+        const float weight = exp2f((base == 0 ? first : lse_of(base + lane)) - m);
+        const int n = min(32, parts - base);
+        for (int i = 0; i < n; i += 8) {
+            uint2 x[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-#pragma unroll 2
-        for (int s = sub; s < parts; s += 4) {
-            const float w = exp2f(part_lse[slot(s)] - m);
-            const uint4* p = reinterpret_cast<const uint4*>(part_out + slot(s) * 512);
-            const uint4 x[2] = {p[lane], p[32 + lane]};   // dims 8 lane.. and 256 + 8 lane..
+            for (int e = 0; e < 8; ++e)
+                x[e] = i + e < n ? __ldcg(reinterpret_cast<const uint2*>(part_out + slot(base + i + e) * 512 + d)) : make_uint2(0u, 0u);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
-                    acc[8 * k + 2 * e] = fmaf(w, f.x, acc[8 * k + 2 * e]);
-                    acc[8 * k + 2 * e + 1] = fmaf(w, f.y, acc[8 * k + 2 * e + 1]);
-                }
+            for (int e = 0; e < 8; ++e) {
+                const float w = __shfl_sync(0xffffffffu, weight, (i + e) & 31);
+                if (i + e >= n) continue;
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&x[e].x)), f1 = __half22float2(*reinterpret_cast<const __half2*>(&x[e].y));
+                acc[0] = fmaf(w, f0.x, acc[0]);
+                acc[1] = fmaf(w, f0.y, acc[1]);
+                acc[2] = fmaf(w, f1.x, acc[2]);
+                acc[3] = fmaf(w, f1.y, acc[3]);
             }
         }
-        float* dst = acc_s[warp >> 2][sub];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-                *reinterpret_cast<float4*>(dst + 256 * k + 8 * lane + e) =
-                    make_float4(acc[8 * k + e], acc[8 * k + e + 1], acc[8 * k + e + 2], acc[8 * k + e + 3]);
     }
-    __syncthreads();
-    if (r >= h.y) return;
-    const float den = tot + (sink != nullptr ? exp2f(sink[(h.x + r) % h_q] * kLog2e - m) : 0.0f);
-    const float f = tot == 0.0f ? 0.0f : 1.0f / den;
-    const int d = 128 * sub + 4 * lane;
-    float v[4];
+    const float f = tot == 0.0f ? 0.0f : 1.0f / (tot + exp2f(sk - m));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float x = (acc_s[warp >> 2][0][d + e] + acc_s[warp >> 2][1][d + e]) + (acc_s[warp >> 2][2][d + e] + acc_s[warp >> 2][3][d + e]);
-        v[e] = f != 0.0f ? x * f : 0.0f;
-    }
-    const int64_t row = static_cast<int64_t>(h.x) + r;
-    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+    for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? acc[e] * f : 0.0f;
+    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc[0], acc[1]), __floats2bfloat162_rn(acc[2], acc[3])};
     *reinterpret_cast<uint2*>(out + row * 512 + d) = *reinterpret_cast<const uint2*>(o);
     if (sub == 0 && lane == 0) lse[row] = tot == 0.0f ? -INFINITY : (m + log2f(tot)) * kLn2;
 }

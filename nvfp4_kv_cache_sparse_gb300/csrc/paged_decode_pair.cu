@@ -12,7 +12,7 @@ namespace nvfp4mla {
 namespace {
 
 using pairdec::Segment;
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanClasses = 8;
 constexpr int kPlanEmpty = 31;   // CTAs of the plan that write the rows without a key
 
@@ -33,51 +33,51 @@ paged_plan_kernel(const paged::Jobs a, int pairs, int max_segments, int headers,
                   int4* __restrict__ hdr, void* out, float* lse, uint32_t* status) {
     constexpr int kRows = 128, kKeys = pairdec::kTile;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");   // (the pairs wait for the whole grid all the same)
     if (blockIdx.x > 0) {
         paged::write_empty_jobs<kRows, kKeys, kPlanThreads>(a, static_cast<int>(blockIdx.x) - 1, kPlanEmpty, out, lse);
         return;
     }
     paged::check_lengths(a, static_cast<int>(threadIdx.x), kPlanThreads, status);
-    __shared__ int64_t sums[2 + kPlanClasses + 1][32];
-    __shared__ int64_t counts[2][32];
+    __shared__ int64_t totals[kPlanWarps], cut_totals[kPlanWarps];
+    __shared__ int32_t jobs_with_keys[kPlanWarps], counts[2][kPlanWarps], classes[kPlanClasses][kPlanWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int jobs = a.batch * a.row_tiles;
     const int per = (jobs + kPlanThreads - 1) / kPlanThreads;
     const int ja = min(jobs, static_cast<int>(threadIdx.x) * per), jb = min(jobs, ja + per);
-    // the block's exclusive prefix sums (rows of scratch are used once, or in turn by calls with a barrier in between)
-    auto scan = [&](int64_t mine, int64_t* row, int64_t* total) {
-        int64_t incl = mine;
+    auto warp_scan = [&](auto v) {   // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const auto u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
         }
-        if (lane == 31) row[warp] = incl;
-        __syncthreads();
-        const int64_t w = row[lane];
-        int64_t upto = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        *total = __shfl_sync(0xffffffffu, upto, 31);
-        return __shfl_sync(0xffffffffu, upto - w, warp) + incl - mine;
+        return v;
     };
     // tiles of the thread's first job stay in a register (most calls have no more jobs than threads)
     const int first_tiles = ja < jb ? paged::job_info<kRows, kKeys>(a, ja).tiles : 0;
     auto tiles_of = [&](int j) { return j == ja ? first_tiles : paged::job_info<kRows, kKeys>(a, j).tiles; };
-    int64_t mine = 0, mine_n = 0, total, n;
+    int64_t mine = 0, total = 0;
+    int mine_n = 0, n = 0;
     for (int j = ja; j < jb; ++j) {
         const int nt = tiles_of(j);
         mine += nt;
         mine_n += nt > 0 ? 1 : 0;
     }
-    (void)scan(mine, sums[0], &total);
-    (void)scan(mine_n, sums[1], &n);
+    mine = warp_scan(mine);
+    mine_n = __reduce_add_sync(0xffffffffu, mine_n);
+    if (lane == 31) {
+        totals[warp] = mine;
+        jobs_with_keys[warp] = mine_n;
+    }
+    __syncthreads();
+    for (int w = 0; w < kPlanWarps; ++w) {
+        total += totals[w];
+        n += jobs_with_keys[w];
+    }
     const int64_t limit = n > 0 ? waves(n, pairs) * pairs : 0;
     // total / limit <= T; and sum ceil(t / T) < total / T + n, so T = ceil(total / (limit - n)) is enough if that is
-    // positive (limit >= n always; with equality one segment per job, T the longest, is)
+    // positive (limit >= n always; with equality one segment per job, T the longest, is). The sums below are under
+    // limit + n, which 31 bits hold.
     int64_t lo = 1, hi = 1;
     if (n > 0) {
         lo = max(int64_t(1), (total + limit - 1) / limit);
@@ -86,9 +86,16 @@ paged_plan_kernel(const paged::Jobs a, int pairs, int max_segments, int headers,
     }
     for (int turn = 0; lo < hi; turn ^= 1) {
         const int64_t mid = (lo + hi) >> 1;
-        int64_t c = 0, all;
-        for (int j = ja; j < jb; ++j) c += (tiles_of(j) + mid - 1) / mid;
-        (void)scan(c, counts[turn], &all);
+        const int m32 = static_cast<int>(min(mid, static_cast<int64_t>(INT32_MAX)));
+        int c = 0, all = 0;
+        for (int j = ja; j < jb; ++j) {
+            const int nt = tiles_of(j);
+            c += nt / m32 + (nt % m32 != 0 ? 1 : 0);
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) counts[turn][warp] = c;
+        __syncthreads();
+        for (int w = 0; w < kPlanWarps; ++w) all += counts[turn][w];
         if (all <= limit)
             hi = mid;
         else
@@ -97,45 +104,66 @@ paged_plan_kernel(const paged::Jobs a, int pairs, int max_segments, int headers,
     const int T = static_cast<int>(min(lo, static_cast<int64_t>(INT32_MAX)));
     auto pieces_of = [&](int nt) { return nt / T + (nt % T != 0 ? 1 : 0); };
     auto class_of = [&](int nt, int np) { return static_cast<int>((static_cast<int64_t>((nt + np - 1) / np - 1) * kPlanClasses) / T); };
-    // slots of the parts and numbers of the jobs that are cut
-    int64_t cuts = 0, all;
+    // segments in each class, slots of the parts and numbers of the jobs that are cut: prefix sums over the threads
+    int64_t cut = 0, all_cuts = 0;
+    int own[kPlanClasses] = {};
     for (int j = ja; j < jb; ++j) {
-        const int np = pieces_of(tiles_of(j));
-        if (np > 1) cuts += (static_cast<int64_t>(np) << 32) + 1;
+        const int nt = tiles_of(j);
+        if (nt == 0) continue;
+        const int np = pieces_of(nt), cl = class_of(nt, np);
+        if (np > 1) cut += (static_cast<int64_t>(np) << 32) + 1;
+#pragma unroll
+        for (int c = 0; c < kPlanClasses; ++c) own[c] += c == cl ? np : 0;
     }
-    cuts = scan(cuts, sums[2], &all);
-    const int cut_jobs = static_cast<int>(all & 0xffffffff);
-    int64_t begin = 0;
-#pragma unroll 1
-    for (int cl = kPlanClasses - 1; cl >= 0; --cl) {
-        int64_t own = 0, in_class;
-        for (int j = ja; j < jb; ++j) {
-            const int nt = tiles_of(j), np = pieces_of(nt);
-            if (nt > 0 && class_of(nt, np) == cl) own += np;
+    const int64_t cut_upto = warp_scan(cut);
+    if (lane == 31) cut_totals[warp] = cut_upto;
+    cut = cut_upto - cut;
+#pragma unroll
+    for (int c = 0; c < kPlanClasses; ++c) {
+        const int upto = warp_scan(own[c]);
+        if (lane == 31) classes[c][warp] = upto;
+        own[c] = upto - own[c];
+    }
+    __syncthreads();
+    for (int w = 0; w < kPlanWarps; ++w) {
+        if (w < warp) cut += cut_totals[w];
+        all_cuts += cut_totals[w];
+    }
+    const int cut_jobs = static_cast<int>(all_cuts & 0xffffffff);
+    int begin = 0;   // segments of the longer classes, of this one in the warps before
+#pragma unroll
+    for (int c = kPlanClasses - 1; c >= 0; --c) {
+        own[c] += begin;
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int v = classes[c][w];
+            if (w < warp) own[c] += v;
+            begin += v;
         }
-        int64_t at = begin + scan(own, sums[3 + cl], &in_class);
-        begin += in_class;
-        int64_t cut = cuts;
-        for (int j = ja; j < jb && own > 0; ++j) {
-            const int nt = tiles_of(j), np = pieces_of(nt);
-            if (nt == 0) continue;
-            if (class_of(nt, np) == cl) {
-                const paged::Job job = paged::job_info<kRows, kKeys>(a, j);
-                if (np > 1 && static_cast<int>(cut & 0xffffffff) < headers)
-                    hdr[cut & 0xffffffff] = make_int4(job.seq * a.rows_per_seq + job.row0, job.rows, np, static_cast<int>(cut >> 32));
-                for (int p = 0; p < np; ++p, ++at) {
-                    if (at >= max_segments) break;
-                    const int t0 = static_cast<int>(static_cast<int64_t>(nt) * p / np), t1 = static_cast<int>(static_cast<int64_t>(nt) * (p + 1) / np);
-                    int4* s = reinterpret_cast<int4*>(segments + at);
-                    s[0] = make_int4(job.seq, job.row0, job.rows, job.keys);
-                    s[1] = make_int4(t0 * kKeys, t1 - t0, job.first_pos, job.first_tok);
-                    s[2] = make_int4(np > 1 ? static_cast<int>(cut >> 32) + p : -1, 0, 0, 0);
-                }
+    }
+    for (int j = ja; j < jb; ++j) {
+        const int nt = tiles_of(j);
+        if (nt == 0) continue;
+        const int np = pieces_of(nt), cl = class_of(nt, np);
+        int at = 0;
+#pragma unroll
+        for (int c = 0; c < kPlanClasses; ++c)
+            if (c == cl) {
+                at = own[c];
+                own[c] += np;
             }
-            if (np > 1) cut += (static_cast<int64_t>(np) << 32) + 1;
+        const paged::Job job = paged::job_info<kRows, kKeys>(a, j);
+        if (np > 1 && static_cast<int>(cut & 0xffffffff) < headers)
+            hdr[cut & 0xffffffff] = make_int4(job.seq * a.rows_per_seq + job.row0, job.rows, np, static_cast<int>(cut >> 32));
+        for (int p = 0; p < np && at < max_segments; ++p, ++at) {
+            const int t0 = static_cast<int>(static_cast<int64_t>(nt) * p / np), t1 = static_cast<int>(static_cast<int64_t>(nt) * (p + 1) / np);
+            int4* s = reinterpret_cast<int4*>(segments + at);
+            s[0] = make_int4(job.seq, job.row0, job.rows, job.keys);
+            s[1] = make_int4(t0 * kKeys, t1 - t0, job.first_pos, job.first_tok);
+            s[2] = make_int4(np > 1 ? static_cast<int>(cut >> 32) + p : -1, 0, 0, 0);
         }
+        if (np > 1) cut += (static_cast<int64_t>(np) << 32) + 1;
     }
-    for (int64_t k = begin + threadIdx.x; k < max_segments; k += kPlanThreads)
+    for (int k = begin + static_cast<int>(threadIdx.x); k < max_segments; k += kPlanThreads)
         reinterpret_cast<int4*>(segments + k)[1] = make_int4(0, 0, 0, 0);
     for (int k = cut_jobs + static_cast<int>(threadIdx.x); k < headers; k += kPlanThreads) hdr[k] = make_int4(0, 0, 0, 0);
 }
