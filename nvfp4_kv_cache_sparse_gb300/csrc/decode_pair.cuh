@@ -697,7 +697,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // (kPaged: slot_of gives slots of the pool and -1, -2 only)
         auto in_range = [&](int32_t v) { return v >= 0 && (kPaged || static_cast<int64_t>(v) < a.num_slots); };
-        const uint32_t fnan = kPaged ? 0u : 0x7E007E00u;   // a masked key's K row: f16 quiet-NaN pairs (kPaged: zeros)
         bool ok = !aborted(ctl);
         if (!vrole) {
             const uint32_t st_a = sbase + kOffStA + j * kStrA;
@@ -735,11 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < n_tiles; ++k) {
                 const bool valid = in_range(idx0);
                 if (q == 0 && (kPaged ? idx0 == -2 : idx0 >= 0 && !valid) && a.status != nullptr) atomicOr(a.status, 0x2u);
-                // ---- blocks 0-3 (dims 0-255) once the previous QK's first half has read them
+                // ---- blocks 0-3 (dims 0-255) once the previous QK's first half has read them. The staged bytes are
+                // taken into registers ahead of that wait, all loads in flight, and the next tile's sent for.
                 cp_async_wait<1>();
                 __syncwarp();
-                if (k >= 1) ok = wait_warp(ctl, &ctl->khalf, (k - 1) & 1, a.status);
-                if (!ok) break;
                 uint32_t sc_lo, sc_hi;   // byte c: scale of block 4c + q (c = 0..3, 4..7)
                 if constexpr (R == 352 && !kBlkOrder) {
                     const uint2 s8 = lds_u64(st_a + 128 + 8 * q);   // permuted placement
@@ -750,53 +748,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sc_lo = gather_byte4(w0, q);
                     sc_hi = gather_byte4(w1, q);
                 }
+                uint2 cw[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) cw[c] = lds_u64(st_a + 32 * c + 8 * q);
+                // a masked key: scale NaN, so that its scores are (kPaged: 0); the codes left in the stage are numbers
+                if (!valid) sc_lo = sc_hi = kPaged ? 0u : 0x7F7F7F7Fu;
+                __syncwarp();
+                stage_a(idx1);   // the key's four threads have read part a of tile k
+                if (k >= 1) ok = wait_warp(ctl, &ctl->khalf, (k - 1) & 1, a.status);
+                if (!ok) break;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint2 cw = lds_u64(st_a + 32 * c + 8 * q);
                     const __half2 s2 = scale_half2((sc_lo >> (8 * c)) & 0xFFu);
-                    const uint4 lo = valid ? dq8(cw.x, s2) : make_uint4(fnan, fnan, fnan, fnan);
-                    const uint4 hi = valid ? dq8(cw.y, s2) : make_uint4(fnan, fnan, fnan, fnan);
-                    sts_u128(k_s + c * kBlk + swz(j, 2 * q), lo);
-                    sts_u128(k_s + c * kBlk + swz(j, 2 * q + 1), hi);
+                    sts_u128(k_s + c * kBlk + swz(j, 2 * q), dq8(cw[c].x, s2));
+                    sts_u128(k_s + c * kBlk + swz(j, 2 * q + 1), dq8(cw[c].y, s2));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) signal_leader(ctl, &ctl->kfull_a, crank, t == 0, 8);
-                stage_a(idx1);   // the key's four threads have read part a of tile k (the warp synced)
                 // ---- blocks 4-8 (dims 256-575) once the previous QK has finished
                 cp_async_wait<1>();
                 __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) cw[c] = lds_u64(st_b + 32 * c + 8 * q);
+                uint4 e0 = lds_u128(st_b + 128 + (R == 352 ? 16 : 32) * q), e1 = {};
+                if constexpr (R == 432) e1 = lds_u128(st_b + 128 + 32 * q + 16);
+                __syncwarp();
+                stage_b(idx1);
+                if constexpr (R == 352) {
+                    const uint2 x0 = e4m3x4_to_f16(e0.x), x1 = e4m3x4_to_f16(e0.y), x2 = e4m3x4_to_f16(e0.z), x3 = e4m3x4_to_f16(e0.w);
+                    e0 = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                    e1 = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                }
+                if (!valid) {
+                    const uint32_t fr = kPaged ? 0u : R == 352 ? 0x7E007E00u : 0x7FC07FC0u;   // RoPE block: f16 / bf16 quiet NaN
+                    e0 = e1 = make_uint4(fr, fr, fr, fr);
+                }
                 if (k >= 1) ok = wait_warp(ctl, &ctl->qkdone, (k - 1) & 1, a.status);
                 if (!ok) break;
 #pragma unroll
-                for (int c = 4; c < 8; ++c) {
-                    const uint2 cw = lds_u64(st_b + 32 * (c - 4) + 8 * q);
-                    const __half2 s2 = scale_half2((sc_hi >> (8 * (c - 4))) & 0xFFu);
-                    const uint4 lo = valid ? dq8(cw.x, s2) : make_uint4(fnan, fnan, fnan, fnan);
-                    const uint4 hi = valid ? dq8(cw.y, s2) : make_uint4(fnan, fnan, fnan, fnan);
-                    sts_u128(k_s + c * kBlk + swz(j, 2 * q), lo);
-                    sts_u128(k_s + c * kBlk + swz(j, 2 * q + 1), hi);
+                for (int c = 0; c < 4; ++c) {
+                    const __half2 s2 = scale_half2((sc_hi >> (8 * c)) & 0xFFu);
+                    sts_u128(k_s + (c + 4) * kBlk + swz(j, 2 * q), dq8(cw[c].x, s2));
+                    sts_u128(k_s + (c + 4) * kBlk + swz(j, 2 * q + 1), dq8(cw[c].y, s2));
                 }
-                if (valid) {
-                    if constexpr (R == 352) {
-                        const uint4 e = lds_u128(st_b + 128 + 16 * q);
-                        const uint2 e0 = e4m3x4_to_f16(e.x), e1 = e4m3x4_to_f16(e.y);
-                        const uint2 e2 = e4m3x4_to_f16(e.z), e3 = e4m3x4_to_f16(e.w);
-                        sts_u128(k_s + 8 * kBlk + swz(j, 2 * q), make_uint4(e0.x, e0.y, e1.x, e1.y));
-                        sts_u128(k_s + 8 * kBlk + swz(j, 2 * q + 1), make_uint4(e2.x, e2.y, e3.x, e3.y));
-                    } else {
-                        sts_u128(k_s + 8 * kBlk + swz(j, 2 * q), lds_u128(st_b + 128 + 32 * q));
-                        sts_u128(k_s + 8 * kBlk + swz(j, 2 * q + 1), lds_u128(st_b + 128 + 32 * q + 16));
-                    }
-                } else {
-                    const uint32_t fr = R == 352 || kPaged ? fnan : 0x7FC07FC0u;   // RoPE block: f16 / bf16 quiet NaN
-                    sts_u128(k_s + 8 * kBlk + swz(j, 2 * q), make_uint4(fr, fr, fr, fr));
-                    sts_u128(k_s + 8 * kBlk + swz(j, 2 * q + 1), make_uint4(fr, fr, fr, fr));
-                }
+                sts_u128(k_s + 8 * kBlk + swz(j, 2 * q), e0);
+                sts_u128(k_s + 8 * kBlk + swz(j, 2 * q + 1), e1);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) signal_leader(ctl, &ctl->kfull_b, crank, t == 0, 8);
-                stage_b(idx1);
                 idx0 = idx1;
                 idx1 = idx2;
                 idx2 = index_at(k + 3, own);   // in flight until the next tile's first arrive
@@ -827,11 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int hv = 0; hv < 2; ++hv) {   // V rows 64 hv + j: CTA hv's keys
                     cp_async_wait<1>();
                     __syncwarp();
-                    if (k == 0 && hv == 0) ok = wait_warp(ctl, &ctl->qstaged, 0, a.status);   // the V buffer held q
-                    if (ok && k >= 1) ok = wait_warp(ctl, hv == 0 ? &ctl->pvhalf : &ctl->pvdone, (k - 1) & 1, a.status);
-                    if (!ok) break;
                     const uint32_t st = sbase + kOffStV<R> + (hv * kOwn + j) * kStrV<R>;
-                    const bool valid = in_range(hv == 0 ? ia0 : ib0);
                     uint32_t sbytes;   // byte cl: scale of block 4 (4 crank + cl) + q
                     if constexpr (R == 352 && !kBlkOrder)
                         sbytes = lds_u32(st + 128 + 4 * q);
@@ -839,19 +835,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sbytes = gather_byte4(lds_u128(st + 128), q);
                     const uint2 c0 = lds_u64(st + 8 * q), c1 = lds_u64(st + 32 + 8 * q);
                     const uint2 c2 = lds_u64(st + 64 + 8 * q), c3 = lds_u64(st + 96 + 8 * q);
-                    // a masked key's V row is zero (its probability is zero, and 0 x 0 stays 0)
+                    // a masked key's V row is zero (its probability is zero, and 0 x 0 stays 0): scales 0, the codes are numbers
+                    if (!in_range(hv == 0 ? ia0 : ib0)) sbytes = 0u;
                     if constexpr (kPaged) {   // dims with a NaN scale are zeros: the key's scores carry the NaN
                         const uint32_t is_nan = __vcmpeq4(sbytes & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                         sbytes &= ~is_nan;
                     }
-                    write_v(v_s, 64 * hv + j, q,
-                            valid ? make_uint4(c0.x, c0.y, c1.x, c1.y) : make_uint4(0u, 0u, 0u, 0u),
-                            valid ? make_uint4(c2.x, c2.y, c3.x, c3.y) : make_uint4(0u, 0u, 0u, 0u),
-                            valid ? sbytes : 0u);
+                    __syncwarp();
+                    stage_v(hv, hv == 0 ? ia1 : ib1);   // the key's four threads have read the tile's
+                    if (k == 0 && hv == 0) ok = wait_warp(ctl, &ctl->qstaged, 0, a.status);   // the V buffer held q
+                    if (ok && k >= 1) ok = wait_warp(ctl, hv == 0 ? &ctl->pvhalf : &ctl->pvdone, (k - 1) & 1, a.status);
+                    if (!ok) break;
+                    write_v(v_s, 64 * hv + j, q, make_uint4(c0.x, c0.y, c1.x, c1.y), make_uint4(c2.x, c2.y, c3.x, c3.y), sbytes);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) signal_leader(ctl, hv == 0 ? &ctl->vfull_a : &ctl->vfull_b, crank, t == 0, 8);
-                    stage_v(hv, hv == 0 ? ia1 : ib1);
                 }
                 if (!ok) break;
                 ia0 = ia1;
