@@ -689,13 +689,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = t >> 2;    // key of the half tile (K: own key j; V: key 64 hv + j)
         const int q = t & 3;     // quarter: blocks 4c + q, RoPE dims 16q..
         constexpr int sb = R == 352 ? 320 : 256;                 // scale bytes of a record
-        auto index_at = [&](int i, int key) -> int32_t {        // key 0..127 of tile i
-            if (i >= n_tiles) return -1;
+        // The index of key 0..127 of tile i (kPaged: the entry of the page table), and the slot it gives. The load is in
+        // flight until slot_in, a tile later. (Looked up and checked at once it was waited for: 600 clk of the 4600 of
+        // a tile of 128 keys.)
+        const int32_t* table_row = kPaged ? a.jobs.page_table + seg.seq * a.jobs.table_stride : nullptr;
+        auto index_at = [&](int i, int key) -> int32_t {
             const int pos = key_begin + kTile * i + key;
-            if constexpr (kPaged) return paged::slot_of(a.jobs, seg.seq, key_end, pos);
-            return pos < key_end ? __ldg(idx_row + pos) : -1;
+            if (i >= n_tiles || pos >= key_end) return -1;
+            return __ldg(kPaged ? table_row + (pos >> a.jobs.page_shift) : idx_row + pos);
         };
-        // (kPaged: slot_of gives slots of the pool and -1, -2 only)
+        auto slot_in = [&](int32_t index, int i, int key) -> int32_t {
+            if constexpr (!kPaged) return index;
+            const int pos = key_begin + kTile * i + key;
+            if (i >= n_tiles || pos >= key_end) return -1;
+            if (static_cast<unsigned>(index) >= static_cast<unsigned>(a.jobs.num_pages)) return -2;
+            return (index << a.jobs.page_shift) + (pos & ((1 << a.jobs.page_shift) - 1));
+        };
+        // (kPaged: slots of the pool and -1, -2 only)
         auto in_range = [&](int32_t v) { return v >= 0 && (kPaged || static_cast<int64_t>(v) < a.num_slots); };
         bool ok = !aborted(ctl);
         if (!vrole) {
@@ -727,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (32 * t < key_end - key_begin) prefetch_l2(idx_row + key_begin + 32 * t);
             }
             const int own = kOwn * crank + j;
-            int32_t idx0 = index_at(0, own), idx1 = index_at(1, own);
+            int32_t idx0 = slot_in(index_at(0, own), 0, own), idx1 = slot_in(index_at(1, own), 1, own);
             stage_a(idx0);
             stage_b(idx0);
             int32_t idx2 = index_at(2, own);
@@ -798,8 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) signal_leader(ctl, &ctl->kfull_b, crank, t == 0, 8);
                 idx0 = idx1;
-                idx1 = idx2;
-                idx2 = index_at(k + 3, own);   // in flight until the next tile's first arrive
+                idx1 = slot_in(idx2, k + 2, own);
+                idx2 = index_at(k + 3, own);
             }
         } else {
             const uint32_t v_s = sbase + kOffV;
@@ -816,13 +826,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 cp_async_commit();
             };
-            int32_t ia0 = index_at(0, j), ib0 = index_at(0, kOwn + j);
-            int32_t ia1 = index_at(1, j), ib1 = index_at(1, kOwn + j);
+            int32_t ia0 = slot_in(index_at(0, j), 0, j), ib0 = slot_in(index_at(0, kOwn + j), 0, kOwn + j);
+            int32_t ia1 = slot_in(index_at(1, j), 1, j), ib1 = slot_in(index_at(1, kOwn + j), 1, kOwn + j);
             stage_v(0, ia0);
             stage_v(1, ib0);
             int32_t ia2 = index_at(2, j), ib2 = index_at(2, kOwn + j);
             for (int k = 0; k < n_tiles; ++k) {
-                if (kPaged && (ia2 == -2 || ib2 == -2)) ctl->outside = 1u;
 #pragma unroll
                 for (int hv = 0; hv < 2; ++hv) {   // V rows 64 hv + j: CTA hv's keys
                     cp_async_wait<1>();
@@ -846,6 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (k == 0 && hv == 0) ok = wait_warp(ctl, &ctl->qstaged, 0, a.status);   // the V buffer held q
                     if (ok && k >= 1) ok = wait_warp(ctl, hv == 0 ? &ctl->pvhalf : &ctl->pvdone, (k - 1) & 1, a.status);
                     if (!ok) break;
+                    // (ahead of the arrival that the softmax of the tile after the next has to have seen)
+                    if (kPaged && hv == 0 && (slot_in(ia2, k + 2, j) == -2 || slot_in(ib2, k + 2, kOwn + j) == -2)) ctl->outside = 1u;
                     write_v(v_s, 64 * hv + j, q, make_uint4(c0.x, c0.y, c1.x, c1.y), make_uint4(c2.x, c2.y, c3.x, c3.y), sbytes);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -854,8 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ia0 = ia1;
                 ib0 = ib1;
-                ia1 = ia2;
-                ib1 = ib2;
+                ia1 = slot_in(ia2, k + 2, j);
+                ib1 = slot_in(ib2, k + 2, kOwn + j);
                 ia2 = index_at(k + 3, j);
                 ib2 = index_at(k + 3, kOwn + j);
             }
