@@ -491,12 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int pos = warp_key + kTile * i;
                 const int n = last_pos + 1 - pos;   // keys up to the row's position
                 if (n < 32) seen = n > 0 ? (1u << n) - 1u : 0u;
-                // (a tile's flag is set ahead of the vfull arrivals of two tiles earlier, and the P of the last tile waited
-                // for that PV)
-                if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&ctl->outside) != 0u))
-                    seen &= __ballot_sync(0xffffffffu, paged::slot_of(a.jobs, seg.seq, key_end, pos + lane) >= 0);
             }
+            // (kPaged: a tile's flag is set ahead of the vfull arrivals of two tiles earlier, and the P of the last tile
+            // waited for that PV)
+            const uint32_t outside = kPaged ? *reinterpret_cast<volatile uint32_t*>(&ctl->outside) : 0u;
             if (ok) ok = wait_warp(ctl, &ctl->qkdone, i & 1, a.status);
+            if (kPaged && __any_sync(0xffffffffu, outside != 0u))
+                seen &= __ballot_sync(0xffffffffu, paged::slot_of(a.jobs, seg.seq, key_end, warp_key + kTile * i + lane) >= 0);
             if (ok) {
                 tc_fence_after_sync();
                 tmem_ld32(lane_base + kColS + 32 * h2, s);
@@ -880,6 +881,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t kdesc0 = sdesc_sw128(sbase + kOffK, 16, 1024);
             const uint64_t qdesc0 = sdesc_sw128(sbase + kOffQs, 16, 1024);
             const bool leader = elect_one_in_warp();
+            // Straight-line MMAs issue at the pace of the instruction fetch, loops over blocks of 64 dims faster once they
+            // have run: 1.03 -> 0.99 ms for 2 chunks of 256 tokens x 64 heads. The sparse decode's few tiles a pair gain
+            // nothing from that (32 rows x 128 heads: 1008 against 1033 K tokens/s).
             bool ok = wait_peer(ctl, &ctl->qready, 0, a.status);
             for (int i = 0; i < n_tiles && ok; ++i) {
                 ok = wait_peer(ctl, &ctl->kfull_a, i & 1, a.status);
@@ -888,11 +892,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after_sync();
                 const uint32_t d = tmem + kColS;
                 if (leader) {
+                    if constexpr (kPaged) {
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b)   // dims 0-255: q from tensor memory
 #pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)   // dims 0-255: q from tensor memory
-                        mma_ts_cg2(d, tmem + kColQ + 8 * kk,
-                                   kdesc0 + static_cast<uint64_t>(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), idesc_f16,
-                                   kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts_cg2(d, tmem + kColQ + 32 * b + 8 * kk, kdesc0 + static_cast<uint64_t>((b * kBlk + kk * 32) >> 4), idesc_f16,
+                                           (b | kk) != 0 ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk)
+                            mma_ts_cg2(d, tmem + kColQ + 8 * kk,
+                                       kdesc0 + static_cast<uint64_t>(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), idesc_f16,
+                                       kk > 0 ? 1u : 0u);
+                    }
                     mma_commit_cg2(&ctl->khalf, 0x3u << pb);
                 }
                 __syncwarp();
@@ -900,14 +913,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (leader) {
+                    if constexpr (kPaged) {
+                        static_assert(kQTmemSteps == 24, "dims 256-383 from tensor memory, the others from shared memory");
+#pragma unroll 1
+                        for (int b = 4; b < 6; ++b)
 #pragma unroll
-                    for (int kk = 16; kk < 36; ++kk) {
-                        const uint64_t kd = kdesc0 + static_cast<uint64_t>(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
-                        if (kk < kQTmemSteps)
-                            mma_ts_cg2(d, tmem + kColQ + 8 * kk, kd, idesc_f16, 1u);
-                        else
-                            mma_ss_cg2(d, qdesc0 + static_cast<uint64_t>((((kk - 24) >> 2) * kBlk + (kk & 3) * 32) >> 4),
-                                       kd, kk >= 32 ? idesc_rope : idesc_f16, 1u);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts_cg2(d, tmem + kColQ + 32 * b + 8 * kk, kdesc0 + static_cast<uint64_t>((b * kBlk + kk * 32) >> 4), idesc_f16, 1u);
+#pragma unroll 1
+                        for (int b = 6; b < 9; ++b)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss_cg2(d, qdesc0 + static_cast<uint64_t>(((b - 6) * kBlk + kk * 32) >> 4),
+                                           kdesc0 + static_cast<uint64_t>((b * kBlk + kk * 32) >> 4), b == 8 ? idesc_rope : idesc_f16, 1u);
+                    } else {
+#pragma unroll
+                        for (int kk = 16; kk < 36; ++kk) {
+                            const uint64_t kd = kdesc0 + static_cast<uint64_t>(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
+                            if (kk < kQTmemSteps)
+                                mma_ts_cg2(d, tmem + kColQ + 8 * kk, kd, idesc_f16, 1u);
+                            else
+                                mma_ss_cg2(d, qdesc0 + static_cast<uint64_t>((((kk - 24) >> 2) * kBlk + (kk & 3) * 32) >> 4),
+                                           kd, kk >= 32 ? idesc_rope : idesc_f16, 1u);
+                        }
                     }
                     mma_commit_cg2(&ctl->qkdone, 0x3u << pb);
                 }
