@@ -368,6 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_tiles = seg.tiles;
     }
     cluster_arrive();
+    if ((!kPaged || n_tiles > 0) && threadIdx.x == 0) {   // this CTA's q (this CTA's barrier and memory only)
+        mbar_arrive_expect_tx(&ctl->qload, 9u * kBlk);
+        for (int bx = 0; bx < 9; ++bx)
+            tma_load_2d(sbase + kOffV + bx * kBlk, &a.qmap, 64 * bx,
+                        kPaged ? seg.seq * a.jobs.rows_per_seq + seg.row0 + 64 * crank : row * 128 + 64 * crank, &ctl->qload);
+    }
+    __syncwarp();
     cluster_wait();   // both CTAs' barriers exist before any remote access
 
     if (!kPaged || n_tiles > 0) {   // (kPaged: the same in both CTAs)
@@ -384,17 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = ((qd >> 1) << 2) | g;                        // 0..7 among the head's threads
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * qd) << 16);
         float* xmax = reinterpret_cast<float*>(smem + kOffXmax);
-        if (threadIdx.x == 0) {
-            mbar_arrive_expect_tx(&ctl->qload, 9u * kBlk);
-            for (int bx = 0; bx < 9; ++bx)
-                tma_load_2d(sbase + kOffV + bx * kBlk, &a.qmap, 64 * bx,
-                            kPaged ? seg.seq * a.jobs.rows_per_seq + seg.row0 + 64 * crank : row * 128 + 64 * crank, &ctl->qload);
-        }
+        // kPaged: the page of a key of the first two tiles (see the softmax), in flight beside q
+        const int key = key_begin + static_cast<int>(threadIdx.x) - 32 * kWarpV;
+        const bool looks = kPaged && warp >= kWarpV && key < key_end;
+        const int32_t page = looks ? __ldg(a.jobs.page_table + seg.seq * a.jobs.table_stride + (key >> a.jobs.page_shift)) : 0;
         const bool okq = wait_warp(ctl, &ctl->qload, 0, a.status);
         const uint32_t stage = sbase + kOffV;   // box b (dims 64b..): head hl chunk c at b*8192 + swz(hl, c)
         float qmax = 0.0f;
         if (okq) {
-#pragma unroll 3
+#pragma unroll
             for (int k = 9 * slot; k < 9 * slot + 9; ++k) {   // 72 chunks of 8 dims per head, 9 per thread
                 const uint4 x = lds_u128(stage + (k >> 3) * kBlk + swz(hl, k & 7));
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -404,10 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         xmax[slot * 64 + hl] = qmax;
-        if (kPaged && warp >= kWarpV) {   // the keys of the first two tiles (see the softmax)
-            const int key = key_begin + static_cast<int>(threadIdx.x) - 32 * kWarpV;
-            if (paged::slot_of(a.jobs, seg.seq, key_end, key) == -2) ctl->outside = 1u;
-        }
+        if (looks && static_cast<unsigned>(page) >= static_cast<unsigned>(a.jobs.num_pages)) ctl->outside = 1u;
         named_bar_sync(2, 512);
 #pragma unroll
         for (int k = 0; k < 8; ++k) qmax = fmaxf(qmax, xmax[k * 64 + hl]);
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // dims [384, 576) = chunks 48..71 into shared memory (one copy, lanes 0-63): 6 chunks per warp
             if (qd < 2) {
-#pragma unroll 2
+#pragma unroll 3
                 for (int cc = 0; cc < 6; ++cc) {
                     const int k = 48 + 6 * g + cc;
                     const bool bf = R == 432 && k >= 64;   // bf16 RoPE of 432-byte records
