@@ -276,8 +276,8 @@ NVFP4_MLA_API int nvfp4_sparse_mla_decode_no_alloc(const void* q, const uint8_t*
 
 /*
  * Scratch size of nvfp4_paged_mla_decode (host-only, no CUDA call; the same on every device): the
- * parts of query rows whose keys were read by several CTAs. Up to 32 rows per sequence
- * (s_q * h_q) it depends on their number only, beyond that also on batch.
+ * parts of query rows whose keys were read by several CTAs, and a plan. One size for up to 16 rows per
+ * sequence (s_q * h_q); above that it grows with batch and with s_q * h_q.
  */
 NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s_q, int32_t h_q, size_t* bytes);
 

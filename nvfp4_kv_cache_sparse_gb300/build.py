@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libnvfp4mla.so")
 SOURCES = ["api.cu", "quantize_append.cu", "sparse_decode.cu", "sparse_decode_pair.cu", "sparse_decode_h64.cu",
-           "decode_no_alloc.cu", "paged_decode.cu", "paged_decode_n16.cu", "paged_decode_n32.cu", "paged_decode_pair.cu",
+           "decode_no_alloc.cu", "paged_decode.cu", "paged_decode_few.cu", "paged_decode_pair.cu",
            "page_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

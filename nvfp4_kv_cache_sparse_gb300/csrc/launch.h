@@ -97,13 +97,12 @@ struct PagedDecodeArgs {
     uint32_t* dev_status;
 };
 constexpr int kPagedMaxSms = 160;                // no sm_103 device has more SMs
-int paged_row_tile(int64_t rows_per_seq);        // query rows that share dequantized keys: 16, 32 (one CTA) or 128 (a pair)
+int paged_row_tile(int64_t rows_per_seq);        // query rows that share dequantized keys: 16 (one CTA) or 128 (a pair)
 size_t paged_workspace_bytes(int64_t batch, int64_t rows_per_seq);
 int64_t paged_max_segments(int64_t jobs, int pairs);
 cudaError_t launch_paged_decode(PagedDecodeArgs d, void* workspace, int sms, cudaStream_t stream);
 int paged_pairs(int sms);
-cudaError_t launch_paged_decode_n16(const PagedDecodeArgs& d, cudaStream_t stream);
-cudaError_t launch_paged_decode_n32(const PagedDecodeArgs& d, cudaStream_t stream);
+cudaError_t launch_paged_decode_few(const PagedDecodeArgs& d, cudaStream_t stream);
 cudaError_t launch_paged_decode_pair(const PagedDecodeArgs& d, int max_segments, int headers, cudaStream_t stream);
 
 // ---- operations on pages (page_ops.cu)

@@ -1,5 +1,5 @@
-// paged_decode.cuh -- attention of each query over all tokens of its own sequence, read from NVFP4
-// records (352 or 432 bytes) through a page table.
+// paged_decode_few.cu -- attention of each query over all tokens of its own sequence, read from NVFP4
+// records (352 or 432 bytes) through a page table, for up to 16 query rows (tokens x heads) of a sequence.
 //
 // What is computed. Sequence b has n = seq_lens[b] tokens; token p lies in slot
 // page_table[b, p / page_size] * page_size + p % page_size. Its s_q queries are its last s_q tokens:
@@ -7,40 +7,45 @@
 //     z_j = sm_scale * q[b,i,h,:] . K_j,   out = sum_j e^{z_j} V_j / (sum_j e^{z_j} + e^{sink_h}),
 //     lse = ln sum_j e^{z_j},              V_j = K_j[0:512]
 //
-// Work split. N query rows of a sequence (16 or 32: the kernel's row tile) share every key that is
-// dequantized; the tiles of 64 keys of all such jobs are cut into equal runs, one per CTA (one CTA per
-// SM; paged_jobs.cuh). A job that lies in one run is finished by its CTA; the parts of a job that was cut
-// go to the workspace (at most two per CTA, f16 outputs divided by their own sums, fp32 log-sum-exps)
-// and a second kernel joins them.
+// Work split. The rows of a sequence (a job) share every key that is dequantized; the tiles of 64 keys of all
+// jobs are cut into equal runs, one per CTA (one CTA per SM; paged_jobs.cuh). A job that lies in one run is
+// finished by its CTA; the parts of a job that was cut go to the workspace (at most two per CTA, f16
+// outputs divided by their own sums, fp32 log-sum-exps) and a second kernel joins them.
 //
 // Contractions. As keys outnumber rows, both products have the keys or the value dims on the MMA's M
-// side: S^T [64 keys x N] = K Q^T and O^T [512 dims x N] += V^T P^T (four M = 128 MMAs per 16
+// side: S^T [64 keys x 16] = K Q^T and O^T [512 dims x 16] += V^T P^T (four M = 128 MMAs per 16
 // keys). A record is dequantized once, into f16 (exact: an e2m1 x e4m3 product has few bits), and
 // read twice: K-major as K, MN-major as V^T. Queries are f16 times a power of two per row (exact
 // within 2^28 of the row's largest), scores fp32, P f16.
 //
 // Pipeline. Shared memory holds a ring of kRing blocks (64 keys x 128 dims, 16 KB), two tiles and more:
 // a block is filled by the converters, read by the QK MMAs, and freed by the PV MMAs of its tile.
-// The conversion of one tile, the softmax of another and the MMAs of both run side by side (two
-// score buffers, two P buffers; QK and PV are issued by a warp each). Tiles of 64 keys, not 128: what a CTA can have in flight is
-// bounded by shared memory, and a tile of 128 keys (128 KB) left the ring half empty while its
-// softmax ran (16 rows, 352-byte records: 3.5 us per 128 keys with a ring of 1.5 such tiles).
+// The conversion of one tile, the softmax of two others and the MMAs of all run side by side (two
+// score buffers, two P buffers; QK and PV are issued by a thread each). Tiles of 64 keys, not 128: what a
+// CTA can have in flight is bounded by shared memory, and a tile of 128 keys (128 KB) left the ring half
+// empty while its softmax ran (3.5 us per 128 keys with a ring of 1.5 such tiles).
 //
 // Softmax. A lazy reference maximum per row (log2 domain): P = 2^(z - m); a tile moves m only where
-// some score exceeds m + 8: the warps vote once per tile, and only then is O^T rescaled. The scores of
-// an M = 64 MMA lie in 16 lanes of each lane quadrant; 16x256b loads spread them over the warp, two
-// keys and a quarter of the columns a thread. Row sums stay in fp32 registers (a thread's share of its
-// columns) and are added up at the end of a job.
+// some score exceeds m + 8: the warps vote once per tile, and only then is O^T rescaled. A tile's softmax
+// is a chain of short waits (2900 to 3800 clk from its scores to the next tile's, against 1500 of MMAs), so
+// two groups of four warps take the even and the odd tiles; only the vote, from reading m to having moved
+// it, goes in the tiles' order (242 -> 223 us for 64 sequences x 16 heads). The scores of an M = 64 MMA lie in
+// 16 lanes of each lane quadrant; 16x256b loads spread them over the warp, two keys and four rows a thread.
+// Row sums stay in fp32 registers (a thread's share of its rows) and are added up at the end of a job.
 //
 // Masks. A key behind the sequence's end or in a page outside the pool gets a zero row in shared memory
 // (V and K share it, and 0 x NaN in PV would reach rows that do not see the key), a block of dims
 // with a NaN scale likewise; P is 0 for a key that a row does not see and NaN for a NaN key that it
 // sees.
 //
+// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 187 us, 2.0 TB/s, where
+// the records alone take 56 us. A tile takes about 2700 clk: the converters' chain of waits, loads and 18
+// stores of 512 bytes (STS 43%, MMA operands 41% of the shared memory's cycles; issue slots 48%; DRAM 28%).
+// What it costs to have one f16 tile for both products, 2 x 64 KB written and read for 22 KB of records, is
+// what keeps it from the memory's rate.
+//
 // Every wait is bounded by time; on timeout the CTA sets NVFP4_MLA_DEV_TIMEOUT, stops issuing work,
 // drains what it issued and returns.
-#pragma once
-
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -57,6 +62,7 @@
 namespace nvfp4mla {
 namespace paged {
 
+constexpr int kRows = 16;                  // query rows of a job (N of both products)
 constexpr int kTile = 64;                  // keys per tile (M of the QK MMAs)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -67,11 +73,11 @@ constexpr int kBlk = 16384;                // 64 keys x 128 dims
 constexpr int kAhead = 8;                  // tiles whose keys' slots are looked up ahead
 constexpr int kLook = 2;                   // of them at a time
 // Shared memory (offsets from a 1024-byte aligned base)
-constexpr int kOffCM = 512;                // float [N/2][4]: per row pair {ch_a, ch_b, -m_a, -m_b}: the score scale
+constexpr int kOffCM = 512;                // float [8][4]: per row pair {ch_a, ch_b, -m_a, -m_b}: the score scale
                                            // sm_scale log2(e) 2^-pre and the negated reference maximum
-constexpr int kOffAlpha = 1024;            // float [N]: rescale factors, then 1 / l
-constexpr int kOffXmax = 1280;             // float [N][8]: per-row values of the four key quadrants, of two groups
-constexpr int kOffPos = 2304;              // int [N]: each row's position (its last visible key)
+constexpr int kOffAlpha = 1024;            // float [kRows]: rescale factors, then 1 / l
+constexpr int kOffXmax = 1280;             // float [kRows][8]: per-row values of the four key quadrants, of two groups
+constexpr int kOffPos = 2304;              // int [kRows]: each row's position (its last visible key)
 constexpr int kOffNan = 2560;              // uint8 [4][2][64]: keys with a NaN scale, by tile and converter group
 constexpr int kOffScan = 3072;             // int64 [32]
 constexpr int kOffTile = 3328;             // int4 [kAhead]: first key position, row 0's position, 2 x (tiles left of the
@@ -80,27 +86,23 @@ constexpr int kOffSlot = 3456;             // int [kAhead][64]: the keys' slots;
 constexpr int kOffQ = 6144;
 static_assert(kOffSlot + kAhead * kTile * 4 <= kOffQ, "control area");
 
-template <int N>
-struct Shape {
-    static constexpr int kSoft = 8;                      // softmax warps: two groups of four, even and odd tiles
-    static constexpr int kConv = 16;                     // converter warps: two groups, even and odd blocks
-    static constexpr int kThreads = 32 * (kSoft + kConv + 3);   // and two MMA issuers and the look-up warp
-    static constexpr int kRing = N == 16 ? 10 : 9;
-    static constexpr int kRopeRing = 3;                      // tiles whose RoPE dims are held (see the converters)
-    // tensor memory columns: O^T four blocks, two score buffers
-    static constexpr uint32_t kColO = 0, kColS = 4 * N;
-    static constexpr int kTmemCols = N == 16 ? 128 : 256;
-    static_assert(6 * N <= kTmemCols, "tensor memory");
-    static constexpr int kQBlk = N * 128;                // N rows x 64 dims
-    static constexpr int kOffK = kOffQ + 9 * kQBlk;
-    static constexpr int kOffRope = kOffK + kRing * kBlk;
-    static constexpr int kOffP = kOffRope + kRopeRing * kSubBlk;
-    static constexpr int kPBytes = N * 128;              // P of a tile: 64 keys x N rows
-    static constexpr int kSmemBytes = kOffP + 2 * kPBytes;
-    static constexpr int kSmemAlloc = kSmemBytes + 1024;
-    static_assert(kSmemAlloc <= 232448, "shared memory");
-    static_assert(kOffQ % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
-};
+constexpr int kSoft = 8;                   // softmax warps: two groups of four, even and odd tiles
+constexpr int kConv = 16;                  // converter warps: two groups, even and odd blocks
+constexpr int kThreads = 32 * (kSoft + kConv + 3);   // and two MMA issuers and the look-up warp
+constexpr int kRing = 10;
+constexpr int kRopeRing = 3;               // tiles whose RoPE dims are held (see the converters)
+// tensor memory columns: O^T four blocks, two score buffers
+constexpr uint32_t kColO = 0, kColS = 4 * kRows;
+constexpr int kTmemCols = 128;
+static_assert(6 * kRows <= kTmemCols, "tensor memory");
+constexpr int kQBlk = kRows * 128;         // rows x 64 dims
+constexpr int kOffK = kOffQ + 9 * kQBlk;
+constexpr int kOffRope = kOffK + kRing * kBlk;
+constexpr int kOffP = kOffRope + kRopeRing * kSubBlk;
+constexpr int kPBytes = kRows * 128;       // P of a tile: 64 keys x rows
+constexpr int kSmemAlloc = kOffP + 2 * kPBytes + 1024;
+static_assert(kSmemAlloc <= 232448, "shared memory");
+static_assert(kOffQ % 1024 == 0 && kOffK % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
 
 struct __align__(8) Ctl {
     uint64_t qload;           // q boxes landed (TMA, tx-counted)
@@ -120,22 +122,21 @@ struct __align__(8) Ctl {
 static_assert(sizeof(Ctl) <= kOffCM, "control block");
 
 struct KernelArgs {
-    CUtensorMap qmap;         // q as bf16 [batch * s_q * h_q, 576], box 64 dims x N rows, 128B swizzle
+    CUtensorMap qmap;         // q as bf16 [batch * s_q * h_q, 576], box 64 dims x kRows rows, 128B swizzle
     const uint8_t* cache;
     Jobs jobs;
     float sm_scale;
     const float* sink;
     __nv_bfloat16* out;       // [batch * rows_per_seq, 512]
     float* lse;
-    uint16_t* part_out;       // f16 [2 * CTAs, N, 512]
-    float* part_lse;          // [2 * CTAs, N], log2 domain
+    uint16_t* part_out;       // f16 [2 * CTAs, kRows, 512]
+    float* part_lse;          // [2 * CTAs, kRows], log2 domain
     int4* hdr;                // [CTAs]: the cut job that begins in the CTA's run: first output row, rows
                               // (0: none), parts, slot of the first part (the others: 2 (CTA + 1), 2 (CTA + 2), ...)
     uint32_t* status;
 };
 
 // A position in the run of tiles of a CTA.
-template <int N>
 struct Walk {
     Job j;
     int job, t, left;         // tile t of the job; tiles left in the run, this one included
@@ -143,7 +144,7 @@ struct Walk {
         job = job0;
         t = tile0;
         left = count;
-        j = job_info<N, kTile>(a, job);
+        j = job_info<kRows, kTile>(a, job);
     }
     __device__ __forceinline__ void next(const Jobs& a) {
         if (left <= 1) {
@@ -152,7 +153,7 @@ struct Walk {
         }
         --left;
         if (++t < j.tiles) return;
-        do j = job_info<N, kTile>(a, ++job);
+        do j = job_info<kRows, kTile>(a, ++job);
         while (j.tiles == 0);
         t = 0;
     }
@@ -218,21 +219,12 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
     return v;
 }
 __device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
-// 16 lanes x 8 kGroups consecutive 32-bit columns over the warp: thread t gets, for each group of eight
+// 16 lanes x 16 consecutive 32-bit columns over the warp: thread t gets, for each group of eight
 // columns, columns 2 (t & 3), 2 (t & 3) + 1 of lane t >> 2 and of lane (t >> 2) + 8.
-template <int kGroups>
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[4 * kGroups]) {
-    static_assert(kGroups == 2 || kGroups == 4, "");
-    if constexpr (kGroups == 2)
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr));
-    else
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 __device__ __forceinline__ uint32_t ldg_stream2(const void* p) {
     uint16_t r;
@@ -301,11 +293,10 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) 
 // Whether one of the four bytes is an e4m3 NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool has_nan_e4m3(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u; }
 
-template <int R, bool kBlkOrder, int N>
-__global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ KernelArgs a) {
-    using S = Shape<N>;
-    constexpr int kSoftThreads = 32 * S::kSoft, kGroupWarps = 4, kGroupThreads = 128;
-    constexpr int kWarpQk = S::kSoft + S::kConv, kWarpPv = kWarpQk + 1, kWarpLook = kWarpQk + 2;
+template <int R, bool kBlkOrder>
+__global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_constant__ KernelArgs a) {
+    constexpr int kSoftThreads = 32 * kSoft, kGroupWarps = 4, kGroupThreads = 128;
+    constexpr int kWarpQk = kSoft + kConv, kWarpLook = kWarpQk + 2;   // the PV issuer between them
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Ctl* ctl = reinterpret_cast<Ctl*>(smem);
@@ -316,8 +307,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     if (threadIdx.x == 0) {
         mbar_init(&ctl->qload, 1);
         mbar_init(&ctl->qready, kGroupWarps);
-        for (int s = 0; s < 4; ++s) mbar_init(&ctl->kfull[s], S::kConv);
-        for (int s = 0; s < S::kRing; ++s) mbar_init(&ctl->kfree[s], 1);
+        for (int s = 0; s < 4; ++s) mbar_init(&ctl->kfull[s], kConv);
+        for (int s = 0; s < kRing; ++s) mbar_init(&ctl->kfree[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->sfull[s], 1);
             mbar_init(&ctl->pfull[s], kGroupWarps);
@@ -325,14 +316,14 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         }
         for (int s = 0; s < kAhead; ++s) {
             mbar_init(&ctl->tfull[s], 1);
-            mbar_init(&ctl->tfree[s], kGroupWarps + S::kConv);
+            mbar_init(&ctl->tfree[s], kGroupWarps + kConv);
         }
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
         fence_barrier_init();
     }
     if (warp == kWarpQk) {
-        tmem_alloc(&ctl->tmem_base, S::kTmemCols);
+        tmem_alloc(&ctl->tmem_base, kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -344,25 +335,25 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    const Run run = find_run<N, kTile, S::kThreads>(a.jobs, reinterpret_cast<int64_t*>(smem + kOffScan), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
+    const Run run = find_run<kRows, kTile, kThreads>(a.jobs, reinterpret_cast<int64_t*>(smem + kOffScan), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
     const int count = run.count;
-    write_empty_jobs<N, kTile, S::kThreads>(a.jobs, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), a.out, a.lse);
-    if (blockIdx.x == 0) check_lengths(a.jobs, static_cast<int>(threadIdx.x), S::kThreads, a.status);
+    write_empty_jobs<kRows, kTile, kThreads>(a.jobs, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), a.out, a.lse);
+    if (blockIdx.x == 0) check_lengths(a.jobs, static_cast<int>(threadIdx.x), kThreads, a.status);
     if (threadIdx.x == 0 && count == 0) a.hdr[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     if (count == 0) {
         // nothing to do in this CTA
-    } else if (warp < S::kSoft) {
+    } else if (warp < kSoft) {
         // ======================= softmax warps: two groups of four, group g the tiles of parity g =======================
-        constexpr int kGroups = N / 8;        // groups of eight rows
+        constexpr int kGroups = kRows / 8;        // groups of eight rows
         const int grp = warp >> 2;
         const int qd = warp & 3;              // TMEM lane quadrant: keys 16 qd .. 16 qd + 15 of a tile, and 128 dims' share of O^T
         const int k0 = 16 * qd + (lane >> 2); // this thread's keys: k0 and k0 + 8; its rows: c0 + 8g, c0 + 8g + 1
         const int c0 = 2 * (lane & 3);
         const uint32_t bar_grp = 1u + static_cast<uint32_t>(grp), bar_all = 3u;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * qd) << 16);
-        const uint32_t s_col = lane_base + S::kColS + N * grp;
-        const uint32_t p_s = sbase + S::kOffP + S::kPBytes * grp;
+        const uint32_t s_col = lane_base + kColS + kRows * grp;
+        const uint32_t p_s = sbase + kOffP + kPBytes * grp;
         const uint32_t cm_s = sbase + kOffCM;
         const uint32_t alpha_s = sbase + kOffAlpha;
         const uint32_t xmax_s = sbase + kOffXmax;
@@ -371,19 +362,20 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         auto negm_addr = [&](int r) { return cm_s + 16 * (r >> 1) + 8 + 4 * (r & 1); };
 
         bool ok = true;
-        // q of a job: rows row0 .. row0 + N - 1 of its sequence (thread 0); rows behind the job's last one are the
+        // q of a job: rows row0 .. row0 + kRows - 1 of its sequence (thread 0); rows behind the job's last one are the
         // next sequence or zeros, and reach columns that nothing reads
         auto load_q = [&](const Job& j) {
-            mbar_arrive_expect_tx(&ctl->qload, 9u * S::kQBlk);
+            mbar_arrive_expect_tx(&ctl->qload, 9u * kQBlk);
             for (int bx = 0; bx < 9; ++bx)
-                tma_load_2d(sbase + kOffQ + bx * S::kQBlk, &a.qmap, 64 * bx, j.seq * a.jobs.rows_per_seq + j.row0, &ctl->qload);
+                tma_load_2d(sbase + kOffQ + bx * kQBlk, &a.qmap, 64 * bx, j.seq * a.jobs.rows_per_seq + j.row0, &ctl->qload);
         };
         // group 0: per-row prescale and f16 (bf16 RoPE for 432-byte records) in place; the rows' scales and positions
         auto stage_q = [&](const Job& j, int seg) {
-            constexpr int kTpr = kGroupThreads / N, kPer = 8 / kTpr;   // threads of a row; blocks of 64 dims, and chunks of 8 RoPE dims, of a thread
+            constexpr int kTpr = kGroupThreads / kRows;   // threads of a row: each a block of 64 dims and a chunk of 8 RoPE dims
+            static_assert(kTpr == 8, "a thread per block");
             if (ok) ok = wait_warp(ctl, &ctl->qload, seg & 1, a.status);
             const int r = threadIdx.x / kTpr, part = threadIdx.x % kTpr;
-            auto chunk_at = [&](int bx, int c) { return sbase + kOffQ + bx * S::kQBlk + swz(r, c); };
+            auto chunk_at = [&](int bx, int c) { return sbase + kOffQ + bx * kQBlk + swz(r, c); };
             float qmax = 0.0f;
             auto take_max = [&](uint4 x) {
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -392,12 +384,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     qmax = fmax3(qmax, fabsf(__uint_as_float(w[m] << 16)), fabsf(__uint_as_float(w[m] & 0xFFFF0000u)));
             };
             if (ok) {
-#pragma unroll 1
-                for (int m = 0; m < kPer; ++m) {
 #pragma unroll 4
-                    for (int i = 0; i < 8; ++i) take_max(lds_u128(chunk_at(part + kTpr * m, (i + part) & 7)));
-                    take_max(lds_u128(chunk_at(8, part + kTpr * m)));
-                }
+                for (int i = 0; i < 8; ++i) take_max(lds_u128(chunk_at(part, (i + part) & 7)));
+                take_max(lds_u128(chunk_at(8, part)));
             }
 #pragma unroll
             for (int o = 1; o < kTpr; o <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
@@ -426,29 +415,25 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             };
             if (ok) {
                 // (odd blocks with the chunks of each pair swapped, as the converters store K)
-#pragma unroll 1
-                for (int m = 0; m < kPer; ++m) {
-                    const int bx = part + kTpr * m;
 #pragma unroll 2
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = 2 * ((i + part) & 3);
-                        const uint4 x = lds_u128(chunk_at(bx, c)), y = lds_u128(chunk_at(bx, c + 1));
-                        sts_u128(chunk_at(bx, c ^ (bx & 1)), scaled(x, false));
-                        sts_u128(chunk_at(bx, (c + 1) ^ (bx & 1)), scaled(y, false));
-                    }
-                    const int c = part + kTpr * m;   // RoPE chunks 1 and 2 of four are swapped (the threads of four lie in one warp)
-                    const uint4 x = scaled(lds_u128(chunk_at(8, c)), R == 432);   // bf16 RoPE of 432-byte records
-                    __syncwarp();
-                    sts_u128(chunk_at(8, (c & 4) | ((c & 1) << 1) | ((c >> 1) & 1)), x);
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 2 * ((i + part) & 3);
+                    const uint4 x = lds_u128(chunk_at(part, c)), y = lds_u128(chunk_at(part, c + 1));
+                    sts_u128(chunk_at(part, c ^ (part & 1)), scaled(x, false));
+                    sts_u128(chunk_at(part, (c + 1) ^ (part & 1)), scaled(y, false));
                 }
+                // RoPE chunks 1 and 2 of four are swapped (the threads of a row lie in one warp); bf16 for 432-byte records
+                const uint4 x = scaled(lds_u128(chunk_at(8, part)), R == 432);
+                __syncwarp();
+                sts_u128(chunk_at(8, (part & 4) | ((part & 1) << 1) | ((part >> 1) & 1)), x);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->qready);
         };
 
-        if (threadIdx.x == 0) load_q(job_info<N, kTile>(a.jobs, run.job));
-        float l[kGroups][2], lnm[kGroups][2];  // this thread's share of its rows' sums of 2^(z - m), and the -m that they are for
+        if (threadIdx.x == 0) load_q(job_info<kRows, kTile>(a.jobs, run.job));
+        float l[kGroups][2] = {}, lnm[kGroups][2] = {};  // this thread's share of its rows' sums of 2^(z - m), and the -m that they are for
         int4 hdr = make_int4(0, 0, 0, 0);
         int seg = 0;
         // the sums for references that have moved since (also by the other group)
@@ -470,7 +455,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         for (int s0 = 0; s0 < count; ++seg) {
             if (ok) ok = wait_warp(ctl, &ctl->tfull[s0 % kAhead], (s0 / kAhead) & 1, a.status);
             const uint4 head = ok ? lds_u128(sbase + kOffTile + 16 * (s0 % kAhead)) : make_uint4(0u, 0u, 2u, static_cast<uint32_t>(run.job));
-            const Job j = job_info<N, kTile>(a.jobs, static_cast<int>(head.w));
+            const Job j = job_info<kRows, kTile>(a.jobs, static_cast<int>(head.w));
             const int s1 = s0 + static_cast<int>(head.z >> 1);
             const int seg_tile = static_cast<int>(head.x) / kTile;
             if (grp == 0) stage_q(j, seg);
@@ -531,7 +516,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 uint32_t nan0 = 0u, nan1 = 0u;
                 if (ok && it >= 2) {   // the PV that read this P buffer
                     const int g = 4 * it - 5;
-                    ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                    ok = wait_warp(ctl, &ctl->kfree[g % kRing], (g / kRing) & 1, a.status);
                 }
                 // the other group's tile before this one has its references
                 if (ok && it > s0) ok = wait_warp(ctl, &ctl->voted[grp ^ 1], ((it - 1) >> 1) & 1, a.status);
@@ -539,7 +524,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 if (ok) {
                     if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
                     tc_fence_after_sync();
-                    tmem_ld_16x256<kGroups>(s_col, sv);
+                    tmem_ld_16x256_x2(s_col, sv);
                     // (the scores' MMAs were issued behind the waits for the blocks that the flags were written before)
                     const uint32_t nan_s = sbase + kOffNan + 128 * (it & 3) + k0;
                     nan0 = lds_u8(nan_s) | lds_u8(nan_s + 64);
@@ -553,7 +538,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     // O^T stands still once the PV of the tile before has completed
                     if (ok && it > s0) {
                         const int g = 4 * it - 1;
-                        ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                        ok = wait_warp(ctl, &ctl->kfree[g % kRing], (g / kRing) & 1, a.status);
                         tc_fence_after_sync();
                     }
                     if (bar_red_or(bar_grp, kGroupThreads, !ok)) {
@@ -576,7 +561,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                             if (lane < 4) sts_f32(xmax_s + 32 * r + 4 * qd, m);
                         }
                     named_bar_sync(bar_grp, kGroupThreads);
-                    if (qd == 0 && lane < N) {   // one thread per row: the new reference and the rescale factor
+                    if (qd == 0 && lane < kRows) {   // one thread per row: the new reference and the rescale factor
                         const uint4 x = lds_u128(xmax_s + 32 * lane);
                         const float zt = fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
                                                fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
@@ -592,16 +577,13 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     if (it > s0) {
                         // O^T (this warp's 32 lanes of each block of dims) *= alpha
 #pragma unroll 1
-                        for (int c = 0; c < 4 * (N / 16); ++c) {
-                            const int r0 = 16 * (c % (N / 16));
-                            const uint32_t col = lane_base + S::kColO + N * (c / (N / 16)) + r0;
-                            uint32_t o[16];
-                            tmem_ld16(col, o);
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t o[kRows];
+                            tmem_ld16(lane_base + kColO + kRows * b, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha_s + 4 * (r0 + e)));
-                            tmem_st16(col, o);
+                            for (int e = 0; e < kRows; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha_s + 4 * e));
+                            tmem_st16(lane_base + kColO + kRows * b, o);
                         }
                         tmem_wait_st();
                     }
@@ -646,13 +628,13 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             const int t_end = seg_tile + s1 - s0 - 1;
             if (ok) {
                 const int g = 4 * s1 - 1;
-                ok = wait_warp(ctl, &ctl->kfree[g % S::kRing], (g / S::kRing) & 1, a.status);
+                ok = wait_warp(ctl, &ctl->kfree[g % kRing], (g / kRing) & 1, a.status);
                 tc_fence_after_sync();
             }
             if (bar_red_or(bar_all, kSoftThreads, !ok)) break;   // the references are final, every QK of the segment has completed
             if (warp == 0 && s1 < count) {
                 ok = wait_warp(ctl, &ctl->tfull[s1 % kAhead], (s1 / kAhead) & 1, a.status);
-                if (ok && lane == 0) load_q(job_info<N, kTile>(a.jobs, static_cast<int>(lds_u32(sbase + kOffTile + 16 * (s1 % kAhead) + 12))));
+                if (ok && lane == 0) load_q(job_info<kRows, kTile>(a.jobs, static_cast<int>(lds_u32(sbase + kOffTile + 16 * (s1 % kAhead) + 12))));
                 __syncwarp();
             }
             const bool whole = seg_tile == 0 && t_end == j.tiles - 1;
@@ -671,7 +653,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 }
             }
             named_bar_sync(bar_all, kSoftThreads);
-            if (warp == 0 && lane < N) {
+            if (warp == 0 && lane < kRows) {
                 const int r = lane;
                 const uint4 x = lds_u128(xmax_s + 32 * r), y = lds_u128(xmax_s + 32 * r + 16);
                 const float sum = ((__uint_as_float(x.x) + __uint_as_float(x.y)) + (__uint_as_float(x.z) + __uint_as_float(x.w))) +
@@ -690,7 +672,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                     if (whole)
                         a.lse[row + r] = lse2 * kLn2;
                     else
-                        a.part_lse[static_cast<int64_t>(slot) * N + r] = lse2;
+                        a.part_lse[static_cast<int64_t>(slot) * kRows + r] = lse2;
                 }
             }
             named_bar_sync(bar_all, kSoftThreads);
@@ -698,18 +680,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             // the chunks of each pair swapped); a warp store covers 32 consecutive dims of one row (64 bytes)
             const int dim = 32 * qd + (qd >= 2 ? lane ^ 8 : lane);
             uint16_t* dst = whole ? reinterpret_cast<uint16_t*>(a.out) + row * 512
-                                  : a.part_out + static_cast<int64_t>(slot) * N * 512;
+                                  : a.part_out + static_cast<int64_t>(slot) * kRows * 512;
 #pragma unroll 1
-            for (int c = 0; c < 2 * (N / 16); ++c) {
-                const int b = 2 * grp + c / (N / 16), r0 = 16 * (c % (N / 16));
-                uint32_t o[16];
-                tmem_ld16(lane_base + S::kColO + N * b + r0, o);
+            for (int b = 2 * grp; b < 2 * grp + 2; ++b) {
+                uint32_t o[kRows];
+                tmem_ld16(lane_base + kColO + kRows * b, o);
                 tmem_wait_ld();
-                uint16_t* p = dst + static_cast<int64_t>(r0) * 512 + 128 * b + dim;
+                uint16_t* p = dst + 128 * b + dim;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    if (r0 + e < j.rows) {
-                        const float f = lds_f32(alpha_s + 4 * (r0 + e));
+                for (int e = 0; e < kRows; ++e) {
+                    if (e < j.rows) {
+                        const float f = lds_f32(alpha_s + 4 * e);
                         const float v = f != 0.0f ? __uint_as_float(o[e]) * f : 0.0f;
                         p[e * 512] = whole ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
                     }
@@ -728,8 +709,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         if (threadIdx.x == 0) a.hdr[blockIdx.x] = hdr;
     } else if (warp < kWarpQk) {
         // ============ converters: two groups of eight warps, group g the 128-dim blocks g and g + 2 ============
-        const int group = (warp - S::kSoft) >> 3;
-        const int t = (threadIdx.x - 32 * S::kSoft) & 255;
+        const int group = (warp - kSoft) >> 3;
+        const int t = (threadIdx.x - 32 * kSoft) & 255;
         // Lane l of a group's warp w: quarter q = l & 3 of key j, so that four lanes load one 64-byte run, and a quarter-warp
         // the runs of keys j and j + 2, which lie in different banks of the load's data stage: 6 of its cycles a load,
         // against 17.6 with the eight keys of a quarter-warp in lanes beside one another. Its eight stores go to
@@ -738,7 +719,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         const int j = 8 * (t >> 5) + ((t >> 3) & 1) + 2 * ((t >> 2) & 1) + 4 * ((t >> 4) & 1);
         const bool with_rope = (t >> 7) == group;     // group 0 the RoPE dims of keys 0-31, group 1 of keys 32-63
         // the thread's four chunks of a block are 16-byte slots x, x ^ 1, x ^ 2, x ^ 3 of row j of its half (128B swizzle)
-        const uint32_t store0 = sbase + S::kOffK + (q >> 1) * kSubBlk + 128 * j + (((4 * (q & 1)) ^ (q >> 1) ^ (j & 7)) << 4);
+        const uint32_t store0 = sbase + kOffK + (q >> 1) * kSubBlk + 128 * j + (((4 * (q & 1)) ^ (q >> 1) ^ (j & 7)) << 4);
         bool ok = true;
         HalfRecord<R, kBlkOrder> raw;
         auto slot_at = [&](int k) { return static_cast<int>(lds_u32(sbase + kOffSlot + 4 * kTile * (k % kAhead) + 4 * j)); };
@@ -765,7 +746,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         for (int k = 0; k < count && ok; ++k) {
             // the tile's three barriers are asked ahead of the work that does not need them
             const bool more = k + 2 < count;
-            const int slot1 = slot + 2 >= S::kRing ? slot + 2 - S::kRing : slot + 2, round1 = round + (slot + 2 >= S::kRing ? 1 : 0);
+            const int slot1 = slot + 2 >= kRing ? slot + 2 - kRing : slot + 2, round1 = round + (slot + 2 >= kRing ? 1 : 0);
             uint32_t ready = test_three(&ctl->kfree[slot], (round - 1) & 1, &ctl->kfree[slot1], (round1 - 1) & 1, tile_bar(k + 2), ((k + 2) / kAhead) & 1);
             if (round == 0) ready |= 1u;
             if (round1 == 0) ready |= 2u;
@@ -794,7 +775,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 // The RoPE dims go to the buffer of kRopeRing tiles ago: the PV commit that freed this group's first
                 // block of the tile (or, before the ring's first round, no tile at all) came behind that QK
                 if (i == 0 && with_rope) {
-                    const uint32_t rope = sbase + S::kOffRope + (k % S::kRopeRing) * kSubBlk;
+                    const uint32_t rope = sbase + kOffRope + (k % kRopeRing) * kSubBlk;
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     const int c = 4 * (q >> 1) + (q & 1);   // chunks 1 and 2 of four swapped, for eight bank slots here too
                     sts_u128(rope + swz(j, c), cur >= 0 ? raw.rope_values(0) : zero);
@@ -809,8 +790,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
             if (more && (ready & 4u) == 0u) ok = wait_warp(ctl, tile_bar(k + 2), ((k + 2) / kAhead) & 1, a.status);
             cur = nxt;
             nxt = more && ok ? slot_at(k + 2) : -1;
-            slot = slot1 + 2 >= S::kRing ? slot1 + 2 - S::kRing : slot1 + 2;
-            round = round1 + (slot1 + 2 >= S::kRing ? 1 : 0);
+            slot = slot1 + 2 >= kRing ? slot1 + 2 - kRing : slot1 + 2;
+            round = round1 + (slot1 + 2 >= kRing ? 1 : 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->kfull[k & 3]);
@@ -818,9 +799,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         }
     } else if (warp == kWarpLook) {
         // ============ look-up warp: the slots of the keys of every tile, and their records into L2 ============
-        // kLook tiles at a time: their loads from the page table are in flight together (one tile after the other, the
-        // loads' latency alone took 1.3 us a tile)
-        Walk<N> w;
+        // kLook tiles at a time: their loads from the page table are in flight together (64 sequences x 16 heads: 206 us
+        // with one tile at a time, 197 with two, 200 with four)
+        Walk w;
         w.start(a.jobs, run.job, run.tile, count);
         bool first = true, ok = true;
         for (int it0 = 0; it0 < count && ok; it0 += kLook) {
@@ -864,10 +845,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         }
     } else if (warp == kWarpQk) {
         // ======================= QK issuer: S^T = K Q^T =======================
-        const uint32_t idesc_qk = idesc_f16_f32(64, N, false, false);
-        const uint32_t idesc_rope = R == 432 ? idesc_bf16_f32(64, N, false, false) : idesc_qk;
-        const uint64_t kdesc0 = sdesc_sw128(sbase + S::kOffK, 16, 1024);          // K-major: keys x dims
-        const uint64_t rdesc0 = sdesc_sw128(sbase + S::kOffRope, 16, 1024);       // K-major: keys x RoPE dims
+        const uint32_t idesc_qk = idesc_f16_f32(64, kRows, false, false);
+        const uint32_t idesc_rope = R == 432 ? idesc_bf16_f32(64, kRows, false, false) : idesc_qk;
+        const uint64_t kdesc0 = sdesc_sw128(sbase + kOffK, 16, 1024);          // K-major: keys x dims
+        const uint64_t rdesc0 = sdesc_sw128(sbase + kOffRope, 16, 1024);       // K-major: keys x RoPE dims
         const uint64_t qdesc0 = sdesc_sw128(sbase + kOffQ, 16, 1024);             // K-major: rows x dims
         const bool leader = elect_one_in_warp();
         if (leader) {
@@ -887,21 +868,21 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 if (ok && !full) ok = wait_one(ctl, &ctl->kfull[it & 3], (it >> 2) & 1, a.status);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem + S::kColS + N * (it & 1);
+                const uint32_t d = tmem + kColS + kRows * (it & 1);
                 // (short loops: straight-line code of 36 MMAs runs at the pace of the instruction fetch, 50 to 60 clk
                 // an MMA against 25)
 #pragma unroll 3
                 for (int b = 0; b < 9; ++b) {   // 64 dims each, the RoPE dims last
                     const uint64_t kd = b < 8 ? kdesc0 + static_cast<uint64_t>((slot * kBlk + (b & 1) * kSubBlk) >> 4)
                                               : rdesc0 + static_cast<uint64_t>((rslot * kSubBlk) >> 4);
-                    const uint64_t qd = qdesc0 + static_cast<uint64_t>((b * S::kQBlk) >> 4);
+                    const uint64_t qd = qdesc0 + static_cast<uint64_t>((b * kQBlk) >> 4);
                     const uint32_t idesc = b < 8 ? idesc_qk : idesc_rope;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_ss(d, kd + static_cast<uint64_t>((kk * 32) >> 4), qd + static_cast<uint64_t>((kk * 32) >> 4), idesc, (b | kk) != 0 ? 1u : 0u);
-                    if ((b & 1) && ++slot == S::kRing) slot = 0;
+                    if ((b & 1) && ++slot == kRing) slot = 0;
                 }
-                if (++rslot == S::kRopeRing) rslot = 0;
+                if (++rslot == kRopeRing) rslot = 0;
                 mma_commit(&ctl->sfull[it & 1]);
             }
         }
@@ -912,9 +893,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
         __syncwarp();
     } else {
         // ======================= PV issuer: O^T += V^T P^T; the tile's ring blocks are free then =======================
-        const uint32_t idesc_pv = idesc_f16_f32(128, N, true, false);
-        const uint64_t vdesc0 = sdesc_sw128(sbase + S::kOffK, kSubBlk, 1024);     // MN-major: dims x keys
-        const uint64_t pdesc0 = sdesc_sw128(sbase + S::kOffP, 16, 1024);          // K-major: rows x keys
+        const uint32_t idesc_pv = idesc_f16_f32(128, kRows, true, false);
+        const uint64_t vdesc0 = sdesc_sw128(sbase + kOffK, kSubBlk, 1024);     // MN-major: dims x keys
+        const uint64_t pdesc0 = sdesc_sw128(sbase + kOffP, 16, 1024);          // K-major: rows x keys
         const bool leader = elect_one_in_warp();
         if (leader) {
             int slot = 0;
@@ -922,16 +903,16 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
                 if (!wait_one(ctl, &ctl->pfull[it & 1], (it >> 1) & 1, a.status)) break;
                 tc_fence_after_sync();
                 const bool first = *reinterpret_cast<volatile uint32_t*>(&ctl->pfirst[it & 1]) != 0u;
-                const uint64_t pd = pdesc0 + static_cast<uint64_t>((S::kPBytes * (it & 1)) >> 4);
+                const uint64_t pd = pdesc0 + static_cast<uint64_t>((kPBytes * (it & 1)) >> 4);
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     const uint64_t vd = vdesc0 + static_cast<uint64_t>((slot * kBlk) >> 4);
 #pragma unroll
                     for (int s = 0; s < 4; ++s)    // keys 16s .. 16s + 15
-                        mma_ss(tmem + S::kColO + N * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
+                        mma_ss(tmem + kColO + kRows * b, vd + static_cast<uint64_t>((s * 2048) >> 4),
                                pd + static_cast<uint64_t>((s * 32) >> 4), idesc_pv, (!first || s > 0) ? 1u : 0u);
                     mma_commit(&ctl->kfree[slot]);
-                    if (++slot == S::kRing) slot = 0;
+                    if (++slot == kRing) slot = 0;
                 }
             }
         }
@@ -946,7 +927,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1) paged_decode_kernel(con
     __syncthreads();
     if (warp == kWarpQk) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, S::kTmemCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -954,8 +935,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// q as bf16 [rows, 576], box 64 dims x N rows, 128B swizzle.
-template <int N>
+// q as bf16 [rows, 576], box 64 dims x kRows rows, 128B swizzle.
 bool encode_q_map(CUtensorMap* map, const void* q, int64_t rows) {
     static const EncodeTiledFn fn = [] {
         void* p = nullptr;
@@ -968,14 +948,14 @@ bool encode_q_map(CUtensorMap* map, const void* q, int64_t rows) {
     if (fn == nullptr || rows < 1 || rows > 0x7FFFFFFF) return false;
     const cuuint64_t dims[2] = {576u, static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {576u * 2u};
-    const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(N)};
+    const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(kRows)};
     const cuuint32_t elem_strides[2] = {1u, 1u};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims, strides, box, elem_strides,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int R, bool kBlkOrder, int N>
+template <int R, bool kBlkOrder>
 cudaError_t prepare_kernel() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -983,20 +963,21 @@ cudaError_t prepare_kernel() {
     if (err != cudaSuccess) return err;
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    err = cudaFuncSetAttribute(paged_decode_kernel<R, kBlkOrder, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmemAlloc);
+    err = cudaFuncSetAttribute(paged_decode_kernel<R, kBlkOrder>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
     if (err == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_relaxed);
     return err;
 }
 
-// The attention grid of one row tile size (the join of cut jobs is a launch of its own).
-template <int N>
-cudaError_t launch_rows(const PagedDecodeArgs& d, cudaStream_t stream) {
+}  // namespace paged
+
+cudaError_t launch_paged_decode_few(const PagedDecodeArgs& d, cudaStream_t stream) {
+    using namespace paged;
     KernelArgs a;
     const int64_t rows = static_cast<int64_t>(d.jobs.batch) * d.jobs.rows_per_seq;
-    if (!encode_q_map<N>(&a.qmap, d.q, rows)) return cudaErrorInvalidValue;
+    if (!encode_q_map(&a.qmap, d.q, rows)) return cudaErrorInvalidValue;
     a.cache = d.cache;
     a.jobs = d.jobs;
-    a.jobs.row_tiles = (a.jobs.rows_per_seq + N - 1) / N;
+    a.jobs.row_tiles = (a.jobs.rows_per_seq + kRows - 1) / kRows;
     a.sm_scale = d.sm_scale;
     a.sink = d.attn_sink;
     a.out = static_cast<__nv_bfloat16*>(d.out);
@@ -1005,17 +986,17 @@ cudaError_t launch_rows(const PagedDecodeArgs& d, cudaStream_t stream) {
     a.part_lse = d.part_lse;
     a.hdr = reinterpret_cast<int4*>(d.hdr);
     a.status = d.dev_status;
-    const auto kernel = d.record_bytes == 432 ? paged_decode_kernel<432, false, N>
-                        : d.block_scales      ? paged_decode_kernel<352, true, N>
-                                              : paged_decode_kernel<352, false, N>;
-    cudaError_t err = d.record_bytes == 432 ? prepare_kernel<432, false, N>()
-                      : d.block_scales      ? prepare_kernel<352, true, N>()
-                                            : prepare_kernel<352, false, N>();
+    const auto kernel = d.record_bytes == 432 ? paged_decode_kernel<432, false>
+                        : d.block_scales      ? paged_decode_kernel<352, true>
+                                              : paged_decode_kernel<352, false>;
+    cudaError_t err = d.record_bytes == 432 ? prepare_kernel<432, false>()
+                      : d.block_scales      ? prepare_kernel<352, true>()
+                                            : prepare_kernel<352, false>();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(d.runs));
-    cfg.blockDim = dim3(Shape<N>::kThreads);
-    cfg.dynamicSmemBytes = Shape<N>::kSmemAlloc;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemAlloc;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddepcontrol.wait
@@ -1026,5 +1007,4 @@ cudaError_t launch_rows(const PagedDecodeArgs& d, cudaStream_t stream) {
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-}  // namespace paged
 }  // namespace nvfp4mla
