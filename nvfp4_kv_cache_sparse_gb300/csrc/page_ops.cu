@@ -28,6 +28,9 @@ constexpr int kThreads = 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;            // 16-byte vectors of a copy thread in flight
 constexpr int kCopyBlocksPerSm = 6;
+constexpr int64_t kResizeCopyBytes = 2 << 20;   // shared pages of a resize that its own cluster copies, at most
+constexpr int kResizeCows = 1024;       // of them of one CTA
+static_assert(kResizeCopyBytes / 352 / kCluster + 1 <= kResizeCows, "a page has a record or more");
 constexpr uint32_t kDevIndex = 0x2u, kDevExhausted = 0x20u, kDevLength = 0x40u;
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -56,8 +59,23 @@ struct CopyShape {
     int parts;                // pieces a page is cut into
 };
 
-// A unit is one piece (at most kCopyThreads x kCopyVecs vectors) of one page of one cache: every
-// thread has its loads in flight before it stores any.
+// A unit is one piece (at most kCopyThreads x kCopyVecs vectors) of the first `vecs` vectors of one page of one
+// cache, for thread t of kCopyThreads: every thread has its loads in flight before it stores any.
+__device__ __forceinline__ void copy_unit(uint8_t* cache, const CopyShape& sh, int s, int d, int vecs, int part, int t) {
+    const int per = (vecs + sh.parts - 1) / sh.parts;
+    const int end = min(vecs, (part + 1) * per);
+    const uint4* from = reinterpret_cast<const uint4*>(cache) + static_cast<int64_t>(s) * sh.page_vecs;
+    uint4* to = reinterpret_cast<uint4*>(cache) + static_cast<int64_t>(d) * sh.page_vecs;
+    const int v0 = part * per + t;
+    uint4 x[kCopyVecs];
+#pragma unroll
+    for (int e = 0; e < kCopyVecs; ++e)
+        if (v0 + e * kCopyThreads < end) x[e] = __ldcs(from + v0 + e * kCopyThreads);
+#pragma unroll
+    for (int e = 0; e < kCopyVecs; ++e)
+        if (v0 + e * kCopyThreads < end) __stcs(to + v0 + e * kCopyThreads, x[e]);
+}
+
 __device__ __forceinline__ void copy_units(const Caches& caches, const CopyShape& sh, const CopyList& list, uint32_t* status) {
     const int n = list.count != nullptr ? *list.count : list.n;
     const int64_t per_cache = static_cast<int64_t>(n) * sh.parts, units = per_cache * sh.num_caches;
@@ -71,19 +89,7 @@ __device__ __forceinline__ void copy_units(const Caches& caches, const CopyShape
             if (l == 0 && part == 0 && threadIdx.x == 0) flag(status, kDevIndex);
             continue;
         }
-        const int vecs = list.records != nullptr ? __ldg(list.records + k) * sh.rec_vecs : sh.page_vecs;
-        const int per = (vecs + sh.parts - 1) / sh.parts;
-        const int end = min(vecs, (part + 1) * per);
-        const uint4* from = reinterpret_cast<const uint4*>(caches.p[l]) + static_cast<int64_t>(s) * sh.page_vecs;
-        uint4* to = reinterpret_cast<uint4*>(caches.p[l]) + static_cast<int64_t>(d) * sh.page_vecs;
-        const int v0 = part * per + threadIdx.x;
-        uint4 x[kCopyVecs];
-#pragma unroll
-        for (int e = 0; e < kCopyVecs; ++e)
-            if (v0 + e * kCopyThreads < end) x[e] = __ldcs(from + v0 + e * kCopyThreads);
-#pragma unroll
-        for (int e = 0; e < kCopyVecs; ++e)
-            if (v0 + e * kCopyThreads < end) __stcs(to + v0 + e * kCopyThreads, x[e]);
+        copy_unit(caches.p[l], sh, s, d, list.records != nullptr ? __ldg(list.records + k) * sh.rec_vecs : sh.page_vecs, part, threadIdx.x);
     }
 }
 
@@ -146,9 +152,13 @@ __device__ __forceinline__ int4 counts4(const int32_t* refs, int p, int end, int
 
 // ---- resize ----------------------------------------------------------------------------------------
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) resize_kernel(const ResizeArgs a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+resize_kernel(const __grid_constant__ Caches caches, const CopyShape sh, const ResizeArgs a) {
     __shared__ int scratch[32];
     __shared__ int need_of[kCluster], free_of[kCluster];
+    __shared__ int4 cow_list[kResizeCows];   // {source page, target page, records} that this CTA copies itself
+    __shared__ int cows;
+    if (threadIdx.x == 0) cows = 0;          // (many barriers ahead of its use)
     pdl_trigger();
     pdl_wait();
     const uint32_t rank = cluster_ctarank();
@@ -293,10 +303,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
                 a.page_refs[own] = 1;
                 row[n0 - 1] = own;
                 a.cow_dst[b] = own;
+                if (sh.num_caches > 0) cow_list[atomicAdd(&cows, 1)] = make_int4(tail, own, old & mask, 0);
             }
             a.cow_records[b] = old & mask;
             a.seq_lens[b] = now;
         }
+    }
+    if (sh.num_caches == 0) return;   // nothing to copy, or the copies are a launch of their own
+    __syncthreads();
+    constexpr int kGroups = kThreads / kCopyThreads;
+    for (int u = threadIdx.x / kCopyThreads; u < cows * sh.parts * sh.num_caches; u += kGroups) {
+        const int4 c = cow_list[u / sh.parts % cows];
+        copy_unit(caches.p[u / sh.parts / cows], sh, c.x, c.y, c.z * sh.rec_vecs, u % sh.parts, threadIdx.x % kCopyThreads);
     }
 }
 
@@ -534,9 +552,13 @@ cudaError_t launch_copy_pages(const PoolArgs& pool, const int32_t* src, const in
 }
 
 cudaError_t launch_resize(const ResizeArgs& a, const PoolArgs& pool, int sms, cudaStream_t stream) {
-    const cudaError_t err = launch(resize_kernel, dim3(kCluster), kThreads, stream, a);
-    if (err != cudaSuccess || pool.num_caches == 0) return err;
     const CopyShape s = shape_of(pool);
+    CopyShape here = s;
+    const int64_t most = static_cast<int64_t>(a.batch) * s.num_caches * s.page_vecs * 16;
+    const bool apart = most > kResizeCopyBytes;
+    if (apart) here.num_caches = 0;
+    const cudaError_t err = launch(resize_kernel, dim3(kCluster), kThreads, stream, caches_of(pool), here, a);
+    if (err != cudaSuccess || !apart) return err;
     const CopyList list = {a.cow_src, a.cow_dst, a.cow_records, nullptr, a.batch};
     return launch(copy_pages_kernel, dim3(copy_blocks(s, a.batch, sms)), kCopyThreads, stream, caches_of(pool), s, list, a.status);
 }
