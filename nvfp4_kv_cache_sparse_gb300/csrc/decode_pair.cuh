@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* xmax = reinterpret_cast<float*>(smem + kOffXmax);
         // kPaged: the page of a key of the first two tiles (see the softmax), in flight beside q
         const int key = key_begin + static_cast<int>(threadIdx.x) - 32 * kWarpV;
-        const bool looks = kPaged && warp >= kWarpV && key < key_end;
+        const bool looks = kPaged && warp >= kWarpV && static_cast<uint32_t>(key) < static_cast<uint32_t>(key_end);   // (no wrap behind 2^31)
         const int32_t page = looks ? __ldg(a.jobs.page_table + seg.seq * a.jobs.table_stride + (key >> a.jobs.page_shift)) : 0;
         const bool okq = wait_warp(ctl, &ctl->qload, 0, a.status);
         const uint32_t stage = sbase + kOffV;   // box b (dims 64b..): head hl chunk c at b*8192 + swz(hl, c)

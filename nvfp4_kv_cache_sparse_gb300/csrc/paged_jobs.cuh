@@ -44,7 +44,7 @@ __device__ __noinline__ Job job_info(const Jobs& a, int job) {
     const int last_tok = (j.row0 + j.rows - 1) / a.h_q;
     j.first_tok = j.row0 / a.h_q;
     j.keys = max(0, len - a.s_q + last_tok + 1);
-    j.tiles = (j.keys + kKeys - 1) / kKeys;
+    j.tiles = j.keys / kKeys + (j.keys % kKeys != 0 ? 1 : 0);   // (keys may lie near 2^31)
     j.first_pos = len - a.s_q + j.first_tok;
     return j;
 }

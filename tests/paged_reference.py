@@ -39,7 +39,14 @@ def attention(q, recs, blk, table, lens, page_size, sm_scale, sink=None):
     it is off by d = 2^-17 sm_scale sum|q||k|, and exp2 and its argument add 2^-20; a weight p is therefore
     off by e = 2 (d + 2^-20) relative to the row's sum, and by 2^-11 from its rounding to f16. A part of a
     cut row is rounded to f16 (2^-11 of it) and out to bf16 (2^-8 of it). With A = sum p|V| / sum p:
-        |out - ref| <= 2^-8 |ref| + (2^-11 + 2^-11 + e) A,    |lse - ref| <= d + 2^-19 + 2^-22 |ref|."""
+        |out - ref| <= 2^-8 |ref| + (2^-11 + 2^-11 + e) A + 2^-25 (1 + sum|V| / sum p),
+        |lse - ref| <= d + 2^-19 + 2^-22 |ref|.
+    The last term: below 2^-14 f16 has steps of 2^-24, so a weight 2^(z - m) there is off by up to 2^-25 of itself
+    held against its reference m, whatever its size. The reference is some earlier largest score, so m is at most
+    the row's (or part's) largest, the weights held against it add up to S' >= S = sum p with p held against the
+    largest score, and the quotient moves by at most 2^-25 sum|V| / S' <= 2^-25 sum|V| / S (for parts: the weighted
+    mean of the parts' moves, which adds up to the same). A part's f16 output likewise: 2^-25. It matters where one
+    key outweighs the others by more than 2^14 and its own V is 0 in a dim."""
     qf = q.float().numpy().astype(np.float64)
     B, s_q, h_q, _ = qf.shape
     out = np.zeros((B, s_q, h_q, 512))
@@ -67,7 +74,8 @@ def attention(q, recs, blk, table, lens, page_size, sm_scale, sink=None):
             out[b, i] = p @ v / denom
             d = 2.0 ** -17 * abs(sm_scale) * (np.abs(qf[b, i]) @ np.abs(k).T).max(axis=1)
             A = p @ np.abs(v) / denom
-            tol_out[b, i] = 2.0 ** -8 * np.abs(out[b, i]) + (2.0 ** -10 + 2 * (d[:, None] + 2.0 ** -20)) * A + 1e-30
+            tol_out[b, i] = 2.0 ** -8 * np.abs(out[b, i]) + (2.0 ** -10 + 2 * (d[:, None] + 2.0 ** -20)) * A
+            tol_out[b, i] += 2.0 ** -25 * (1 + np.abs(v).sum(axis=0)[None, :] / denom)
             tol_lse[b, i] = d + 2.0 ** -19 + 2.0 ** -22 * np.abs(lse[b, i])
     return out, lse, tol_out, tol_lse
 

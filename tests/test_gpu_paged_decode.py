@@ -214,3 +214,92 @@ def test_a_pool_past_four_gigabytes():
     far = np.where(table < 0, -1, table + pages - n).astype(np.int32)
     out, lse = lib.paged_mla_decode(q.to(DEV), pool, torch.from_numpy(far).to(DEV), torch.from_numpy(lens).to(DEV), SCALE, page_size=ps)
     ref.check_attention(out, lse, ref.attention(q, recs, False, table, lens, ps, SCALE))
+
+
+def uneven(rng, n, lo, hi, empty=0.0, long=()):
+    lens = rng.integers(lo, hi + 1, n)
+    lens[rng.random(n) < empty] = 0
+    lens[:len(long)] = long
+    return lens
+
+
+@pytest.mark.parametrize("name,h_q,s_q,lens", [
+    ("more jobs than the plan has threads, a third of them empty", 17, 2, uneven(np.random.default_rng(20), 300, 1, 260, 0.33)),
+    ("one long sequence among short ones", 33, 1, uneven(np.random.default_rng(21), 71, 1, 130, 0.0, (7000, 2500))),
+    ("a wave and a little more", 64, 1, uneven(np.random.default_rng(22), 80, 500, 700)),
+    ("few sequences, all cut", 128, 1, uneven(np.random.default_rng(23), 5, 1500, 3000)),
+    ("many row tiles of one sequence", 128, 90, np.array([700])),
+    ("all empty but one", 20, 3, np.array([0, 0, 0, 2, 0, 900, 0])),
+    ("nothing at all", 40, 1, np.zeros(9, dtype=np.int64)),
+])
+def test_plans_of_the_pairs(name, h_q, s_q, lens):
+    rng = np.random.default_rng(len(name))
+    sink = rng.standard_normal(h_q).astype(np.float32)
+    recs, table, lens, q = ref.random_batch(rng, lens, 32, h_q=h_q, s_q=s_q, scale=1.5)
+    out, lse, st = run(recs, table, lens, q, 32, sink=sink)
+    assert st == 0
+    ref.check_attention(out, lse, ref.attention(q, recs, False, table, lens, 32, SCALE, sink))
+
+
+@pytest.mark.parametrize("h_q,s_q", [(16, 1), (24, 1), (64, 2)])
+@pytest.mark.parametrize("places", [[(0, 0)], [(0, 3), (1, 9)], [(0, 40), (1, 12)], [(0, k) for k in range(44)]])
+def test_pages_outside_the_pool_anywhere(h_q, s_q, places):
+    rng = np.random.default_rng(30 + len(places))
+    recs, table, lens, q = ref.random_batch(rng, [1400, 410], 32, h_q=h_q, s_q=s_q)
+    for b, k in places:
+        table[b, k] = recs.shape[0] // 32 + k if k % 2 else -1 - k
+    out, lse, st = run(recs, table, lens, q, 32)
+    assert st == lib.DEV_INDEX_OUT_OF_RANGE
+    ref.check_attention(out, lse, ref.attention(q, recs, False, table, lens, 32, SCALE))
+
+
+@pytest.mark.parametrize("h_q", [16, 48])
+def test_references_that_move_in_every_order(h_q):
+    # the largest score of a row lies in any tile, also far above or below all others: rows of one call move
+    # their references in different tiles, and in both groups of softmax warps
+    rng = np.random.default_rng(31)
+    recs, table, lens, q = ref.random_batch(rng, [3000, 1000], 64, h_q=h_q, scale=1.0)
+    keys = oracle.dequant_records(recs, False)
+    for b in range(2):
+        slots = ref.slots_of(table[b], int(lens[b]), 64)
+        for h in range(h_q):                       # a query along one of the sequence's own keys
+            k = keys[slots[(977 * h + 31 * b) % slots.size]]
+            q[b, 0, h] = torch.from_numpy(((2.0 - 4.0 * (h % 2)) * (0.2 + h % 5) * k).astype(np.float32)).to(torch.bfloat16)
+    out, lse, st = run(recs, table, lens, q, 64)
+    assert st == 0
+    ref.check_attention(out, lse, ref.attention(q, recs, False, table, lens, 64, SCALE))
+
+
+@pytest.mark.parametrize("h_q,s_q", [(16, 1), (64, 3)])
+def test_two_graphs_share_a_workspace_and_follow_the_lengths(h_q, s_q):
+    rng = np.random.default_rng(32)
+    recs, table, lens, q = ref.random_batch(rng, [2000, 300, 0, 700], 64, h_q=h_q, s_q=s_q)
+    dev = [torch.from_numpy(x).to(DEV) for x in (recs, table, lens)]
+    qs = [q.to(DEV), (0.5 * q.float()).to(torch.bfloat16).to(DEV)]
+    ws = torch.empty(lib.paged_workspace_size(4, s_q, h_q), dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for x in qs:
+        lib.paged_mla_decode(x, dev[0], dev[1], dev[2], SCALE, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(lib.paged_mla_decode(x, dev[0], dev[1], dev[2], SCALE, workspace=ws))
+        graphs.append(g)
+    for now in ([2000, 300, 0, 700], [1, 300, 0, 64], [0, 0, 0, 0], [1999, 299, 5, 699]):
+        now = np.minimum(np.array(now, dtype=np.int32), np.maximum(lens, 0))
+        dev[2].copy_(torch.from_numpy(now))
+        ws.fill_(0xFF)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for x, (out, lse) in zip(qs, outs):
+            ref.check_attention(out, lse, ref.attention(x.cpu(), recs, False, table, now, 64, SCALE))
+
+
+@pytest.mark.parametrize("h_q", [16, 64, 128])
+def test_a_negative_scale_and_none(h_q):
+    rng = np.random.default_rng(33)
+    recs, table, lens, q = ref.random_batch(rng, [700, 90], 16, h_q=h_q)
+    for scale in (-0.04, 0.0):
+        out, lse = lib.paged_mla_decode(q.to(DEV), torch.from_numpy(recs).to(DEV), torch.from_numpy(table).to(DEV),
+                                        torch.from_numpy(lens).to(DEV), scale, page_size=16)
+        ref.check_attention(out, lse, ref.attention(q, recs, False, table, lens, 16, scale))

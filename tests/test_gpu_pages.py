@@ -264,3 +264,27 @@ def test_a_serving_loop():
     history[3], history[0], history[1] = history[1], history[3], history[0]
     sizes[3], sizes[0], sizes[1] = sizes[1], sizes[3], sizes[0]
     step([57, 21, 14, 58], 1)
+
+
+@pytest.mark.parametrize("pairs,width", [(3, 5000), (300, 6), (40, 700), (9, 4096), (256, 128), (257, 3)])
+def test_forks_of_wide_rows_and_many_pairs(pairs, width):
+    rng = np.random.default_rng(pairs)
+    batch, ps = 2 * pairs + 1, 4
+    s = State(batch, width, 400 + 2 * batch, ps, 1)
+    lens = [int(n) for n in rng.integers(0, min(width * ps, 24) + 1, batch)]
+    lens[0], lens[1] = min(width * ps, 1500), 0
+    s.resize(lens)
+    order = [int(v) for v in rng.permutation(batch)]
+    s.fork(order[:pairs], order[pairs:2 * pairs])
+    s.fork(order[pairs:2 * pairs], order[:pairs][::-1])
+    s.fork([order[0]] * pairs, [order[1]] * (pairs - 1) + [order[2]])   # one target named many times
+
+
+@pytest.mark.parametrize("batch,ps,layers", [(24, 64, 1), (90, 64, 2), (40, 256, 1), (1, 4096, 2), (700, 8, 1)])
+def test_shared_last_pages_of_every_sequence_are_copied(batch, ps, layers):
+    # few bytes: by the call's own cluster; more: by a grid of copies
+    s = State(2 * batch, 2, 4 * batch + 3, ps, layers)
+    s.resize([ps // 2 + i % (ps // 2) for i in range(batch)] + [0] * batch)
+    s.fork(list(range(batch)), list(range(batch, 2 * batch)))
+    s.resize([min(n + 1 + i % 3, 2 * ps) for i, n in enumerate(s.plain.lens)], 3)
+    s.resize([0] * (2 * batch))
