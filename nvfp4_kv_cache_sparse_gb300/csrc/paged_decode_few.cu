@@ -75,21 +75,21 @@ constexpr int kLook = 2;                   // of them at a time
 // Shared memory (offsets from a 1024-byte aligned base)
 constexpr int kOffCM = 512;                // float [8][4]: per row pair {ch_a, ch_b, -m_a, -m_b}: the score scale
                                            // sm_scale log2(e) 2^-pre and the negated reference maximum
-constexpr int kOffAlpha = 1024;            // float [kRows]: rescale factors, then 1 / l
-constexpr int kOffXmax = 1280;             // float [kRows][8]: per-row values of the four key quadrants, of two groups
-constexpr int kOffPos = 2304;              // int [kRows]: each row's position (its last visible key)
-constexpr int kOffNan = 2560;              // uint8 [4][2][64]: keys with a NaN scale, by tile and converter group
-constexpr int kOffScan = 3072;             // int64 [32]
-constexpr int kOffTile = 3328;             // int4 [kAhead]: first key position, row 0's position, 2 x (tiles left of the
+constexpr int kOffAlpha = 640;             // float [kRows]: rescale factors, then 1 / l
+constexpr int kOffPos = 704;               // int [kRows]: each row's position (its last visible key)
+constexpr int kOffXmax = 768;              // float [kRows][8]: per-row values of the four key quadrants, of two groups
+constexpr int kOffNan = 1280;              // uint8 [4][2][64]: keys with a NaN scale, by tile and converter group
+constexpr int kOffTile = 1792;             // int4 [kAhead]: first key position, row 0's position, 2 x (tiles left of the
                                            // segment) + (its first one), job
-constexpr int kOffSlot = 3456;             // int [kAhead][64]: the keys' slots; -1: no key, -2: its page is outside the pool
-constexpr int kOffQ = 6144;
+constexpr int kOffSlot = 1920;             // int [kAhead][64]: the keys' slots; -1: no key, -2: its page is outside the pool
+constexpr int kOffScan = kOffSlot;         // int64 [35], while the CTA's run is looked for
+constexpr int kOffQ = 4096;
 static_assert(kOffSlot + kAhead * kTile * 4 <= kOffQ, "control area");
 
 constexpr int kSoft = 8;                   // softmax warps: two groups of four, even and odd tiles
 constexpr int kConv = 16;                  // converter warps: two groups, even and odd blocks
 constexpr int kThreads = 32 * (kSoft + kConv + 3);   // and two MMA issuers and the look-up warp
-constexpr int kRing = 10;
+constexpr int kRing = 11;
 constexpr int kRopeRing = 3;               // tiles whose RoPE dims are held (see the converters)
 // tensor memory columns: O^T four blocks, two score buffers
 constexpr uint32_t kColO = 0, kColS = 4 * kRows;
@@ -108,7 +108,7 @@ struct __align__(8) Ctl {
     uint64_t qload;           // q boxes landed (TMA, tx-counted)
     uint64_t qready;          // four softmax warps: q converted in shared memory
     uint64_t kfull[4];        // converter warps, by tile mod 4: the tile's blocks and RoPE dims are written
-    uint64_t kfree[10];       // PV commit: a ring block has been read
+    uint64_t kfree[kRing];       // PV commit: a ring block has been read
     uint64_t sfull[2];        // QK commit, by tile parity: S^T ready
     uint64_t pfull[2];        // softmax warps, by tile parity: P^T written (and O^T rescaled)
     uint64_t voted[2];        // softmax warps, by tile parity: the references are those of the next tile
@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     asm volatile("griddepcontrol.launch_dependents;");
 
     const Run run = find_run<kRows, kTile, kThreads>(a.jobs, reinterpret_cast<int64_t*>(smem + kOffScan), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
+    __syncthreads();   // every thread has its run: the scratch becomes the table of slots
     const int count = run.count;
     write_empty_jobs<kRows, kTile, kThreads>(a.jobs, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), a.out, a.lse);
     if (blockIdx.x == 0) check_lengths(a.jobs, static_cast<int>(threadIdx.x), kThreads, a.status);
