@@ -477,13 +477,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 const bool full = pos0 + kTile - 1 <= j.first_pos;   // every row sees every key of the tile
                 uint32_t sv[4 * kGroups];
                 float z[kGroups][4];
+                uint4 rows[kGroups];   // score scales and references of this thread's rows
+                auto load_rows = [&]() {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        rows[g] = lds_u128(cm_s + 8 * (c0 + 8 * g));
+                        move_sum(g, __uint_as_float(rows[g].z), __uint_as_float(rows[g].w));
+                    }
+                };
                 // z - m of this thread's scores (-inf for a row that does not see the key); returns the largest
                 auto load_z = [&]() -> float {
                     float tmax = -INFINITY;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        const uint4 c = lds_u128(cm_s + 8 * (c0 + 8 * g));
-                        move_sum(g, __uint_as_float(c.z), __uint_as_float(c.w));
+                        const uint4 c = rows[g];
                         const uint64_t ch = f32x2_pack(__uint_as_float(c.x), __uint_as_float(c.y));
                         const uint64_t nm = f32x2_pack(__uint_as_float(c.z), __uint_as_float(c.w));
                         const float2 a0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[4 * g]), __uint_as_float(sv[4 * g + 1])), ch, nm));
@@ -521,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 }
                 // the other group's tile before this one has its references
                 if (ok && it > s0) ok = wait_warp(ctl, &ctl->voted[grp ^ 1], ((it - 1) >> 1) & 1, a.status);
+                if (ok) load_rows();
                 if (ok) ok = wait_warp(ctl, &ctl->sfull[grp], (it >> 1) & 1, a.status);
                 if (ok) {
                     if (lane == 0) mbar_arrive(&ctl->tfree[at]);   // (the wait's vote put every lane's reads before)
@@ -588,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                         }
                         tmem_wait_st();
                     }
+                    load_rows();
                     (void)load_z();   // against the moved references
                     __syncwarp();
                 }
