@@ -44,7 +44,7 @@ PEAKS_FALLBACK = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # DRAM bytes (read + write) of one decode_pair_kernel launch on this workload, from an ncu
 # capture (dram__bytes_read.sum + dram__bytes_write.sum), keyed by the hash of the decode code
 # (comments removed) it was taken with; reported as null once that code changes.
-NCU_TRAFFIC = {"f7a55f8541dd": 34268672 + 47104}
+NCU_TRAFFIC = {"9e2ee7c41e93": 34267136 + 41728}
 DECODE_CALLS_TIMED = 128   # the decode call alone: 16 laps of 8 back-to-back calls
 
 
@@ -71,8 +71,8 @@ def code_hash(text: str) -> str:
 
 
 def decode_source_hash() -> str:
-    src = os.path.join(ROOT, "nvfp4_kv_cache_sparse_gb300", "csrc", "sparse_decode_pair.cu")
-    return code_hash(open(src).read())
+    csrc = os.path.join(ROOT, "nvfp4_kv_cache_sparse_gb300", "csrc")
+    return code_hash("\n".join(open(os.path.join(csrc, f)).read() for f in ("decode_pair.cuh", "sparse_decode_pair.cu")))
 
 
 

@@ -38,11 +38,13 @@
 // with a NaN scale likewise; P is 0 for a key that a row does not see and NaN for a NaN key that it
 // sees.
 //
-// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 187 us, 2.0 TB/s, where
-// the records alone take 56 us. A tile takes about 2700 clk: the converters' chain of waits, loads and 18
-// stores of 512 bytes (STS 43%, MMA operands 41% of the shared memory's cycles; issue slots 48%; DRAM 28%).
-// What it costs to have one f16 tile for both products, 2 x 64 KB written and read for 22 KB of records, is
-// what keeps it from the memory's rate.
+// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 176 to 187 us, 2.1 TB/s, where
+// the records alone take 56 us. A tile takes about 1.5 us: its converters' chain (barrier, scales, two blocks of
+// conversion and stores, fence: 2600 clk) and the ring, whose blocks live through the QK, the softmax and the PV of
+// their tile (ring of 10 blocks 197 us, of 11 192). Of the shared memory's cycles the threads' accesses take 64% and
+// the MMAs' operands 43% (two pipes, side by side in part), issue slots 54%, DRAM 30%: one f16 tile for both
+// products, 64 KB written and read twice for 22 KB of records, is what keeps it from the memory's rate. One sequence
+// of 1500 tokens: 18 us on the device, a chain of latencies (lengths, page table, records, products, join).
 //
 // Every wait is bounded by time; on timeout the CTA sets NVFP4_MLA_DEV_TIMEOUT, stops issuing work,
 // drains what it issued and returns.
