@@ -44,7 +44,7 @@
 // their tile (ring of 10 blocks 197 us, of 11 192). Of the shared memory's cycles the threads' accesses take 64% and
 // the MMAs' operands 43% (two pipes, side by side in part), issue slots 54%, DRAM 30%: one f16 tile for both
 // products, 64 KB written and read twice for 22 KB of records, is what keeps it from the memory's rate. One sequence
-// of 1500 tokens: 18 us on the device, a chain of latencies (lengths, page table, records, products, join).
+// of 1500 tokens: 17 us on the device, a chain of latencies (lengths, page table, records, products, join).
 //
 // Every wait is bounded by time; on timeout the CTA sets NVFP4_MLA_DEV_TIMEOUT, stops issuing work,
 // drains what it issued and returns.
@@ -288,6 +288,8 @@ struct HalfRecord {
         }
     }
 };
+// Brings a tensor map near ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 // Starts bringing `bytes` (a multiple of 16, from a 16-byte boundary) into L2.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -307,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+        prefetch_tensormap(&a.qmap);
         mbar_init(&ctl->qload, 1);
         mbar_init(&ctl->qready, kGroupWarps);
         for (int s = 0; s < 4; ++s) mbar_init(&ctl->kfull[s], kConv);
@@ -693,25 +696,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             const int dim = 32 * qd + (qd >= 2 ? lane ^ 8 : lane);
             uint16_t* dst = whole ? reinterpret_cast<uint16_t*>(a.out) + row * 512
                                   : a.part_out + static_cast<int64_t>(slot) * kRows * 512;
+            float factor[kRows];
+#pragma unroll
+            for (int e = 0; e < kRows; e += 4) {
+                const uint4 f = lds_u128(alpha_s + 4 * e);
+                factor[e] = __uint_as_float(f.x);
+                factor[e + 1] = __uint_as_float(f.y);
+                factor[e + 2] = __uint_as_float(f.z);
+                factor[e + 3] = __uint_as_float(f.w);
+            }
 #pragma unroll 1
             for (int b = 2 * grp; b < 2 * grp + 2; ++b) {
                 uint32_t o[kRows];
                 tmem_ld16(lane_base + kColO + kRows * b, o);
                 tmem_wait_ld();
-                uint16_t* p = dst + 128 * b + dim;
+                // neighbouring lanes (dims) exchange a row each: 32-bit stores, the even lane's of row e, the odd lane's of row e + 1
+                uint16_t* p = dst + 128 * b + (dim & ~1);
 #pragma unroll
-                for (int e = 0; e < kRows; ++e) {
-                    if (e < j.rows) {
-                        const float f = lds_f32(alpha_s + 4 * e);
-                        const float v = f != 0.0f ? __uint_as_float(o[e]) * f : 0.0f;
-                        p[e * 512] = whole ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-                    }
+                for (int e = 0; e < kRows; e += 2) {
+                    const float v0 = factor[e] != 0.0f ? __uint_as_float(o[e]) * factor[e] : 0.0f;
+                    const float v1 = factor[e + 1] != 0.0f ? __uint_as_float(o[e + 1]) * factor[e + 1] : 0.0f;
+                    const float u = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
+                    const float lo = (lane & 1) ? u : v0, hi = (lane & 1) ? v1 : u;
+                    const int r = e + (lane & 1);
+                    if (r < j.rows) *reinterpret_cast<uint32_t*>(p + r * 512) = whole ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
                 }
             }
             tc_fence_before_sync();
             if (!whole && seg_tile == 0) {
                 // the first part of a cut job: its last tile lies (tiles - t_end - 1) behind the end of this run
-                const int64_t end = run.total * (static_cast<int64_t>(blockIdx.x) + 1) / run.runs;
+                const int64_t end = run_begin(run.total, run.runs, static_cast<int64_t>(blockIdx.x) + 1);
                 hdr = make_int4(static_cast<int>(row), j.rows, run_of(run, end - (t_end + 1) + j.tiles - 1) - static_cast<int>(blockIdx.x) + 1,
                                 2 * static_cast<int>(blockIdx.x) + 1);
             }

@@ -32,17 +32,18 @@ struct Job {
     int first_pos, first_tok; // position and token of row row0
 };
 
-// Job `job` of row tiles of kRows rows and key tiles of kKeys keys. (Not inlined: its divisions are long,
-// and it runs once per job, beside loops that should stay in the instruction cache.)
+// Job `job` of row tiles of kRows rows and key tiles of kKeys keys. Row tiles of 128 cut the rows of a sequence; with
+// smaller ones a sequence's rows are one job. (Not inlined: its divisions are long, and it runs once per
+// job, beside loops that should stay in the instruction cache.)
 template <int kRows, int kKeys>
 __device__ __noinline__ Job job_info(const Jobs& a, int job) {
     Job j;
-    j.seq = job / a.row_tiles;
-    j.row0 = (job - j.seq * a.row_tiles) * kRows;
-    j.rows = min(kRows, a.rows_per_seq - j.row0);
+    j.seq = kRows < 128 ? job : job / a.row_tiles;
+    j.row0 = kRows < 128 ? 0 : (job - j.seq * a.row_tiles) * kRows;
+    j.rows = kRows < 128 ? a.rows_per_seq : min(kRows, a.rows_per_seq - j.row0);
     const int len = min(max(__ldg(a.seq_lens + j.seq), 0), a.capacity);
-    const int last_tok = (j.row0 + j.rows - 1) / a.h_q;
-    j.first_tok = j.row0 / a.h_q;
+    const int last_tok = kRows < 128 ? a.s_q - 1 : (j.row0 + j.rows - 1) / a.h_q;
+    j.first_tok = kRows < 128 ? 0 : j.row0 / a.h_q;
     j.keys = max(0, len - a.s_q + last_tok + 1);
     j.tiles = j.keys / kKeys + (j.keys % kKeys != 0 ? 1 : 0);   // (keys may lie near 2^31)
     j.first_pos = len - a.s_q + j.first_tok;
@@ -65,6 +66,12 @@ struct Run {
 };
 // The run that holds tile t of all.
 __device__ __forceinline__ int run_of(const Run& r, int64_t t) { return static_cast<int>(((t + 1) * r.runs - 1) / r.total); }
+
+// Where run c of runs (at most 160) begins.
+__device__ __forceinline__ int64_t run_begin(int64_t total, int64_t runs, int64_t c) {
+    if (total < (int64_t(1) << 23)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(runs);   // short division
+    return total * c / runs;
+}
 
 template <int kRows, int kKeys, int kThreads>
 __device__ __noinline__ Run find_run(const Jobs& a, int64_t* scratch, int runs, int c) {
@@ -94,8 +101,8 @@ __device__ __noinline__ Run find_run(const Jobs& a, int64_t* scratch, int runs, 
     r.count = 0;
     int* found = reinterpret_cast<int*>(scratch + 33);
     if (c < r.runs) {
-        const int64_t g0 = r.total * c / r.runs;
-        r.count = static_cast<int>(r.total * (c + 1) / r.runs - g0);
+        const int64_t g0 = run_begin(r.total, r.runs, c);
+        r.count = static_cast<int>(run_begin(r.total, r.runs, c + 1) - g0);
         if (before <= g0 && g0 < before + mine) {
             int64_t at = before;
             int j = ja;
