@@ -110,7 +110,7 @@ struct __align__(8) Ctl {
     uint64_t qload;           // q boxes landed (TMA, tx-counted)
     uint64_t qready;          // four softmax warps: q converted in shared memory
     uint64_t kfull[4];        // converter warps, by tile mod 4: the tile's blocks and RoPE dims are written
-    uint64_t kfree[kRing];       // PV commit: a ring block has been read
+    uint64_t kfree[kRing];    // PV commit: a ring block has been read
     uint64_t sfull[2];        // QK commit, by tile parity: S^T ready
     uint64_t pfull[2];        // softmax warps, by tile parity: P^T written (and O^T rescaled)
     uint64_t voted[2];        // softmax warps, by tile parity: the references are those of the next tile
