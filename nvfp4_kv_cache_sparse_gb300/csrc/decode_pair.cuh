@@ -28,7 +28,7 @@
 // same numbers as with bf16 q, and S comes out as 2^pre times the exact score, which the softmax
 // folds into its scale. P is f16 (entries in [0, 2^8]).
 // Softmax. A lazy reference maximum m per head (log2 domain): P = 2^(z - m) and O, l accumulate
-// against m. A tile only needs the reference to move when some score exceeds m + 8; the softmax
+// against m. A tile only needs the reference to move when some score exceeds m + 8 (kPaged: 15); the softmax
 // warps vote on that once per tile (one barrier reduction) and only then exchange maxima and
 // rescale O in tensor memory, so the common tile has no cross-thread exchange at all. Masked keys
 // have quiet-NaN K rows: their scores are NaN, max() ignores them and max(2^NaN, 0) = 0.
@@ -57,7 +57,7 @@
 // sees whole takes the same path as the sparse decode's. A page outside the pool (an error that is reported)
 // is announced to the softmax two tiles ahead; only then does it look up the pages of its keys itself (looked
 // up for every tile: 1320 against 1241 us for 2 chunks of 256 tokens x 64 heads).
-// Measured: 2 chunks of 256 tokens x 64 heads over up to 16640 tokens 0.98 ms, 1.04 PFLOP/s (55% of a library's product);
+// Measured: 2 chunks of 256 tokens x 64 heads over up to 16640 tokens 0.96 ms, 1.06 PFLOP/s (55% of a library's product);
 // 32 sequences of up to 8192 tokens x 2 tokens x 128 heads 118 us. A tile of 128 keys takes 2.4 us (tensor pipe 52%
 // busy, issue slots 57%, shared-memory accesses 58%): K, V and S are single buffers, so conversion, QK, softmax and PV
 // of a tile wait for one another in turn; a segment adds 11 us of its own (q 4.5, output 3.3, barriers and first tile).
@@ -94,7 +94,11 @@ constexpr int kQTmemSteps = 24;            // K-steps of 16 dims taken from tens
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// log2 units: P in f16 is at most 2^threshold (< 65504). A move of a reference waits for the PV before and rescales O;
+// over whole sequences there are several a row. 2 chunks of 256 tokens x 64 heads, thresholds 8 / 12 / 15: 990 / 961 / 960 us;
+// 32 sequences x 2 tokens x 128 heads 123.0 / 117.5 / 116.6 us.
+template <bool kPaged>
+constexpr float kRescaleThreshold = kPaged ? 15.0f : 8.0f;
 
 // Shared memory (offsets from a 1024-byte aligned base)
 constexpr int kBlk = 8192;                 // 64 rows x 128 B (one 64-wide 16-bit block)
@@ -537,12 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- does any head of this CTA need a new reference? (one barrier reduction)
-            if (bar_red_or(1, 256, mx > m_ref + kRescaleThreshold)) {
+            if (bar_red_or(1, 256, mx > m_ref + kRescaleThreshold<kPaged>)) {
                 xmax[qi * 64 + hl] = mx;
                 named_bar_sync(1, 256);
                 const float tmax = fmaxf(fmaxf(xmax[hl], xmax[64 + hl]), fmaxf(xmax[128 + hl], xmax[192 + hl]));
                 float alpha = 1.0f;
-                if (tmax > m_ref + kRescaleThreshold) {
+                if (tmax > m_ref + kRescaleThreshold<kPaged>) {
                     alpha = m_ref == -INFINITY ? 0.0f : ex2_approx(m_ref - tmax);
                     m_ref = tmax;
                 }

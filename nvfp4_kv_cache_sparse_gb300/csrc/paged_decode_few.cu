@@ -26,7 +26,7 @@
 // empty while its softmax ran (3.5 us per 128 keys with a ring of 1.5 such tiles).
 //
 // Softmax. A lazy reference maximum per row (log2 domain): P = 2^(z - m); a tile moves m only where
-// some score exceeds m + 8: the warps vote once per tile, and only then is O^T rescaled. A tile's softmax
+// some score exceeds m + 15: the warps vote once per tile, and only then is O^T rescaled. A tile's softmax
 // is a chain of short waits (2900 to 3800 clk from its scores to the next tile's, against 1500 of MMAs), so
 // two groups of four warps take the even and the odd tiles; only the vote, from reading m to having moved
 // it, goes in the tiles' order (242 -> 223 us for 64 sequences x 16 heads). The scores of an M = 64 MMA lie in
@@ -38,7 +38,7 @@
 // with a NaN scale likewise; P is 0 for a key that a row does not see and NaN for a NaN key that it
 // sees.
 //
-// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 176 to 187 us, 2.1 TB/s, where
+// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 171 to 179 us, 2.2 TB/s, where
 // the records alone take 56 us. A tile takes about 1.5 us: its converters' chain (barrier, scales, two blocks of
 // conversion and stores, fence: 2600 clk) and the ring, whose blocks live through the QK, the softmax and the PV of
 // their tile (ring of 10 blocks 197 us, of 11 192). Of the shared memory's cycles the threads' accesses take 64% and
@@ -68,7 +68,7 @@ constexpr int kRows = 16;                  // query rows of a job (N of both pro
 constexpr int kTile = 64;                  // keys per tile (M of the QK MMAs)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kRescaleThreshold = 15.0f; // log2 units: P in f16 is at most 2^15 (64 sequences x 16 heads, 8 / 12 / 15: 183.5 / 178.7 / 179.0 us)
 
 constexpr int kSubBlk = 8192;              // 64 keys x 64 dims
 constexpr int kBlk = 16384;                // 64 keys x 128 dims
