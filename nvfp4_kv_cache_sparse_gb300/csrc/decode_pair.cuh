@@ -57,8 +57,8 @@
 // sees whole takes the same path as the sparse decode's. A page outside the pool (an error that is reported)
 // is announced to the softmax two tiles ahead; only then does it look up the pages of its keys itself (looked
 // up for every tile: 1320 against 1241 us for 2 chunks of 256 tokens x 64 heads).
-// Measured: 2 chunks of 256 tokens x 64 heads over up to 16640 tokens 0.96 ms, 1.06 PFLOP/s (55% of a library's product);
-// 32 sequences of up to 8192 tokens x 2 tokens x 128 heads 118 us. A tile of 128 keys takes 2.4 us (tensor pipe 52%
+// Measured: 2 chunks of 256 tokens x 64 heads over up to 16640 tokens 0.92 ms, 1.11 PFLOP/s (58% of a library's product);
+// 32 sequences of up to 8192 tokens x 2 tokens x 128 heads 118 us. A tile of 128 keys takes 2.3 us (tensor pipe 55%
 // busy, issue slots 57%, shared-memory accesses 58%): K, V and S are single buffers, so conversion, QK, softmax and PV
 // of a tile wait for one another in turn; a segment adds 11 us of its own (q 4.5, output 3.3, barriers and first tile).
 #pragma once
@@ -227,6 +227,16 @@ __device__ __forceinline__ void signal_leader(Ctl* ctl, uint64_t* bar, int crank
     } else {
         st_async_b32(mapa_shared(smem_addr(&ctl->sig_sink), leader), 0u, mapa_shared(smem_addr(bar), leader));
     }
+}
+
+// kPaged: which of the 32 keys from position pos on a row sees whose last key is last_pos (bit j: key pos + j); with
+// `looks`, only those in pages of the pool. (Not inlined: it runs in few tiles, beside the softmax's registers.)
+static __device__ __noinline__ uint32_t seen_keys(const paged::Jobs& jobs, int seq, int keys, int pos, int last_pos, bool looks) {
+    const int n = last_pos + 1 - pos;
+    uint32_t seen = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
+    if (__any_sync(0xffffffffu, looks))
+        seen &= __ballot_sync(0xffffffffu, paged::slot_of(jobs, seq, keys, pos + static_cast<int>(threadIdx.x & 31)) >= 0);
+    return seen;
 }
 
 // V row of one key: the four blocks 4c + q (c = 4 half + cl) into V block cl, chunks 2q, 2q + 1.
@@ -496,18 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s[32];
             float mx = -INFINITY;
             float mul = ch;
-            uint32_t seen = 0xffffffffu;   // kPaged: which of the warp's keys this row sees
-            if constexpr (kPaged) {
-                const int pos = warp_key + kTile * i;
-                const int n = last_pos + 1 - pos;   // keys up to the row's position
-                if (n < 32) seen = n > 0 ? (1u << n) - 1u : 0u;
-            }
             // (kPaged: a tile's flag is set ahead of the vfull arrivals of two tiles earlier, and the P of the last tile
             // waited for that PV)
             const uint32_t outside = kPaged ? *reinterpret_cast<volatile uint32_t*>(&ctl->outside) : 0u;
             if (ok) ok = wait_warp(ctl, &ctl->qkdone, i & 1, a.status);
-            if (kPaged && __any_sync(0xffffffffu, outside != 0u))
-                seen &= __ballot_sync(0xffffffffu, paged::slot_of(a.jobs, seg.seq, key_end, warp_key + kTile * i + lane) >= 0);
             if (ok) {
                 tc_fence_after_sync();
                 tmem_ld32(lane_base + kColS + 32 * h2, s);
@@ -516,8 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) signal_leader(ctl, &ctl->sfree, crank, warp == 0, 8);
                 float m0 = -INFINITY, m1 = -INFINITY;
-                if (pos_scale) {
-                    if (kPaged && seen != 0xffffffffu) {
+                if constexpr (kPaged) {
+                    // Scores of keys that a row does not see become -inf: in tiles that reach behind the position of the warp's
+                    // first row, and where a page lies outside the pool (one branch for the warp, taken in few tiles; masks
+                    // worked out for every tile cost 6%: 959 against 900 us for 2 chunks of 256 tokens x 64 heads)
+                    if (!pos_scale) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * ch);
+                        mul = 1.0f;
+                    }
+                    const int pos = warp_key + kTile * i;
+                    if (__any_sync(0xffffffffu, pos + 31 > last_pos || outside != 0u)) {
+                        const uint32_t seen = seen_keys(a.jobs, seg.seq, key_end, pos, last_pos, outside != 0u);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (((seen >> j) & 1u) == 0u) s[j] = 0xFF800000u;   // -inf
@@ -527,12 +539,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m0 = fmax3(m0, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
                         m1 = fmax3(m1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
                     }
+                    mx = fmaxf(m0, m1) * mul;
+                } else if (pos_scale) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        m0 = fmax3(m0, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                        m1 = fmax3(m1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                    }
                     mx = fmaxf(m0, m1) * ch;
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float z = __uint_as_float(s[j]) * ch;
-                        if (kPaged && ((seen >> j) & 1u) == 0u) z = -INFINITY;
+                        const float z = __uint_as_float(s[j]) * ch;
                         s[j] = __float_as_uint(z);
                         m0 = fmaxf(m0, z);
                     }
