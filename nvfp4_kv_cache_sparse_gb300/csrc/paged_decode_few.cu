@@ -41,8 +41,8 @@
 // What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 171 to 179 us, 2.2 TB/s, where
 // the records alone take 56 us. A tile takes about 1.5 us: its converters' chain (barrier, scales, two blocks of
 // conversion and stores, fence: 2600 clk) and the ring, whose blocks live through the QK, the softmax and the PV of
-// their tile (ring of 10 blocks 197 us, of 11 192). Of the shared memory's cycles the threads' accesses take 64% and
-// the MMAs' operands 43% (two pipes, side by side in part), issue slots 54%, DRAM 30%: one f16 tile for both
+// their tile (ring of 10 blocks 197 us, of 11 192). Of the shared memory's cycles the threads' accesses take 67% and
+// the MMAs' operands 46% (two pipes, side by side in part), issue slots 55%, DRAM 31%: one f16 tile for both
 // products, 64 KB written and read twice for 22 KB of records, is what keeps it from the memory's rate. One sequence
 // of 1500 tokens: 17 us on the device, a chain of latencies (lengths, page table, records, products, join).
 //
