@@ -132,7 +132,8 @@ __device__ __forceinline__ int block_scan(int a, int* scratch, int* total) {
     return __shfl_sync(0xffffffffu, s - t, warp) + incl;
 }
 
-// Gives every CTA of the cluster this CTA's value at slot[rank]; to be read after cluster_sync().
+// Gives every CTA of the cluster this CTA's value at slot[rank]; to be read after cluster_sync(). A CTA's shared memory
+// may be written to once it runs, which a barrier of the cluster has to have shown before a kernel's first use.
 __device__ __forceinline__ void publish(int* slot, uint32_t rank, int value) {
     if (threadIdx.x < kCluster) {
         const uint32_t remote = mapa_shared(smem_addr(slot + rank), threadIdx.x);
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_write_kernel(const ForkArgs
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) compact_plan_kernel(const CompactArgs a) {
     __shared__ int scratch[32];
     __shared__ int live_of[kCluster], below_of[kCluster];
+    cluster_arrive();   // (its wait, ahead of the first publish, is hidden by the counting)
     pdl_trigger();
     pdl_wait();
     const uint32_t rank = cluster_ctarank();
@@ -436,6 +438,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
         return total;
     };
     const int mine = count_live(hi);
+    cluster_wait();     // every CTA of the cluster runs
     publish(live_of, rank, mine);
     cluster_sync();
     int n = 0, before = 0;
