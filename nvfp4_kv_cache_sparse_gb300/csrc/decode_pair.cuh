@@ -26,9 +26,9 @@
 // and V tiles are f16 (the bf16 RoPE of 432-byte records stays bf16). q enters as f16 scaled by a
 // per-head power of two (2^pre with max|q| 2^pre in [2^14, 2^15)): the products q_d K_d are the
 // same numbers as with bf16 q, and S comes out as 2^pre times the exact score, which the softmax
-// folds into its scale. P is f16 (entries in [0, 2^8]).
-// Softmax. A lazy reference maximum m per head (log2 domain): P = 2^(z - m) and O, l accumulate
-// against m. A tile only needs the reference to move when some score exceeds m + 8 (kPaged: 15); the softmax
+// folds into its scale. P is f16 (entries in [0, 2^8], kPaged: [0, 2^15.9]).
+// Softmax. A lazy reference m per head (log2 domain): P = 2^(z - m) and O, l accumulate
+// against m. A tile only needs the reference to move when some score exceeds m + 8 (kPaged: 15.9); the softmax
 // warps vote on that once per tile (one barrier reduction) and only then exchange maxima and
 // rescale O in tensor memory, so the common tile has no cross-thread exchange at all. Masked keys
 // have quiet-NaN K rows: their scores are NaN, max() ignores them and max(2^NaN, 0) = 0.
@@ -94,11 +94,10 @@ constexpr int kQTmemSteps = 24;            // K-steps of 16 dims taken from tens
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// log2 units: P in f16 is at most 2^threshold (< 65504). A move of a reference waits for the PV before and rescales O;
-// over whole sequences there are several a row. 2 chunks of 256 tokens x 64 heads, thresholds 8 / 12 / 15: 990 / 961 / 960 us;
-// 32 sequences x 2 tokens x 128 heads 123.0 / 117.5 / 116.6 us.
+// log2 units: scores above the reference by more than this move it. The sparse decode's new reference is the largest
+// score; whole sequences may be long, and theirs lies below it (new_reference in paged_jobs.cuh, with the measurements).
 template <bool kPaged>
-constexpr float kRescaleThreshold = kPaged ? 15.0f : 8.0f;
+constexpr float kRescaleThreshold = kPaged ? paged::kMaxWeightLog2 : 8.0f;
 
 // Shared memory (offsets from a 1024-byte aligned base)
 constexpr int kBlk = 8192;                 // 64 rows x 128 B (one 64-wide 16-bit block)
@@ -565,8 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float tmax = fmaxf(fmaxf(xmax[hl], xmax[64 + hl]), fmaxf(xmax[128 + hl], xmax[192 + hl]));
                 float alpha = 1.0f;
                 if (tmax > m_ref + kRescaleThreshold<kPaged>) {
-                    alpha = m_ref == -INFINITY ? 0.0f : ex2_approx(m_ref - tmax);
-                    m_ref = tmax;
+                    const float m = kPaged ? paged::new_reference(tmax, fminf(fminf(xmax[hl], xmax[64 + hl]), fminf(xmax[128 + hl], xmax[192 + hl]))) : tmax;
+                    alpha = m_ref == -INFINITY ? 0.0f : ex2_approx(m_ref - m);
+                    m_ref = m;
                 }
                 l *= alpha;
                 if (ok && i > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {

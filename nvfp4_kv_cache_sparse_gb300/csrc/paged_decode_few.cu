@@ -25,8 +25,9 @@
 // CTA can have in flight is bounded by shared memory, and a tile of 128 keys (128 KB) left the ring half
 // empty while its softmax ran (3.5 us per 128 keys with a ring of 1.5 such tiles).
 //
-// Softmax. A lazy reference maximum per row (log2 domain): P = 2^(z - m); a tile moves m only where
-// some score exceeds m + 15: the warps vote once per tile, and only then is O^T rescaled. A tile's softmax
+// Softmax. A lazy reference per row (log2 domain): P = 2^(z - m) in f16; a tile moves m only where some
+// score exceeds m + 15.9, to a little below its largest score (new_reference in paged_jobs.cuh): the
+// warps vote once per tile, and only then is O^T rescaled. A tile's softmax
 // is a chain of short waits (2900 to 3800 clk from its scores to the next tile's, against 1500 of MMAs), so
 // two groups of four warps take the even and the odd tiles; only the vote, from reading m to having moved
 // it, goes in the tiles' order (242 -> 223 us for 64 sequences x 16 heads). The scores of an M = 64 MMA lie in
@@ -68,7 +69,6 @@ constexpr int kRows = 16;                  // query rows of a job (N of both pro
 constexpr int kTile = 64;                  // keys per tile (M of the QK MMAs)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 15.0f; // log2 units: P in f16 is at most 2^15 (64 sequences x 16 heads, 8 / 12 / 15: 183.5 / 178.7 / 179.0 us)
 
 constexpr int kSubBlk = 8192;              // 64 keys x 64 dims
 constexpr int kBlk = 16384;                // 64 keys x 128 dims
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 if (ok) tmax = load_z();
                 // ---- does any row need a new reference? (one barrier reduction; also entered where a wait ran out,
                 // and then left by the whole group at once)
-                if (bar_red_or(bar_grp, kGroupThreads, tmax > kRescaleThreshold || !ok)) {
+                if (bar_red_or(bar_grp, kGroupThreads, tmax > kMaxWeightLog2 || !ok)) {
                     // O^T stands still once the PV of the tile before has completed
                     if (ok && it > s0) {
                         const int g = 4 * it - 1;
@@ -581,9 +581,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                                                fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
                         const float mo = -lds_f32(negm_addr(lane));
                         float al = 1.0f;
-                        if (zt > mo + kRescaleThreshold) {
-                            al = mo == -INFINITY ? 0.0f : ex2_approx(mo - zt);
-                            sts_f32(negm_addr(lane), -zt);
+                        if (zt > mo + kMaxWeightLog2) {
+                            const float m = new_reference(zt, fminf(fminf(__uint_as_float(x.x), __uint_as_float(x.y)),
+                                                                    fminf(__uint_as_float(x.z), __uint_as_float(x.w))));
+                            al = mo == -INFINITY ? 0.0f : ex2_approx(mo - m);
+                            sts_f32(negm_addr(lane), -m);
                         }
                         sts_f32(alpha_s + 4 * lane, al);
                     }

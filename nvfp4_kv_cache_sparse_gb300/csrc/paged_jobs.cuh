@@ -50,6 +50,17 @@ __device__ __noinline__ Job job_info(const Jobs& a, int job) {
     return j;
 }
 
+// The reference m of a row whose tile has the largest score zt (log2 units), zmin being the smallest of the largest scores
+// of its four quarters. Weights 2^(z - m) are held in f16: off by 2^-11 of themselves down to 2^-14, by 2^-25 below,
+// so a key that lies far below the largest is held the better the further m lies below it; a score may exceed m
+// by kMaxWeightLog2 until the row's output has to be rescaled. m = zt - 3 costs no time against m = zt (64 sequences x 16
+// heads 166 / 166 us, 2 chunks of 256 tokens x 64 heads 904 / 911 us: 15 bits of range above m then, 12.9 now), m = zt - 7
+// does (172.5 and 943 us), as ordinary rows meet larger scores later. Where one key outweighs whole quarters of its tile
+// (an attention sink, whose own value is often near 0: the others are what the output consists of), larger scores are
+// rare, and m lies up to 12 below, so that the others stay above 2^-14 up to 2^26 below the largest.
+constexpr float kMaxWeightLog2 = 15.9f;   // 2^15.9 < 65504
+__device__ __forceinline__ float new_reference(float zt, float zmin) { return zt - fminf(fmaxf(zt - zmin - 14.0f, 3.0f), 12.0f); }
+
 // Slot of the token at position pos of a sequence; -1: none of the `keys` first, -2: its page is outside the pool.
 __device__ __forceinline__ int slot_of(const Jobs& a, int seq, int keys, int pos) {
     if (pos >= keys) return -1;
