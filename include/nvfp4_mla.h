@@ -297,8 +297,8 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s
  *                lse = -inf.
  *   workspace    device scratch of at least ..._workspace_size bytes, 256-byte aligned; needs no
  *                initialization. Calls that may overlap on the GPU need one each.
- * Precision: as nvfp4_sparse_mla_decode on NVFP4 records (parts of a row are f16 normalized outputs,
- * joined in fp32). A weight e^z is held in f16: off by 2^-11 of itself, and at least by 2^-28 of the row's
+ * Precision: as nvfp4_sparse_mla_decode on NVFP4 records (parts of a row are normalized outputs in
+ * f16 steps of at least 2^-28, joined in fp32). A weight e^z is held in f16: off by 2^-11 of itself, and at least by 2^-28 of the row's
  * largest weight (down to 2^-37 where that one outweighs whole quarters of its tile of 64 or 128 keys by more
  * than 2^17, as an attention sink does). Over n tokens that is at most 2^-28 sum|V| / (sum of the weights over the
  * largest one), which counts where V is 0 for the few keys that hold most of the weight and n passes some 10^5. A NaN in a query or in a record makes NaN the rows that see it, and only those.

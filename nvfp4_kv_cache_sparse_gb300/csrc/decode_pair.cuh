@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float denom = lt;
             if (single && a.sink != nullptr)
                 denom += exp2f(__ldg(a.sink + (kPaged ? (seg.row0 + head) % a.jobs.h_q : head)) * kLog2e - m_ref);
-            factor = 1.0f / denom;
+            factor = (kPaged && !single ? paged::kPartScale : 1.0f) / denom;
         }
         if (qi == 0 && (!kPaged || head < seg.rows)) {
             if (single)

@@ -17,7 +17,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // Entry c of hdr names a job that was cut: first output row, rows (0: there is none), parts n, slot f of the
 // first part; the others lie in slots next(c), next(c) + step, ... With part lse L_s (log2) and f16 output
-// O_s (divided by its own sum): w_s = 2^(L_s - m), out = sum_s w_s O_s / (sum_s w_s + 2^(sink - m)),
+// O_s (divided by its own sum, times kPartScale): w_s = 2^(L_s - m), out = sum_s w_s O_s / (kPartScale (sum_s w_s + 2^(sink - m))),
 // lse = (m + log2 sum_s w_s) ln 2, in fp32. A warp per row and 128 dims: its lanes weigh the parts (one each, in
 // turns of 32), then the warp adds the parts up in their order, eight loads in flight. A NaN L_s makes the
 // row NaN; a row without any key gets out = 0, lse = -inf.
@@ -66,7 +66,7 @@ paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict
             }
         }
     }
-    const float f = tot == 0.0f ? 0.0f : 1.0f / (tot + exp2f(sk - m));
+    const float f = tot == 0.0f ? 0.0f : 1.0f / (paged::kPartScale * (tot + exp2f(sk - m)));
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? acc[e] * f : 0.0f;
     __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc[0], acc[1]), __floats2bfloat162_rn(acc[2], acc[3])};

@@ -10,7 +10,7 @@
 // Work split. The rows of a sequence (a job) share every key that is dequantized; the tiles of 64 keys of all
 // jobs are cut into equal runs, one per CTA (one CTA per SM; paged_jobs.cuh). A job that lies in one run is
 // finished by its CTA; the parts of a job that was cut go to the workspace (at most two per CTA, f16
-// outputs divided by their own sums, fp32 log-sum-exps) and a second kernel joins them.
+// outputs divided by their own sums, times kPartScale, and fp32 log-sum-exps) and a second kernel joins them.
 //
 // Contractions. As keys outnumber rows, both products have the keys or the value dims on the MMA's M
 // side: S^T [64 keys x 16] = K Q^T and O^T [512 dims x 16] += V^T P^T (four M = 128 MMAs per 16
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 if (!empty) {
                     float denom = sum;
                     if (whole && a.sink != nullptr && r < j.rows) denom += exp2f(__ldg(a.sink + (j.row0 + r) % a.jobs.h_q) * kLog2e - mref);
-                    factor = 1.0f / denom;
+                    factor = (whole ? 1.0f : kPartScale) / denom;
                 }
                 sts_f32(alpha_s + 4 * r, factor);
                 if (r < j.rows) {

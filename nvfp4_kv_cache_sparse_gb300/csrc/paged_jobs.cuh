@@ -61,6 +61,10 @@ __device__ __noinline__ Job job_info(const Jobs& a, int job) {
 constexpr float kMaxWeightLog2 = 15.9f;   // 2^15.9 < 65504
 __device__ __forceinline__ float new_reference(float zt, float zmin) { return zt - fminf(fmaxf(zt - zmin - 14.0f, 3.0f), 12.0f); }
 
+// Parts of cut rows are f16 outputs times this: |V| is at most 6 x 448 (and 16 times that below 65504), and what is
+// rounded to steps of f16 below 2^-14 should be small against the smallest V other than 0, 2^-10.
+constexpr float kPartScale = 16.0f;
+
 // Slot of the token at position pos of a sequence; -1: none of the `keys` first, -2: its page is outside the pool.
 __device__ __forceinline__ int slot_of(const Jobs& a, int seq, int keys, int pos) {
     if (pos >= keys) return -1;

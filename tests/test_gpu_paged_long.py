@@ -69,3 +69,25 @@ def test_keys_far_below_the_first_one_keep_their_share(R, h_q, batch, n):
     err = np.abs(out - want)
     assert np.all(err <= tol), f"{np.max(err / tol):.3g} times the bound"
     assert np.all(np.abs(lse - (gap + np.log(S))) <= 2.0 ** -16 + sums + 2.0 ** -22 * gap)
+
+
+@pytest.mark.parametrize("R", [352, 432])
+@pytest.mark.parametrize("h_q,batch,n", [(16, 76, 2048), (16, 1, 9000), (64, 20, 2048), (128, 3, 5000)])
+def test_small_outputs_of_cut_rows(R, h_q, batch, n):
+    """The bounds of the test above with the smallest value other than 0, 2^-10, and rows that are cut: a part is held in f16
+    after a scale of 16, so that it is off by 2^-11 of itself and at least by 2^-29."""
+    recs, _ = shared_pool(R, np.ones(512))
+    recs[1:, :256] = 0x91                            # codes 0.5 and -0.5
+    recs[1:, 320 if R == 352 else 256:][:, :32] = 0x01   # scales 2^-9
+    v = oracle.dequant_records(recs)[1, :512]
+    assert np.all(np.abs(v) == 2.0 ** -10)
+    q, gap = queries(h_q, [12.0, 13.0, 14.0, 15.0, 16.0, 17.0])
+    out, lse = call(recs, batch, n, q)
+    N, p = n - 1, np.exp(-gap)
+    S = 1 + N * p
+    want = (N * p / S)[:, None] * v
+    k = np.clip(gap / np.log(2) - 14, 3, 12)
+    rel = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -16 + n / 128 * 2.0 ** -24 + n / 16 * 2.0 ** -23
+    tol = rel * np.abs(want) + (2.0 ** -25 * 2.0 ** -k * N / S)[:, None] * np.abs(v) + 2.0 ** -29
+    err = np.abs(out - want)
+    assert np.all(err <= tol), f"{np.max(err / tol):.3g} times the bound"
