@@ -91,3 +91,26 @@ def test_small_outputs_of_cut_rows(R, h_q, batch, n):
     tol = rel * np.abs(want) + (2.0 ** -25 * 2.0 ** -k * N / S)[:, None] * np.abs(v) + 2.0 ** -29
     err = np.abs(out - want)
     assert np.all(err <= tol), f"{np.max(err / tol):.3g} times the bound"
+
+
+@pytest.mark.parametrize("h_q,batch", [(1, 40_000), (16, 40_000), (24, 40_000), (1, 10_000_000)])
+def test_padding_between_two_sequences(h_q, batch):
+    # a CTA's run spans the gap; read one length at a time, the largest took longer than the waits of its other warps last
+    rng = np.random.default_rng(batch)
+    ps, n0, n1 = 4096, 169 * 64, 151 * 64 - 5
+    lat = synth.bf16_from_f32(rng.standard_normal((ps, 512)).astype(np.float32))
+    recs = oracle.quantize_records(synth.bf16_bits(lat), synth.bf16_bits(synth.bf16_from_f32(np.zeros((ps, 64), np.float32))), 352)
+    v = oracle.dequant_records(recs)[:, :512]
+    lens = torch.zeros(batch, dtype=torch.int32, device=DEV)
+    lens[0], lens[-1] = n0, n1
+    table = torch.zeros((batch, 3), dtype=torch.int32, device=DEV)     # one page, named by every entry
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = torch.zeros((batch, 1, h_q, 576), dtype=torch.bfloat16, device=DEV)
+    out, lse = lib.paged_mla_decode(q, torch.from_numpy(recs).to(DEV), table, lens, 1.0, page_size=ps, dev_status=status)
+    assert int(status.item()) == 0
+    assert not out[1:-1].any() and bool(torch.isneginf(lse[1:-1]).all())
+    for b, n in ((0, n0), (-1, n1)):                                   # scores 0: means over the tokens
+        seen = np.bincount(np.arange(n) % ps, minlength=ps) / n
+        want, size = seen @ v, seen @ np.abs(v)
+        assert np.all(np.abs(out[b, 0].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * size + 2.0 ** -28)
+        assert np.all(np.abs(lse[b, 0].double().cpu().numpy() - np.log(n)) <= 2.0 ** -18)
