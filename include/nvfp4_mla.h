@@ -297,11 +297,14 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s
  *                lse = -inf.
  *   workspace    device scratch of at least ..._workspace_size bytes, 256-byte aligned; needs no
  *                initialization. Calls that may overlap on the GPU need one each.
- * Precision: as nvfp4_sparse_mla_decode on NVFP4 records (parts of a row are normalized outputs in
- * f16 steps of at least 2^-28, joined in fp32). A weight e^z is held in f16: off by 2^-11 of itself, and at least by 2^-28 of the row's
- * largest weight (down to 2^-37 where that one outweighs whole quarters of its tile of 64 or 128 keys by more
- * than 2^17, as an attention sink does). Over n tokens that is at most 2^-28 sum|V| / (sum of the weights over the
- * largest one), which counts where V is 0 for the few keys that hold most of the weight and n passes some 10^5. A NaN in a query or in a record makes NaN the rows that see it, and only those.
+ * batch * s_q must stay below 2^24.
+ * Precision: as nvfp4_sparse_mla_decode on NVFP4 records (parts of a row are normalized outputs in f16,
+ * in steps of at least 2^-28, joined in fp32). A weight e^z is held in f16: off by 2^-11 of itself, and at
+ * least by 2^-28 of the row's largest weight (down to 2^-37 where that one outweighs whole quarters of
+ * its tile of 64 or 128 keys by more than 2^17, as an attention sink does). Over n tokens that is at most
+ * 2^-28 sum|V| / (sum of the weights over the largest one), which counts where V is 0 for the few keys
+ * that hold most of the weight and n passes some 10^5. A NaN in a query or in a record makes NaN the rows
+ * that see it, and only those.
  */
 NVFP4_MLA_API int nvfp4_paged_mla_decode(const void* q, const uint8_t* cache, int64_t num_pages, int32_t page_size,
                                          int32_t record_bytes, const int32_t* page_table, int64_t table_stride,
@@ -351,7 +354,9 @@ NVFP4_MLA_API int nvfp4_mla_fork_sequences(int32_t* page_table, int64_t table_st
  *    finished, drafted tokens that were rejected. These pages may be taken by the same call.
  *  - A longer one takes the lowest free pages, sequence by sequence. If its last page is partly
  *    filled and shared, it first takes a page of its own for it, into which the records it holds are
- *    copied in every cache (`caches`, as in copy_pages; num_caches 0: no records are copied).
+ *    copied in every cache (`caches`, as in copy_pages; num_caches 0: no records are copied). The counts
+ *    before the call decide: if all k holders of such a page grow in one call, each takes a page of its
+ *    own, k in all, and the shared one is free behind the call (not within it).
  *  - slots (int64 [batch, max_new], 8-byte aligned; unused when max_new is 0) receives the slots of
  *    the first max_new new tokens of each sequence, -1 behind its last one: the slot_mapping of the
  *    append that writes them.

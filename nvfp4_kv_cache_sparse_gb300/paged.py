@@ -191,7 +191,7 @@ def resize_sequences(caches: Sequence[torch.Tensor], page_table: torch.Tensor, s
                      workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Give each sequence the length ``new_lens[b]`` (int32 [batch]): pages are given back (0 frees a
     sequence) or taken, a shared partly filled last page is copied before its sequence grows into it (in
-    every cache; ``caches`` may be empty). Returns the slots of the first ``max_new`` new tokens of each
+    every cache; ``caches`` may be empty; where all its holders grow at once, every one of them takes a page). Returns the slots of the first ``max_new`` new tokens of each
     sequence, int64 [batch, max_new], -1 where there is none: the slot_mapping of their append. With too few
     free pages no sequence grows (DEV_PAGES_EXHAUSTED)."""
     b, width, stride = _table(page_table, seq_lens)
