@@ -44,7 +44,7 @@ PEAKS_FALLBACK = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # DRAM bytes (read + write) of one decode_pair_kernel launch on this workload, from an ncu
 # capture (dram__bytes_read.sum + dram__bytes_write.sum), keyed by the hash of the decode code
 # (comments removed) it was taken with; reported as null once that code changes.
-NCU_TRAFFIC = {"5356eb35f52e": 34267392 + 48128}
+NCU_TRAFFIC = {"8d73f376ca96": 34267392 + 41472}
 DECODE_CALLS_TIMED = 128   # the decode call alone: 16 laps of 8 back-to-back calls
 
 

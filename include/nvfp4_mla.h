@@ -288,8 +288,9 @@ NVFP4_MLA_API int nvfp4_paged_mla_decode_workspace_size(int32_t batch, int32_t s
  *                Query i of sequence b has position seq_lens[b] - s_q + i; its record and those of
  *                the tokens before it are in the cache already.
  *   cache        uint8 [num_pages * page_size, record_bytes & 0xFFFF], 16-byte aligned.
- *   record_bytes 352, 352 | NVFP4_MLA_SCALES_BLOCK_ORDER or 432 (656-byte fp8 records are not
- *                supported by this call: NVFP4_MLA_ERR_UNSUPPORTED).
+ *   record_bytes 352, 352 | NVFP4_MLA_SCALES_BLOCK_ORDER or 432. 656-byte fp8 records are refused
+ *                (NVFP4_MLA_ERR_UNSUPPORTED): the kernels convert e2m1 codes, and an e4m3 value times its
+ *                fp32 scale is no f16 number, which their exact keys rest on.
  *   h_q          1 to 128.
  *   sm_scale, attn_sink, out, lse: as in nvfp4_sparse_mla_decode, the sum running over the tokens
  *                at positions 0 .. seq_lens[b] - s_q + i. A query with a negative position (a

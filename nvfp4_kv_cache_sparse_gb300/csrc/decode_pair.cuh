@@ -58,7 +58,7 @@
 // is announced to the softmax two tiles ahead; only then does it look up the pages of its keys itself (looked
 // up for every tile: 1320 against 1241 us for 2 chunks of 256 tokens x 64 heads).
 // Measured: 2 chunks of 256 tokens x 64 heads over up to 16640 tokens 0.92 ms, 1.11 PFLOP/s (58% of a library's product);
-// 32 sequences of up to 8192 tokens x 2 tokens x 128 heads 118 us. A tile of 128 keys takes 2.3 us (tensor pipe 55%
+// 32 sequences of up to 8192 tokens x 2 tokens x 128 heads 115 us. A tile of 128 keys takes 2.3 us (tensor pipe 55%
 // busy, issue slots 57%, shared-memory accesses 58%): K, V and S are single buffers, so conversion, QK, softmax and PV
 // of a tile wait for one another in turn; a segment adds 11 us of its own (q 4.5, output 3.3, barriers and first tile).
 #pragma once

@@ -77,8 +77,8 @@ paged_join_kernel(const uint16_t* __restrict__ part_out, const float* __restrict
 }  // namespace
 
 // Up to 16 rows one CTA per SM (paged_decode_few.cu), above that CTA pairs (paged_decode_pair.cu).
-// 64 sequences of 1024 to 32768 tokens, few / pairs: 16 rows 209 / 329 us, 32 rows (two jobs of 16) 377 / 323 us;
-// 8 sequences of up to 8192 tokens: 16 rows 32 / 32 us, 32 rows 40 / 34 us.
+// One CTA / pairs at 16 rows: 64 sequences of 1024 to 32768 tokens 166 / 276 us, 8 of up to 8192 tokens 30 / 32 us. The one-CTA
+// kernel holds 16 rows; 17 and 32 rows on pairs take 276 and 277 us, 33 us (a pair's 128 rows are filled up).
 int paged_row_tile(int64_t rows_per_seq) { return rows_per_seq <= 16 ? 16 : 128; }
 
 namespace {

@@ -39,7 +39,7 @@
 // with a NaN scale likewise; P is 0 for a key that a row does not see and NaN for a NaN key that it
 // sees.
 //
-// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 171 to 179 us, 2.2 TB/s, where
+// What bounds it. 64 sequences of 1024 to 32768 tokens, 16 heads, 352-byte records (382 MB): 166 to 172 us, 2.3 TB/s, where
 // the records alone take 56 us. A tile takes about 1.5 us: its converters' chain (barrier, scales, two blocks of
 // conversion and stores, fence: 2600 clk) and the ring, whose blocks live through the QK, the softmax and the PV of
 // their tile (ring of 10 blocks 197 us, of 11 192). Of the shared memory's cycles the threads' accesses take 67% and

@@ -1,9 +1,10 @@
 // paged_jobs.cuh -- how attention through a page table is cut into work: jobs (a sequence and a tile of its
-// query rows), their tiles of keys, and the runs of tiles that CTAs or CTA pairs take.
+// query rows), their tiles of keys, and the runs of tiles that the CTAs of the one-CTA kernel take.
 //
 // The s_q * h_q query rows of a sequence lie one behind the other in q; rows row0 .. row0 + rows - 1 of a
-// job share every key that is dequantized. The tiles of all jobs, one job behind the other, are cut into
-// equal runs, whatever the lengths are: they are read on the device, so a captured call follows them.
+// job share every key that is dequantized. For one CTA each (paged_decode_few.cu) the tiles of all jobs, one job behind
+// the other, are cut into equal runs; CTA pairs take the segments that a plan kernel cuts the jobs into
+// (paged_decode_pair.cu). Lengths are read on the device, so a captured call follows them.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -73,7 +74,7 @@ __device__ __forceinline__ int slot_of(const Jobs& a, int seq, int keys, int pos
     return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
-// Where run c of (at most) `runs` begins, its tiles, and the tiles of all jobs. The prefix sum over the jobs'
+// Where run c of (at most) `runs` begins, its tiles, and the tiles of all jobs (one-CTA kernel). The prefix sum over the jobs'
 // tiles takes a contiguous piece of the jobs per thread; scratch: int64 [33 + 2], shared. Block-collective.
 struct Run {
     int64_t total, runs;      // tiles of all jobs; runs that are not empty
