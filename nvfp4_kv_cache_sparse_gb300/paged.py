@@ -190,10 +190,11 @@ def resize_sequences(caches: Sequence[torch.Tensor], page_table: torch.Tensor, s
                      new_lens: torch.Tensor, max_new: int = 0, page_size: int = 64, slots: Optional[torch.Tensor] = None,
                      workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Give each sequence the length ``new_lens[b]`` (int32 [batch]): pages are given back (0 frees a
-    sequence) or taken, a shared partly filled last page is copied before its sequence grows into it (in
-    every cache; ``caches`` may be empty; where all its holders grow at once, every one of them takes a page). Returns the slots of the first ``max_new`` new tokens of each
-    sequence, int64 [batch, max_new], -1 where there is none: the slot_mapping of their append. With too few
-    free pages no sequence grows (DEV_PAGES_EXHAUSTED)."""
+    sequence) or taken, a shared partly filled last page is copied before its sequence grows into it (in every
+    cache; ``caches`` may be empty; where all its holders grow at once, every one of them takes a page).
+    Returns the slots of the first ``max_new`` new tokens of each sequence, int64 [batch, max_new], -1 where
+    there is none: the slot_mapping of their append. With too few free pages no sequence grows
+    (DEV_PAGES_EXHAUSTED)."""
     b, width, stride = _table(page_table, seq_lens)
     pages = _refs(page_refs)
     _need(new_lens.dtype == torch.int32 and new_lens.dim() == 1 and new_lens.shape[0] == b and new_lens.is_contiguous(),
