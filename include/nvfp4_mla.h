@@ -390,6 +390,85 @@ NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_ca
                                           void* stream);
 
 /*
+ * ---- Heads and latents --------------------------------------------------------------------------
+ *
+ * The calls below stand around the latent attention of one layer. With c the latent (512) of a token, head h's key
+ * is W_uk[h] c (128 dims) beside the 64 RoPE dims that all heads share, and its value W_uv[h] c (128 dims).
+ *   kv_b  bf16 [h_q, 256, 512]: rows 0-127 of head h are W_uk[h], rows 128-255 W_uv[h].
+ * Two forms of the attention give the same result:
+ *   absorbed  nvfp4_mla_absorb_query -> nvfp4_paged_mla_decode or nvfp4_sparse_mla_decode ->
+ *             nvfp4_mla_project_values. The cache is read as it stands: for single tokens and short chunks.
+ *   expanded  nvfp4_paged_mla_expand -> nvfp4_ragged_mla_attention. 640 instead of 2176 FLOP per query, key and head,
+ *             after 262144 per key and head: for chunks of some 200 tokens and more.
+ * All tensors are bf16, sums run in fp32 and are rounded once; h_q is 1 to 128, other values return
+ * NVFP4_MLA_ERR_UNSUPPORTED. Strides are in elements and multiples of 8, inner strides 1; inputs are 16-byte aligned, outputs
+ * contiguous and 32-byte aligned. The stride of a dimension of one entry is not looked at. Row counts stay below 2^31 - 4096.
+ * Sequences lie packed, one behind the other: sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32
+ * [batch + 1], device, not decreasing; entries are read as clamped to [0, rows], a decrease as an empty sequence).
+ * Rows from cu_seqlens[batch] on are neither read nor written, so buffers may be larger than what a batch fills, and a
+ * captured call follows the lengths of its replay. A pipeline wait that gives up sets NVFP4_MLA_DEV_TIMEOUT.
+ */
+
+/*
+ * out[t, h, 0:512] = W_uk[h]^T q[t, h, 0:128]; out[t, h, 512:576] = q[t, h, 128:192], rotated where positions is not NULL.
+ *   q              [num_tokens, h_q, 192], any token and head stride.
+ *   positions      int64 [num_tokens] or NULL; cos_table, sin_table fp32 [num_positions, 32], 16-byte aligned; rotate_half 1:
+ *                  pairs (f, f + 32), 0: pairs (2f, 2f + 1), as in nvfp4_mla_norm_rope_quantize_append. A token whose
+ *                  position lies outside sets NVFP4_MLA_DEV_POSITION_OUT_OF_RANGE; its RoPE dims of out are left as they were.
+ *   out            [num_tokens, h_q, 576]: the q of the decode calls.
+ */
+NVFP4_MLA_API int nvfp4_mla_absorb_query(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* kv_b,
+                                         int64_t kv_b_row_stride, int64_t kv_b_head_stride, const int64_t* positions,
+                                         const float* cos_table, const float* sin_table, int64_t num_positions,
+                                         int32_t rotate_half, int64_t num_tokens, int32_t h_q, void* out,
+                                         uint32_t* dev_status, void* stream);
+
+/*
+ * out[t, h, 0:128] = W_uv[h] latent[t, h, 0:512]: the heads' outputs from the decode calls' out.
+ */
+NVFP4_MLA_API int nvfp4_mla_project_values(const void* latent, int64_t latent_token_stride, int64_t latent_head_stride,
+                                           const void* kv_b, int64_t kv_b_row_stride, int64_t kv_b_head_stride,
+                                           int64_t num_tokens, int32_t h_q, void* out, uint32_t* dev_status, void* stream);
+
+/*
+ * Keys and values of the first cu_seqlens[b + 1] - cu_seqlens[b] tokens of each sequence from their records in pages
+ * (see "Sequences in pages"; record_bytes as in nvfp4_paged_mla_decode):
+ *   kv     [num_rows, h_q, 256]: W_uk[h] c, then W_uv[h] c.
+ *   k_pe   [num_rows, 64], 16-byte aligned: the records' RoPE dims.
+ * A token whose table entry names no page of the pool, or that lies behind the table's last entry, sets
+ * NVFP4_MLA_DEV_INDEX_OUT_OF_RANGE and gets zeros.
+ */
+NVFP4_MLA_API int nvfp4_paged_mla_expand(const uint8_t* cache, int64_t num_pages, int32_t page_size, int32_t record_bytes,
+                                         const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                         const int32_t* cu_seqlens, int32_t batch, const void* kv_b, int64_t kv_b_row_stride,
+                                         int64_t kv_b_head_stride, int32_t h_q, void* kv, void* k_pe, int64_t num_rows,
+                                         uint32_t* dev_status, void* stream);
+
+/* Scratch size of nvfp4_ragged_mla_attention: one size for every call. */
+NVFP4_MLA_API int nvfp4_ragged_mla_attention_workspace_size(size_t* bytes);
+
+/*
+ * Attention of the last lq tokens of each sequence over its lk tokens up to their own position: query i sees the keys
+ * 0 .. lk - lq + i of its sequence.
+ *   q                [num_q, h_q, 192], RoPE dims last, rotated already; any token and head stride.
+ *   kv, k_pe         [num_k, h_q, 256] and [num_k, 64] as from nvfp4_paged_mla_expand; any token and head stride.
+ *   sm_scale, attn_sink, lse: as in nvfp4_sparse_mla_decode; lse [num_q, h_q].
+ *   out              [num_q, h_q, 128].
+ *   workspace        at least ..._workspace_size bytes, 256-byte aligned; needs no initialization. Calls that may overlap on
+ *                    the GPU need one each.
+ * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^24.
+ * Precision: weights e^z are rounded to bf16 (2^-8 of themselves, however small), row sums are of the unrounded ones.
+ * A NaN or infinity in a query or a key makes NaN the rows that see it, one in a value the rows of its sequence that see it and
+ * those up to 255 rows before them; other sequences' rows never.
+ */
+NVFP4_MLA_API int nvfp4_ragged_mla_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_q,
+                                             const void* kv, int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe,
+                                             int64_t k_pe_stride, int64_t num_k, const int32_t* cu_seqlens_q,
+                                             const int32_t* cu_seqlens_k, int32_t batch, int32_t h_q, float sm_scale,
+                                             const float* attn_sink, void* out, float* lse, void* workspace,
+                                             size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
  * Self-test of the decode's wait bound (no counterpart on the pages). Every pipeline wait in
  * the decode kernel gives up after about one second (then the kernel sets
  * NVFP4_MLA_DEV_TIMEOUT, drains its own work and returns; the context stays usable). This call

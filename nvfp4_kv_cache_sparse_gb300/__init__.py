@@ -54,6 +54,11 @@ EXPORTED = (
     "nvfp4_mla_fork_sequences",
     "nvfp4_mla_resize_sequences",
     "nvfp4_mla_compact_pages",
+    "nvfp4_mla_absorb_query",
+    "nvfp4_mla_project_values",
+    "nvfp4_paged_mla_expand",
+    "nvfp4_ragged_mla_attention_workspace_size",
+    "nvfp4_ragged_mla_attention",
 )
 
 _lib: Optional[ctypes.CDLL] = None
@@ -106,7 +111,12 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                         ("nvfp4_mla_copy_pages", [P, i32, i64, i32, i32, P, P, i32, P, P]),
                         ("nvfp4_mla_fork_sequences", [P, i64, i32, P, i32, P, i64, i32, P, P, i32, P, sz, P, P]),
                         ("nvfp4_mla_resize_sequences", [P, i64, i32, P, P, i32, P, i64, i32, P, i32, i32, P, i32, P, sz, P, P]),
-                        ("nvfp4_mla_compact_pages", [P, i32, i32, P, i64, P, i64, i32, P, i32, P, P, i64, i32, P, P, P, sz, P, P])):
+                        ("nvfp4_mla_compact_pages", [P, i32, i32, P, i64, P, i64, i32, P, i32, P, P, i64, i32, P, P, P, sz, P, P]),
+                        ("nvfp4_mla_absorb_query", [P, i64, i64, P, i64, i64, P, P, P, i64, i32, i64, i32, P, P, P]),
+                        ("nvfp4_mla_project_values", [P, i64, i64, P, i64, i64, i64, i32, P, P, P]),
+                        ("nvfp4_paged_mla_expand", [P, i64, i32, i32, P, i64, i32, P, i32, P, i64, i64, i32, P, P, i64, P, P]),
+                        ("nvfp4_ragged_mla_attention_workspace_size", [ctypes.POINTER(sz)]),
+                        ("nvfp4_ragged_mla_attention", [P, i64, i64, i64, P, i64, i64, P, i64, i64, P, P, i32, i32, f32, P, P, P, P, sz, P, P])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = types
     _lib = lib
@@ -278,3 +288,5 @@ def selftest_wait_timeout(device=None, stream=None) -> Tuple[int, int]:
 
 from .paged import (compact_pages, copy_pages, fork_sequences, paged_mla_decode, paged_workspace_size,  # noqa: E402,F401
                     pages_workspace_size, resize_sequences)
+from .heads import (mla_absorb_query, mla_project_values, paged_mla_expand, ragged_mla_attention,  # noqa: E402,F401
+                    ragged_workspace_size)

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libnvfp4mla.so")
 SOURCES = ["api.cu", "quantize_append.cu", "sparse_decode.cu", "sparse_decode_pair.cu", "sparse_decode_h64.cu",
            "decode_no_alloc.cu", "paged_decode.cu", "paged_decode_few.cu", "paged_decode_pair.cu",
-           "page_ops.cu"]
+           "page_ops.cu", "head_products.cu", "paged_expand.cu", "ragged_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/nvfp4_mla.h"
 #include "launch.h"
@@ -114,6 +115,22 @@ int check_caches(uint8_t* const* caches, int32_t num_caches, int32_t record_byte
     for (int i = 0; i < num_caches; ++i)
         if (!caches[i] || !aligned(caches[i], 16)) return NVFP4_MLA_ERR_INVALID_ARG;
     return NVFP4_MLA_OK;
+}
+
+// Sizes of the calls around the latent attention: rows and heads.
+int check_heads(int64_t rows, int32_t h_q) {
+    if (rows < 0 || rows > 0x7FFFF000) return NVFP4_MLA_ERR_INVALID_ARG;
+    return h_q < 1 || h_q > 128 ? NVFP4_MLA_ERR_UNSUPPORTED : NVFP4_MLA_OK;
+}
+
+// Whether TMA can read bf16 [outer, mid, inner] with these strides (elements): a 16-byte aligned base, strides that are multiples
+// of 16 bytes. The stride of a dimension of one entry is never used and may be anything.
+bool strides_ok(const void* base, int64_t outer, int64_t mid, int64_t inner, int64_t* outer_stride, int64_t* mid_stride) {
+    if (outer == 1) *outer_stride = inner;
+    if (mid == 1) *mid_stride = inner;
+    for (const int64_t s : {*outer_stride, *mid_stride})
+        if (s < 8 || s % 8 != 0 || s >= (int64_t(1) << 38)) return false;
+    return base != nullptr && aligned(base, 16);
 }
 
 // Workspaces of the page calls, in 32-bit words. Resize: the free pages it hands out, four words per
@@ -501,6 +518,163 @@ NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_ca
     a.status = dev_status;
     const nvfp4mla::PoolArgs pool = {caches, num_caches, a.num_pages, a.shift, record_width(record_bytes)};
     const cudaError_t e = nvfp4mla::launch_compact(a, pool, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_mla_absorb_query(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* kv_b,
+                                         int64_t kv_b_row_stride, int64_t kv_b_head_stride, const int64_t* positions,
+                                         const float* cos_table, const float* sin_table, int64_t num_positions,
+                                         int32_t rotate_half, int64_t num_tokens, int32_t h_q, void* out,
+                                         uint32_t* dev_status, void* stream) {
+    int st = check_heads(num_tokens, h_q);
+    if (st != NVFP4_MLA_OK) return st;
+    if (num_positions < 0 || (rotate_half != 0 && rotate_half != 1)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return NVFP4_MLA_OK;
+    if (!strides_ok(q, num_tokens, h_q, 192, &q_token_stride, &q_head_stride) || !strides_ok(kv_b, h_q, 256, 512, &kv_b_head_stride, &kv_b_row_stride))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!out || !aligned(out, 32) || !aligned(positions, 8) || !aligned(cos_table, 16) || !aligned(sin_table, 16)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (positions && (!cos_table || !sin_table)) return NVFP4_MLA_ERR_INVALID_ARG;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::HeadProductArgs p = {};
+    p.in = q;
+    p.in_token_stride = q_token_stride;
+    p.in_head_stride = q_head_stride;
+    p.tokens = num_tokens;
+    p.heads = h_q;
+    p.kv_b = kv_b;
+    p.w_row_stride = kv_b_row_stride;
+    p.w_head_stride = kv_b_head_stride;
+    p.positions = positions;
+    p.cos_table = cos_table;
+    p.sin_table = sin_table;
+    p.num_positions = num_positions;
+    p.rotate_half = rotate_half;
+    p.out = out;
+    p.status = dev_status;
+    const cudaError_t e = nvfp4mla::launch_head_product(p, true, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_mla_project_values(const void* latent, int64_t latent_token_stride, int64_t latent_head_stride,
+                                           const void* kv_b, int64_t kv_b_row_stride, int64_t kv_b_head_stride,
+                                           int64_t num_tokens, int32_t h_q, void* out, uint32_t* dev_status, void* stream) {
+    int st = check_heads(num_tokens, h_q);
+    if (st != NVFP4_MLA_OK) return st;
+    if (num_tokens == 0) return NVFP4_MLA_OK;
+    if (!strides_ok(latent, num_tokens, h_q, 512, &latent_token_stride, &latent_head_stride) ||
+        !strides_ok(kv_b, h_q, 256, 512, &kv_b_head_stride, &kv_b_row_stride) || !out || !aligned(out, 32))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::HeadProductArgs p = {};
+    p.in = latent;
+    p.in_token_stride = latent_token_stride;
+    p.in_head_stride = latent_head_stride;
+    p.tokens = num_tokens;
+    p.heads = h_q;
+    p.kv_b = kv_b;
+    p.w_row_stride = kv_b_row_stride;
+    p.w_head_stride = kv_b_head_stride;
+    p.out = out;
+    p.status = dev_status;
+    const cudaError_t e = nvfp4mla::launch_head_product(p, false, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_paged_mla_expand(const uint8_t* cache, int64_t num_pages, int32_t page_size, int32_t record_bytes,
+                                         const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                         const int32_t* cu_seqlens, int32_t batch, const void* kv_b, int64_t kv_b_row_stride,
+                                         int64_t kv_b_head_stride, int32_t h_q, void* kv, void* k_pe, int64_t num_rows,
+                                         uint32_t* dev_status, void* stream) {
+    int st = check_pages(batch, max_pages, num_pages, page_size, table_stride);
+    if (st == NVFP4_MLA_OK) st = check_heads(num_rows, h_q);
+    if (st != NVFP4_MLA_OK) return st;
+    if (!record_ok(record_bytes) || record_width(record_bytes) == 656) return NVFP4_MLA_ERR_UNSUPPORTED;
+    if (batch == 0 || num_rows == 0) return NVFP4_MLA_OK;
+    if (!cu_seqlens || !kv || !k_pe || (max_pages > 0 && !page_table) || (num_pages > 0 && !cache)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!aligned(cache, 16) || !aligned(page_table, 4) || !aligned(cu_seqlens, 4) || !aligned(kv, 32) || !aligned(k_pe, 16))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!strides_ok(kv_b, h_q, 256, 512, &kv_b_head_stride, &kv_b_row_stride)) return NVFP4_MLA_ERR_INVALID_ARG;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::ExpandArgs p = {};
+    p.cache = cache;
+    p.num_pages = static_cast<int>(num_pages);
+    p.page_shift = page_shift_of(page_size);
+    p.record_bytes = record_width(record_bytes);
+    p.block_scales = block_scales(record_bytes);
+    p.page_table = page_table;
+    p.table_stride = table_stride;
+    p.width = max_pages;
+    p.starts = cu_seqlens;
+    p.batch = batch;
+    p.kv_b = kv_b;
+    p.w_row_stride = kv_b_row_stride;
+    p.w_head_stride = kv_b_head_stride;
+    p.heads = h_q;
+    p.rows = num_rows;
+    p.kv = kv;
+    p.k_pe = k_pe;
+    p.status = dev_status;
+    const cudaError_t e = nvfp4mla::launch_paged_expand(p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
+}
+
+NVFP4_MLA_API int nvfp4_ragged_mla_attention_workspace_size(size_t* bytes) {
+    if (!bytes) return NVFP4_MLA_ERR_INVALID_ARG;
+    *bytes = round256(nvfp4mla::ragged_workspace_bytes());
+    return NVFP4_MLA_OK;
+}
+
+NVFP4_MLA_API int nvfp4_ragged_mla_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_q,
+                                             const void* kv, int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe,
+                                             int64_t k_pe_stride, int64_t num_k, const int32_t* cu_seqlens_q,
+                                             const int32_t* cu_seqlens_k, int32_t batch, int32_t h_q, float sm_scale,
+                                             const float* attn_sink, void* out, float* lse, void* workspace,
+                                             size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+    int st = check_heads(num_q, h_q);
+    if (st == NVFP4_MLA_OK) st = check_heads(num_k, h_q);
+    if (st != NVFP4_MLA_OK) return st;
+    if (batch < 0 || batch > (1 << 24)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (batch == 0 || num_q == 0) return NVFP4_MLA_OK;
+    if (!cu_seqlens_q || !cu_seqlens_k || !out || !lse) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(attn_sink, 4) || !aligned(out, 32) || !aligned(lse, 4))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    if (!strides_ok(q, num_q, h_q, 192, &q_token_stride, &q_head_stride)) return NVFP4_MLA_ERR_INVALID_ARG;
+    if (num_k == 0) {   // nothing is read of them: any address that TMA accepts
+        kv = k_pe = q;
+        kv_token_stride = kv_head_stride = 256;
+        k_pe_stride = 64;
+    }
+    int64_t one = 1;
+    if (!strides_ok(kv, num_k, h_q, 256, &kv_token_stride, &kv_head_stride) || !strides_ok(k_pe, num_k, 1, 64, &k_pe_stride, &one))
+        return NVFP4_MLA_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, round256(nvfp4mla::ragged_workspace_bytes()));
+    if (st != NVFP4_MLA_OK) return st;
+    const int sms = device_sm_count(&st);
+    if (sms <= 0) return st;
+    nvfp4mla::RaggedArgs p = {};
+    p.q = q;
+    p.q_token_stride = q_token_stride;
+    p.q_head_stride = q_head_stride;
+    p.rows_q = num_q;
+    p.kv = kv;
+    p.kv_token_stride = kv_token_stride;
+    p.kv_head_stride = kv_head_stride;
+    p.k_pe = k_pe;
+    p.pe_stride = k_pe_stride;
+    p.rows_k = num_k;
+    p.starts_q = cu_seqlens_q;
+    p.starts_k = cu_seqlens_k;
+    p.batch = batch;
+    p.heads = h_q;
+    p.sm_scale = sm_scale;
+    p.attn_sink = attn_sink;
+    p.out = out;
+    p.lse = lse;
+    p.status = dev_status;
+    const cudaError_t e = nvfp4mla::launch_ragged_attention(p, workspace, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? NVFP4_MLA_OK : NVFP4_MLA_ERR_CUDA;
 }
 

@@ -160,4 +160,63 @@ cudaError_t launch_resize(const ResizeArgs& a, const PoolArgs& pool, int sms, cu
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream);
 cudaError_t launch_compact(const CompactArgs& a, const PoolArgs& pool, int sms, cudaStream_t stream);
 
+
+// ---- around the latent attention (head_products.cu, paged_expand.cu, ragged_attention.cu)
+struct HeadProductArgs {
+    const void* in;              // absorb: q bf16 [tokens, heads, 192]; project: latent output bf16 [tokens, heads, 512]
+    int64_t in_token_stride, in_head_stride;
+    int64_t tokens;
+    int heads;
+    const void* kv_b;            // bf16 [heads, 256, 512]: 128 rows of the key's weights, 128 of the value's
+    int64_t w_row_stride, w_head_stride;
+    const int64_t* positions;    // absorb: nullable [tokens]
+    const float* cos_table;      // fp32 [num_positions, 32]
+    const float* sin_table;
+    int64_t num_positions;
+    int rotate_half;
+    void* out;                   // bf16 [tokens, heads, 576 or 128]
+    uint32_t* status;
+};
+cudaError_t launch_head_product(const HeadProductArgs& p, bool absorb, int sms, cudaStream_t stream);
+
+struct ExpandArgs {
+    const uint8_t* cache;        // [num_pages << page_shift, record_bytes]
+    int num_pages, page_shift;
+    int record_bytes;            // 352 or 432
+    bool block_scales;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int width;                   // entries of a page table row
+    const int32_t* starts;       // [batch + 1]
+    int batch;
+    const void* kv_b;
+    int64_t w_row_stride, w_head_stride;
+    int heads;
+    int64_t rows;                // rows of kv and k_pe
+    void* kv;                    // bf16 [rows, heads, 256]
+    void* k_pe;                  // bf16 [rows, 64]
+    uint32_t* status;
+};
+cudaError_t launch_paged_expand(const ExpandArgs& p, int sms, cudaStream_t stream);
+
+struct RaggedArgs {
+    const void* q;               // bf16 [rows_q, heads, 192]
+    int64_t q_token_stride, q_head_stride;
+    int64_t rows_q;
+    const void* kv;              // bf16 [rows_k, heads, 256]
+    int64_t kv_token_stride, kv_head_stride;
+    const void* k_pe;            // bf16 [rows_k, 64]
+    int64_t pe_stride;
+    int64_t rows_k;
+    const int32_t *starts_q, *starts_k;   // [batch + 1]
+    int batch, heads;
+    float sm_scale;
+    const float* attn_sink;      // nullable [heads]
+    void* out;                   // bf16 [rows_q, heads, 128]
+    float* lse;                  // [rows_q, heads]
+    uint32_t* status;
+};
+size_t ragged_workspace_bytes();
+cudaError_t launch_ragged_attention(const RaggedArgs& p, void* workspace, int sms, cudaStream_t stream);
+
 }  // namespace nvfp4mla

@@ -1,0 +1,649 @@
+// ragged_attention.cu -- attention of chunks of new tokens over their sequences' expanded keys and values (head dims 128 + 64
+// shared RoPE dims for scores, 128 for values), sequences of any lengths packed one behind the other.
+//
+//   z[i, n] = sm_scale (q[i, h, 0:128] . kv[n, h, 0:128] + q[i, h, 128:192] . k_pe[n]),   n <= lk - lq + i
+//   out[i, h] = sum_n e^z kv[n, h, 128:256] / (sum_n e^z + e^sink[h]),   lse[i, h] = log sum_n e^z
+// 640 FLOP per query, key and head against 2176 in the absorbed form, which works on the latents themselves: the tensor cores
+// bound it. One pass over the keys with a running reference m of each row: P = 2^(z log2 e - m) in bf16, whose range
+// is that of fp32, so that no weight is lost however far it lies below the largest; row sums and outputs in fp32. m moves
+// only when a score passes it by 2^8 (the output in tensor memory is rescaled then).
+//
+// A tile is 256 query rows of one sequence and head, in two halves of 128. S = Q K^T of a half is one tcgen05.mma chain
+// (M = 128 rows, N = 128 keys, K = 192) into tensor memory; a warpgroup per half turns it into P, which overwrites S
+// and feeds P V from tensor memory. While one half's softmax runs, the tensor cores work for the other. Keys and
+// values come through a ring of eight 16 KB units (a key block is three units of 128 keys x 64 dims, its values two
+// units of 64 keys x 128 dims).
+//
+// Tiles are of very different lengths and often fewer than SMs, so the CTAs, one per SM, take equal runs of (tile, head, block
+// of 128 keys) units, heads inside tiles: neighbouring tiles of a head are then read by several CTAs at about the same
+// time, from L2. A tile that two runs share leaves fp32 parts in the workspace, which a second kernel joins.
+#include "head_tiles.cuh"
+#include "launch.h"
+
+namespace nvfp4mla {
+namespace {
+
+using namespace tiles;
+
+constexpr int kUnits = 8;              // ring
+constexpr int kOffQ = 1024;
+constexpr int kOffRing = kOffQ + 6 * kBox;
+constexpr int kSmem = kOffRing + kUnits * kBox + 1024;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10;   // warps 0-3 and 4-7: softmax of the two halves
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;      // 2 x 128 x 208 + 128 x 88 = 384 x 168, the registers at launch
+constexpr int kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;              // two halves of 128 columns each
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMoveLog2 = 8.0f;      // a reference moves when a score passes it by 2^8
+constexpr int kExtra = 1;              // what a tile costs besides its blocks, in blocks
+constexpr int kMinRun = 2;
+constexpr int kMaxCtas = kPagedMaxSms;
+
+struct Ctl {
+    uint64_t full[kUnits], empty[kUnits];   // a unit is handed back by the products and by the warp that cleans values
+    uint64_t q_full[2], q_free[2];     // a half's queries landed; its last scores are done
+    uint64_t s_full[2];                // scores in tensor memory
+    uint64_t p_full[2];                // 4 warps: P written, O rescaled
+    uint64_t o_done[2];                // a block's P V is done
+    uint64_t v_clean[2];               // rows behind a sequence's end were zeroed (in turn: the ring has room for the values of two tiles)
+    uint64_t drain;
+    uint32_t tmem_base, abort;
+    // the first item of the CTA's run
+    int64_t u0, u1, total;
+    int seq, tile, head, b0;
+};
+static_assert(sizeof(Ctl) <= kOffQ, "control block");
+
+struct KernelArgs {
+    CUtensorMap q_map;                 // [rows_q, heads, 192], box 128 x 1 x 64
+    CUtensorMap k_map;                 // kv [rows_k, heads, 256], box 128 x 1 x 64
+    CUtensorMap v_map;                 // the same, box 64 x 1 x 64
+    CUtensorMap pe_map;                // [rows_k, 1, 64], box 128 x 1 x 64
+    RaggedArgs p;
+    float* part_out;                   // [2 CTAs, 256, 128], each divided by its own sum
+    float* part_lse;                   // [2 CTAs, 256], log2
+    int4* headers;                     // [CTAs]: first output row, rows, head, parts (0: no tile begins here and ends elsewhere)
+};
+
+struct Seq {
+    int q0, lq, k0, lk;
+};
+__device__ __forceinline__ int clamp_start(int v, int64_t rows) { return static_cast<int>(min(max(static_cast<int64_t>(v), int64_t(0)), rows)); }
+__device__ __forceinline__ Seq seq_at(const RaggedArgs& p, int b) {
+    Seq s;
+    s.q0 = clamp_start(__ldg(p.starts_q + b), p.rows_q);
+    s.k0 = clamp_start(__ldg(p.starts_k + b), p.rows_k);
+    s.lq = max(clamp_start(__ldg(p.starts_q + b + 1), p.rows_q) - s.q0, 0);
+    s.lk = max(clamp_start(__ldg(p.starts_k + b + 1), p.rows_k) - s.k0, 0);
+    return s;
+}
+__device__ __forceinline__ int tiles_of(const Seq& s) { return (s.lq + 255) >> 8; }
+// Key blocks of rows [0, rows) of a sequence: its last row sees the first lk - lq + rows keys.
+__device__ __forceinline__ int blocks_of(const Seq& s, int rows) {
+    const int keys = s.lk - s.lq + min(rows, s.lq);
+    return keys <= 0 ? 0 : (keys + 127) >> 7;
+}
+// Units of the first m tiles: a tile before the last one ends on a multiple of 256 rows, tile j has max(0, p + 2 (j + 1)) blocks
+// with p = ceil((lk - lq) / 128), and kExtra.
+__device__ __forceinline__ int64_t units_of(const Seq& s, int m) {
+    const int count = tiles_of(s);
+    if (m <= 0) return 0;
+    const int whole = m < count ? m : count - 1;            // tiles that are surely full
+    const int64_t pre = (s.lk - s.lq + 127) >> 7;           // (rounds up for negative ones too)
+    int64_t none = pre < 0 ? (-pre) >> 1 : 0;               // tiles without keys
+    if (none > whole) none = whole;
+    const int64_t a = none + 1, n = whole - none;           // j + 1 = a .. whole
+    int64_t sum = n * pre + n * (a + whole);
+    if (m >= count) sum += blocks_of(s, s.lq);
+    return sum + static_cast<int64_t>(kExtra) * (m < count ? m : count);
+}
+
+// A tile's part in a run.
+struct Item {
+    Seq s;
+    int head, row0;                    // rows row0 .. of the sequence
+    int from, count[2];                // first block; blocks of each half
+    bool used1;                        // the second half has rows
+    bool cut;
+    int slot;                          // of the part, where cut
+};
+
+// Calls f(item) for the items of the CTA's run, in order.
+template <typename F>
+__device__ __forceinline__ void for_items(const RaggedArgs& p, const Ctl* ctl, F f) {
+    int64_t left = ctl->u1 - ctl->u0;
+    int seq = ctl->seq, tile = ctl->tile, head = ctl->head, b0 = ctl->b0;
+    Item it;
+    if (left > 0) it.s = seq_at(p, seq);
+    while (left > 0) {
+        const int n0 = blocks_of(it.s, 256 * tile + 128), n = blocks_of(it.s, 256 * tile + 256), weight = n + kExtra;
+        const int take = static_cast<int>(min(left, static_cast<int64_t>(weight - b0))), b1 = b0 + take;
+        it.head = head;
+        it.row0 = 256 * tile;
+        it.used1 = it.s.lq > it.row0 + 128;
+        it.from = min(b0, n);
+        it.count[0] = max(min(b1, n0) - it.from, 0);
+        it.count[1] = it.used1 ? min(b1, n) - it.from : 0;
+        it.cut = b0 > 0 || b1 < weight;
+        it.slot = 2 * static_cast<int>(blockIdx.x) + (b0 > 0 ? 0 : 1);
+        if (!f(it)) return;
+        left -= take;
+        b0 = 0;
+        if (++head == p.heads) {
+            head = 0;
+            ++tile;
+            while (left > 0 && tile >= tiles_of(it.s)) {
+                it.s = seq_at(p, ++seq);
+                tile = 0;
+            }
+        }
+    }
+}
+
+// One warp: where the CTA's run begins. Also its header, where the run's last tile goes on in the next run.
+__device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane) {
+    const RaggedArgs& p = a.p;
+    const unsigned full = 0xffffffffu;
+    int64_t total = 0;
+    for (int b = 0; b < p.batch; b += 32) {
+        int64_t n = 0;
+        if (b + lane < p.batch) {
+            const Seq s = seq_at(p, b + lane);
+            n = units_of(s, tiles_of(s));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(full, n, o);
+        total += n;
+    }
+    total *= p.heads;
+    // (a run has at least kMinRun units: shorter ones would be all parts and joining)
+    const int64_t most = (total + kMinRun - 1) / kMinRun, g = most < gridDim.x ? most : gridDim.x, c = blockIdx.x;
+    const int64_t u0 = c < g ? total * c / g : 0, u1 = c < g ? total * (c + 1) / g : 0;
+    // the sequences that the first and the last unit lie in
+    int seq_of[2] = {0, 0};
+    int64_t at[2] = {0, 0};
+    const int64_t want[2] = {u0, u1 - 1};
+    if (u1 > u0) {
+        int64_t before = 0;
+        bool found[2] = {false, false};
+        for (int b = 0; b < p.batch && !(found[0] && found[1]); b += 32) {
+            int64_t n = 0;
+            if (b + lane < p.batch) {
+                const Seq s = seq_at(p, b + lane);
+                n = units_of(s, tiles_of(s)) * p.heads;
+            }
+            int64_t sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(full, sum, o);
+                if (lane >= o) sum += v;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const unsigned m = __ballot_sync(full, before + sum > want[e]);
+                if (!found[e] && m != 0u) {
+                    const int l = __ffs(m) - 1;
+                    seq_of[e] = b + l;
+                    at[e] = before + __shfl_sync(full, sum - n, l);
+                    found[e] = true;
+                }
+            }
+            before += __shfl_sync(full, sum, 31);
+        }
+    }
+    if (lane != 0) return;
+    int4 header = make_int4(0, 0, 0, 0);
+    int first[4] = {0, 0, 0, 0};
+    if (u1 > u0) {
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+            const Seq s = seq_at(p, seq_of[e]);
+            const int64_t off = want[e] - at[e];
+            int lo = 0, hi = tiles_of(s);                   // units_of(lo) * heads <= off < units_of(hi) * heads
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (units_of(s, mid) * p.heads <= off) lo = mid;
+                else hi = mid;
+            }
+            const int64_t in_tile = off - units_of(s, lo) * p.heads;
+            const int weight = blocks_of(s, 256 * lo + 256) + kExtra;
+            const int head = static_cast<int>(in_tile / weight), b = static_cast<int>(in_tile - static_cast<int64_t>(head) * weight);
+            if (e == 0) {
+                first[0] = seq_of[0], first[1] = lo, first[2] = head, first[3] = b;
+            } else {
+                const int64_t begin = want[1] - b, end = begin + weight;
+                if (begin >= u0 && end > u1) {
+                    int parts = 1;
+                    for (int64_t n = c + 1; n < g && total * n / g < end; ++n) ++parts;
+                    header = make_int4(s.q0 + 256 * lo, min(256, s.lq - 256 * lo), head, parts);
+                }
+            }
+        }
+    }
+    ctl->u0 = u0, ctl->u1 = u1, ctl->total = total;
+    ctl->seq = first[0], ctl->tile = first[1], ctl->head = first[2], ctl->b0 = first[3];
+    a.headers[c] = header;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __grid_constant__ KernelArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    Ctl* ctl = reinterpret_cast<Ctl*>(smem);
+    const uint32_t sbase = smem_addr(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const RaggedArgs& p = a.p;
+    if (warp == kWarpLoad && lane == 0) {
+        prefetch_map(&a.q_map);
+        prefetch_map(&a.k_map);
+        prefetch_map(&a.v_map);
+        prefetch_map(&a.pe_map);
+        for (int i = 0; i < kUnits; ++i) mbar_init(&ctl->full[i], 1), mbar_init(&ctl->empty[i], 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
+            mbar_init(&ctl->s_full[i], 1), mbar_init(&ctl->p_full[i], 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->v_clean[i], 1);
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0u;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(&ctl->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == kWarpFix) find_run(a, ctl, lane);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = ctl->tmem_base;
+    uint32_t* abort = &ctl->abort;
+    uint32_t* status = p.status;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kWarpLoad) {
+            if (lane == 0) {
+                int unit = 0, items[2] = {0, 0};
+                uint32_t phase = 1;
+                auto take = [&]() -> uint64_t* {            // the next unit of the ring, armed
+                    if (!wait_or_give_up(&ctl->empty[unit], phase, abort, status)) return nullptr;
+                    mbar_arrive_expect_tx(&ctl->full[unit], kBox);
+                    return &ctl->full[unit];
+                };
+                auto step = [&] {
+                    if (++unit == kUnits) unit = 0, phase ^= 1;
+                };
+                for_items(p, ctl, [&](const Item& it) -> bool {
+                    const int n = max(it.count[0], it.count[1]);
+                    if (n == 0) return true;
+                    auto load_q = [&](int h) -> bool {
+                        if (it.count[h] == 0) return true;
+                        if (!wait_or_give_up(&ctl->q_free[h], (items[h] & 1) ^ 1, abort, status)) return false;
+                        ++items[h];
+                        mbar_arrive_expect_tx(&ctl->q_full[h], 3 * kBox);
+                        for (int c = 0; c < 3; ++c)
+                            tma_load_3d(sbase + kOffQ + (3 * h + c) * kBox, &a.q_map, 64 * c, it.head, it.s.q0 + it.row0 + 128 * h, &ctl->q_full[h]);
+                        return true;
+                    };
+                    auto load_k = [&](int i) -> bool {
+                        const int row = it.s.k0 + 128 * (it.from + i);
+                        for (int c = 0; c < 3; ++c) {
+                            uint64_t* bar = take();
+                            if (bar == nullptr) return false;
+                            if (c < 2) tma_load_3d(sbase + kOffRing + unit * kBox, &a.k_map, 64 * c, it.head, row, bar);
+                            else tma_load_3d(sbase + kOffRing + unit * kBox, &a.pe_map, 0, 0, row, bar);
+                            step();
+                        }
+                        return true;
+                    };
+                    auto load_v = [&](int i) -> bool {
+                        const int row = it.s.k0 + 128 * (it.from + i);
+                        for (int c = 0; c < 2; ++c) {
+                            uint64_t* bar = take();
+                            if (bar == nullptr) return false;
+                            tma_load_3d(sbase + kOffRing + unit * kBox, &a.v_map, 128, it.head, row + 64 * c, bar);
+                            tma_load_3d(sbase + kOffRing + unit * kBox + kBox / 2, &a.v_map, 192, it.head, row + 64 * c, bar);
+                            step();
+                        }
+                        return true;
+                    };
+                    if (!load_q(0) || !load_k(0) || !load_q(1) || !load_v(0)) return false;
+                    for (int i = 1; i < n; ++i)
+                        if (!load_k(i) || !load_v(i)) return false;
+                    return true;
+                });
+            }
+            __syncwarp();
+        } else if (warp == kWarpMma) {
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false), idesc_o = idesc_bf16_f32(128, 128, false, true);
+                const uint64_t q0 = sdesc_sw128(sbase + kOffQ, 16, 1024);                // K-major: rows x dims
+                const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);             // K-major: keys x dims
+                const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);       // MN-major: dims x keys
+                int unit = 0, items[2] = {0, 0}, ps[2] = {0, 0}, cleans = 0;
+                uint32_t phase = 0;
+                auto wait_units = [&](int at, uint32_t ph, int n) -> bool {
+                    for (int c = 0; c < n; ++c) {
+                        if (!wait_or_give_up(&ctl->full[at], ph, abort, status)) return false;
+                        if (++at == kUnits) at = 0, ph ^= 1;
+                    }
+                    return true;
+                };
+                auto commit_units = [&](int at, int n) {
+                    for (int c = 0; c < n; ++c) {
+                        mma_commit(&ctl->empty[at]);
+                        if (++at == kUnits) at = 0;
+                    }
+                };
+                auto scores = [&](int h, int at) {          // S of half h from the three units at `at`
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ss(tmem + kColS + 128 * h, q0 + static_cast<uint64_t>(((3 * h + c) * kBox + ks * 32) >> 4),
+                                   k0 + static_cast<uint64_t>((at * kBox + ks * 32) >> 4), idesc_s, c > 0 || ks > 0 ? 1u : 0u);
+                        if (++at == kUnits) at = 0;
+                    }
+                    mma_commit(&ctl->s_full[h]);
+                };
+                auto outputs = [&](int h, int at, bool first) {   // O of half h (+)= P V from the two units at `at`
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(tmem + kColO + 128 * h, tmem + kColS + 128 * h + 8 * (4 * c + ks),
+                                   v0 + static_cast<uint64_t>((at * kBox + ks * 2048) >> 4), idesc_o, first && c == 0 && ks == 0 ? 0u : 1u);
+                        if (++at == kUnits) at = 0;
+                    }
+                    mma_commit(&ctl->o_done[h]);
+                };
+                for_items(p, ctl, [&](const Item& it) -> bool {
+                    const int n = max(it.count[0], it.count[1]);
+                    if (n == 0) return true;
+                    // the first block's scores
+                    if (!wait_units(unit, phase, 3)) return false;
+                    for (int h = 0; h < 2; ++h) {
+                        if (it.count[h] == 0) continue;
+                        if (!wait_or_give_up(&ctl->q_full[h], items[h]++ & 1, abort, status)) return false;
+                        scores(h, unit);
+                        if (it.count[h] == 1) mma_commit(&ctl->q_free[h]);
+                    }
+                    commit_units(unit, 3);
+                    unit += 3;
+                    if (unit >= kUnits) unit -= kUnits, phase ^= 1;
+                    for (int i = 0; i < n; ++i) {
+                        const int vat = unit;
+                        const uint32_t vph = phase;
+                        unit += 2;
+                        if (unit >= kUnits) unit -= kUnits, phase ^= 1;
+                        const int kat = unit;
+                        const uint32_t kph = phase;
+                        const bool more = i + 1 < n;
+                        if (!wait_units(vat, vph, 2)) return false;
+                        if (128 * (it.from + i + 1) > it.s.lk) {
+                            if (!wait_or_give_up(&ctl->v_clean[cleans & 1], (cleans >> 1) & 1, abort, status)) return false;
+                            ++cleans;
+                        }
+                        bool keys_here = false;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (i < it.count[h]) {
+                                if (!wait_or_give_up(&ctl->p_full[h], ps[h]++ & 1, abort, status)) return false;
+                                outputs(h, vat, i == 0);
+                            }
+                            if (h == 1) commit_units(vat, 2);
+                            if (i + 1 < it.count[h]) {
+                                if (!keys_here && !wait_units(kat, kph, 3)) return false;
+                                keys_here = true;
+                                scores(h, kat);
+                                if (i + 2 == it.count[h]) mma_commit(&ctl->q_free[h]);
+                            }
+                        }
+                        if (more) {
+                            commit_units(kat, 3);
+                            unit += 3;
+                            if (unit >= kUnits) unit -= kUnits, phase ^= 1;
+                        }
+                    }
+                    return true;
+                });
+                mma_commit(&ctl->drain);
+                wait_or_give_up(&ctl->drain, 0, abort, status);
+            }
+            __syncwarp();
+        } else if (warp == kWarpFix) {
+            // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN.
+            // (The warp takes note of every unit and hands it back beside the products, so that it stays within the ring.)
+            int unit = 0, cleans = 0;
+            uint32_t phase = 0;
+            for_items(p, ctl, [&](const Item& it) -> bool {
+                const int n = max(it.count[0], it.count[1]);
+                for (int i = 0; i < n; ++i) {
+                    const int left = it.s.lk - 128 * (it.from + i);
+                    for (int c = -3; c < 2; ++c) {         // three units of keys, two of values
+                        if (!wait_warp(&ctl->full[unit], phase, abort, status)) return false;
+                        if (c >= 0 && left < 128) {
+                            const uint32_t base = sbase + kOffRing + unit * kBox;
+                            for (int x = max(left - 64 * c, 0) * 8 + lane; x < 64 * 8; x += 32) {
+                                sts_u128(base + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                                sts_u128(base + kBox / 2 + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->empty[unit]);
+                        if (++unit == kUnits) unit = 0, phase ^= 1;
+                    }
+                    if (left < 128) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->v_clean[cleans & 1]);
+                        ++cleans;
+                    }
+                }
+                return true;
+            });
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int h = warp >> 2, w = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        const uint32_t s_addr = lanes + kColS + 128 * h, o_addr = lanes + kColO + 128 * h;
+        const float mul = p.sm_scale == 0.0f ? 1e-30f : p.sm_scale * kLog2e;   // (0 x -inf would be NaN where a key is masked)
+        int seen = 0;                  // blocks of this half so far: scores, P and P V count alike
+        for_items(p, ctl, [&](const Item& it) -> bool {
+            if (h == 1 && !it.used1) return true;
+            const int row = it.row0 + 128 * h + 32 * w + lane;          // of the sequence
+            const int limit = min(it.s.lk - it.s.lq + row + 1, it.s.lk);   // keys that the row sees
+            const int first_limit = it.s.lk - it.s.lq + it.row0 + 128 * h + 1;
+            float m = -INFINITY, l = 0.0f;
+            for (int i = 0; i < it.count[h]; ++i, ++seen) {
+                if (!wait_warp(&ctl->s_full[h], seen & 1, abort, status)) return false;
+                tc_fence_after_sync();
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+                tmem_wait_ld();
+                const int key0 = 128 * (it.from + i);
+                const uint32_t nothing = __float_as_uint(mul < 0.0f ? INFINITY : -INFINITY);   // times mul: a weight of 0
+                if (key0 + 128 > first_limit) {
+                    const int keep = limit - key0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = c < keep ? s[c] : nothing;
+                }
+                float top;
+                if (mul >= 0.0f) {
+                    float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 8) {
+                        t0 = fmax3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                        t1 = fmax3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+                        t2 = fmax3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+                        t3 = fmax3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+                    }
+                    top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                } else {
+                    top = INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) top = fminf(top, __uint_as_float(s[c]));
+                }
+                top = top == __uint_as_float(nothing) ? -INFINITY : top * mul;
+                if (__any_sync(0xffffffffu, top > m + kMoveLog2 || (m == -INFINITY && top > m))) {
+                    float alpha = 1.0f;
+                    if (top > m + kMoveLog2 || m == -INFINITY) {
+                        alpha = m == -INFINITY ? 0.0f : ex2_approx(m - top);
+                        m = top;
+                    }
+                    l *= alpha;
+                    if (i > 0) {
+                        if (!wait_warp(&ctl->o_done[h], (seen - 1) & 1, abort, status)) return false;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_addr + 16 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(o_addr + 16 * c, o);
+                        }
+                    }
+                }
+                const float neg_m = m == -INFINITY ? 0.0f : -m;
+                const uint64_t mul2 = f32x2_pack(mul, mul), neg2 = f32x2_pack(neg_m, neg_m);
+                uint64_t la = f32x2_pack(0.0f, 0.0f), lb = la;
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const uint32_t* v = s + 32 * part + c;
+                        const float2 z0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2, neg2));
+                        const float2 z1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[2]), __uint_as_float(v[3])), mul2, neg2));
+                        const float e0 = ex2_approx(z0.x), e1 = ex2_approx(z0.y), e2 = ex2_approx(z1.x), e3 = ex2_approx(z1.y);
+                        la = f32x2_add(la, f32x2_pack(e0, e1));
+                        lb = f32x2_add(lb, f32x2_pack(e2, e3));
+                        pw[c / 2] = pack_bf16x2(e0, e1);
+                        pw[c / 2 + 1] = pack_bf16x2(e2, e3);
+                    }
+                    tmem_st16(s_addr + 16 * part, pw);
+                }
+                const float2 sa = f32x2_unpack(la), sb = f32x2_unpack(lb);
+                l += (sa.x + sa.y) + (sb.x + sb.y);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->p_full[h]);
+            }
+            const int n = it.count[h];
+            if (n > 0) {
+                if (!wait_warp(&ctl->o_done[h], (seen - 1) & 1, abort, status)) return false;
+                tc_fence_after_sync();
+            }
+            const bool valid = row < it.s.lq, empty = l == 0.0f;
+            const float lse2 = empty ? -INFINITY : m + log2f(l);
+            float f = empty ? 0.0f : 1.0f / l;
+            if (!it.cut && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + it.head) * kLog2e - m));
+            const int64_t at = static_cast<int64_t>(it.s.q0 + row) * p.heads + it.head;
+            const int64_t part = static_cast<int64_t>(it.slot) * 256 + 128 * h + 32 * w + lane;
+            if (it.cut) a.part_lse[part] = lse2;
+            else if (valid) p.lse[at] = lse2 * kLn2;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                if (n > 0) tmem_ld32_wait(o_addr + 32 * c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = n == 0 || empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
+                if (it.cut) {
+                    float* dst = a.part_out + part * 128 + 32 * c;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st_sector(dst + 8 * e, o + 8 * e);
+                } else if (valid) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at * 128 + 32 * c;
+                    st_bf16x16(dst, o, 1.0f);
+                    st_bf16x16(dst + 16, o + 16, 1.0f);
+                }
+            }
+            tc_fence_before_sync();
+            return true;
+        });
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (*reinterpret_cast<volatile uint32_t*>(abort) != 0u) let_copies_land();
+    if (warp == kWarpMma) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the parts of a tile that was cut: with part s's lse L_s (log2) and output O_s, w_s = 2^(L_s - max L),
+// out = sum_s w_s O_s / (sum_s w_s + 2^(sink - max L)). The first part of header c lies in slot 2c + 1, the others in slots
+// 2 (c + 1), 2 (c + 2), ... A warp per row, in the parts' order.
+__global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restrict__ part_out, const float* __restrict__ part_lse,
+                                                          const int4* __restrict__ headers, const float* __restrict__ sink, int heads,
+                                                          __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x, lane = threadIdx.x & 31, r = 8 * blockIdx.y + (threadIdx.x >> 5);
+    const int4 hd = __ldcg(headers + c);
+    if (hd.w == 0 || r >= hd.y) return;
+    auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * 256 + r; };
+    float m = -INFINITY;
+    for (int s = lane; s < hd.w; s += 32) m = fmaxf(m, __ldcg(part_lse + slot(s)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0f;
+    float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < hd.w; ++s) {
+        const float w = exp2f(__ldcg(part_lse + slot(s)) - m);
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_out + slot(s) * 128 + 4 * lane));
+        sum += w;
+        acc[0] = fmaf(w, x.x, acc[0]);
+        acc[1] = fmaf(w, x.y, acc[1]);
+        acc[2] = fmaf(w, x.z, acc[2]);
+        acc[3] = fmaf(w, x.w, acc[3]);
+    }
+    const float denom = sink != nullptr ? sum + exp2f(__ldg(sink + hd.z) * kLog2e - m) : sum;
+    const float f = sum == 0.0f ? 0.0f : 1.0f / denom;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? acc[e] * f : 0.0f;
+    const int64_t at = static_cast<int64_t>(hd.x + r) * heads + hd.z;
+    *reinterpret_cast<uint2*>(out + at * 128 + 4 * lane) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    if (lane == 0) lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+constexpr size_t kPartsBytes = static_cast<size_t>(2 * kMaxCtas) * 256 * 128 * sizeof(float);
+constexpr size_t kLseBytes = static_cast<size_t>(2 * kMaxCtas) * 256 * sizeof(float);
+
+}  // namespace
+
+size_t ragged_workspace_bytes() { return kPartsBytes + kLseBytes + kMaxCtas * sizeof(int4); }
+
+cudaError_t launch_ragged_attention(const RaggedArgs& p, void* workspace, int sms, cudaStream_t stream) {
+    KernelArgs a;
+    a.p = p;
+    a.part_out = static_cast<float*>(workspace);
+    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPartsBytes);
+    a.headers = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + kPartsBytes + kLseBytes);
+    const int64_t rows_k = p.rows_k > 0 ? p.rows_k : 1;      // (no row is read where there is none)
+    if (!encode_map(&a.q_map, p.q, 192, p.heads, p.rows_q, p.q_head_stride, p.q_token_stride, 1, 128) ||
+        !encode_map(&a.k_map, p.kv, 256, p.heads, rows_k, p.kv_head_stride, p.kv_token_stride, 1, 128) ||
+        !encode_map(&a.v_map, p.kv, 256, p.heads, rows_k, p.kv_head_stride, p.kv_token_stride, 1, 64) ||
+        !encode_map(&a.pe_map, p.k_pe, 64, 1, rows_k, 64, p.pe_stride, 1, 128))
+        return cudaErrorInvalidValue;
+    cudaError_t err = allow_smem<ragged_attention_kernel>(kSmem);
+    if (err != cudaSuccess) return err;
+    const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    err = launch_dependent(ragged_attention_kernel, dim3(ctas), kThreads, kSmem, 1, stream, a);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(ragged_join_kernel, dim3(ctas, 32), 256, 0, 1, stream, static_cast<const float*>(a.part_out),
+                            static_cast<const float*>(a.part_lse), static_cast<const int4*>(a.headers), p.attn_sink, p.heads,
+                            static_cast<__nv_bfloat16*>(p.out), p.lse);
+}
+
+}  // namespace nvfp4mla
