@@ -21,17 +21,18 @@ namespace {
 
 using namespace tiles;
 
-constexpr int kStages = 5;            // ring of boxes of 128 tokens x 64 dims
+constexpr int kStages = 4;            // ring of boxes of 128 tokens x 64 dims
+constexpr int kStage = 4096;          // a warp's 32 tokens x 64 columns on the way out, two of them a warp
 constexpr int kOffW = 1024;
 constexpr int kWarpLoad = 4, kWarpMma = 5, kWarpRope = 6;   // warps 0-3 read the accumulators out
-constexpr int kRopeWarps = 4;
+constexpr int kRopeWarps = 8;
 constexpr int kTmemCols = 512;
 
 template <bool kAbsorb> constexpr int kK = kAbsorb ? 128 : 512;
 template <bool kAbsorb> constexpr int kN = kAbsorb ? 512 : 128;
 template <bool kAbsorb> constexpr int kThreads = kAbsorb ? 32 * (kWarpRope + kRopeWarps) : 32 * kWarpRope;
 template <bool kAbsorb, int kPiece> constexpr int kWBytes = kK<kAbsorb> * kPiece * 2;
-template <bool kAbsorb, int kPiece> constexpr int kSmem = kOffW + kWBytes<kAbsorb, kPiece> + kStages * kBox + 1024;
+template <bool kAbsorb, int kPiece> constexpr int kSmem = kOffW + kWBytes<kAbsorb, kPiece> + kStages * kBox + 8 * kStage + 1024;
 static_assert(kSmem<true, 512> <= 232448 && kSmem<false, 128> <= 232448, "shared memory");
 
 struct Ctl {
@@ -45,6 +46,7 @@ struct Ctl {
 struct KernelArgs {
     CUtensorMap a_map;                 // [tokens, heads, 192 or 512], box 128 x 1 x 64
     CUtensorMap w_map;                 // kv_b [heads, 256, 512], box 1 x rows x 64
+    CUtensorMap out_map;               // [tokens, heads, 576 or 128], box 32 x 1 x 64
     HeadProductArgs p;
     int64_t jobs;
     int tiles, pieces;
@@ -76,55 +78,59 @@ __device__ __forceinline__ void rotate4(uint32_t (&x)[4], bool half, float4 c, f
     for (int e = 0; e < 4; ++e) x[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
 }
 
-// The RoPE dims of a tile's tokens, 32 tokens a warp: eight lanes hold a token, four tokens at a time, four of those in flight.
+// Positions of a lane's tokens of a tile (16 tokens a warp, four at a time, eight lanes a token); -1: none to rotate by.
+__device__ __forceinline__ void rope_positions(const HeadProductArgs& p, int64_t t0, int lane, int64_t (&pos)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t t = t0 + 4 * e + (lane >> 3);
+        pos[e] = p.positions != nullptr && t < p.tokens ? __ldg(p.positions + t) : -1;
+    }
+}
+
+// The RoPE dims of a tile's tokens: all of a lane's loads are in flight at once (one latency a tile instead of two for the
+// tables behind the positions: 262 -> see the header's figures).
 template <bool kHalf>
-__device__ __forceinline__ void rope_tile(const HeadProductArgs& p, int64_t t0, int head, int lane) {
+__device__ __forceinline__ void rope_tile(const HeadProductArgs& p, int64_t t0, int head, int lane, const int64_t (&pos)[4]) {
     const int j = lane & 7;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.in) + head * p.in_head_stride + 128;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 512;
-#pragma unroll 1
-    for (int it = 0; it < 8; it += 4) {
-        uint32_t x[4][4];
-        float4 c[4], s[4];
-        bool use[4];
+    uint32_t x[4][4];
+    float4 c[4], s[4];
+    bool use[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t t = t0 + 4 * (it + e) + (lane >> 3);
-            use[e] = t < p.tokens;
-            c[e] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-            s[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (!use[e]) continue;
-            const __nv_bfloat16* src = q + t * p.in_token_stride;
-            if (kHalf) {
-                const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src + 4 * j)), hi = __ldg(reinterpret_cast<const uint2*>(src + 32 + 4 * j));
-                x[e][0] = lo.x, x[e][1] = lo.y, x[e][2] = hi.x, x[e][3] = hi.y;
-            } else {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + 8 * j));
-                x[e][0] = w.x, x[e][1] = w.y, x[e][2] = w.z, x[e][3] = w.w;
-            }
-            if (p.positions != nullptr) {
-                const int64_t pos = __ldg(p.positions + t);
-                if (pos < 0 || pos >= p.num_positions) {
-                    use[e] = false;
-                    if (p.status != nullptr && j == 0) atomicOr(p.status, 0x10u);
-                    continue;
-                }
-                c[e] = __ldg(reinterpret_cast<const float4*>(p.cos_table + pos * 32 + 4 * j));
-                s[e] = __ldg(reinterpret_cast<const float4*>(p.sin_table + pos * 32 + 4 * j));
-            }
+    for (int e = 0; e < 4; ++e) {
+        const int64_t t = t0 + 4 * e + (lane >> 3);
+        use[e] = t < p.tokens;
+        if (!use[e]) continue;
+        const __nv_bfloat16* src = q + t * p.in_token_stride;
+        if (kHalf) {
+            const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src + 4 * j)), hi = __ldg(reinterpret_cast<const uint2*>(src + 32 + 4 * j));
+            x[e][0] = lo.x, x[e][1] = lo.y, x[e][2] = hi.x, x[e][3] = hi.y;
+        } else {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + 8 * j));
+            x[e][0] = w.x, x[e][1] = w.y, x[e][2] = w.z, x[e][3] = w.w;
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!use[e]) continue;
-            const int64_t t = t0 + 4 * (it + e) + (lane >> 3);
-            if (p.positions != nullptr) rotate4(x[e], kHalf, c[e], s[e]);
-            __nv_bfloat16* dst = out + (t * p.heads + head) * 576;
-            if (kHalf) {
-                *reinterpret_cast<uint2*>(dst + 4 * j) = make_uint2(x[e][0], x[e][1]);
-                *reinterpret_cast<uint2*>(dst + 32 + 4 * j) = make_uint2(x[e][2], x[e][3]);
-            } else {
-                *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(x[e][0], x[e][1], x[e][2], x[e][3]);
+        if (p.positions != nullptr) {
+            if (pos[e] < 0 || pos[e] >= p.num_positions) {
+                use[e] = false;
+                if (p.status != nullptr && j == 0) atomicOr(p.status, 0x10u);
+                continue;
             }
+            c[e] = __ldg(reinterpret_cast<const float4*>(p.cos_table + pos[e] * 32 + 4 * j));
+            s[e] = __ldg(reinterpret_cast<const float4*>(p.sin_table + pos[e] * 32 + 4 * j));
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (!use[e]) continue;
+        const int64_t t = t0 + 4 * e + (lane >> 3);
+        if (p.positions != nullptr) rotate4(x[e], kHalf, c[e], s[e]);
+        __nv_bfloat16* dst = out + (t * p.heads + head) * 576;
+        if (kHalf) {
+            *reinterpret_cast<uint2*>(dst + 4 * j) = make_uint2(x[e][0], x[e][1]);
+            *reinterpret_cast<uint2*>(dst + 32 + 4 * j) = make_uint2(x[e][2], x[e][3]);
+        } else {
+            *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(x[e][0], x[e][1], x[e][2], x[e][3]);
         }
     }
 }
@@ -146,6 +152,7 @@ __global__ void __launch_bounds__(kThreads<kAbsorb>, 1) head_product_kernel(cons
     if (warp == kWarpLoad && lane == 0) {
         prefetch_map(&a.a_map);
         prefetch_map(&a.w_map);
+        prefetch_map(&a.out_map);
         for (int i = 0; i < kStages; ++i) mbar_init(&ctl->full[i], 1), mbar_init(&ctl->empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&ctl->acc_full[i], 1), mbar_init(&ctl->acc_empty[i], 4);
         mbar_init(&ctl->w_full, 1), mbar_init(&ctl->w_empty, 1), mbar_init(&ctl->drain, 1);
@@ -243,26 +250,37 @@ __global__ void __launch_bounds__(kThreads<kAbsorb>, 1) head_product_kernel(cons
         __syncwarp();
     } else if (warp < 4) {
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-        int acc = 0;
+        const uint32_t stage = sbase + kOffRing + kStages * kBox + 2 * warp * kStage;
+        int acc = 0, boxes = 0;
         bool ok = true;
         for (int i = 0; i < n_jobs && ok; ++i) {
             const int head = hp / a.pieces, n0 = (hp - head * a.pieces) * kPiece;
-            const int64_t t = static_cast<int64_t>(tile) * 128 + 32 * warp + lane;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.p.out) + (t * a.p.heads + head) * kOutRow + n0;
+            const int t0 = tile * 128 + 32 * warp;
 #pragma unroll 1
             for (int sub = 0; sub < kSubs && ok; ++sub, ++acc) {
                 const int buf = acc & 1;
                 ok = wait_warp(&ctl->acc_full[buf], (acc >> 1) & 1, abort, status);
                 if (!ok) break;
                 tc_fence_after_sync();
-                if (static_cast<int64_t>(tile) * 128 + 32 * warp < a.p.tokens) {   // (the same for the whole warp)
+                if (t0 < a.p.tokens) {   // (the same for the whole warp)
+                    if constexpr (kSub >= 64) {
 #pragma unroll 1
-                    for (int c = 0; c < kSub / 32; ++c) {
+                        for (int c = 0; c < kSub / 64; ++c, ++boxes) {
+                            const uint32_t box = stage + (boxes & 1) * kStage;
+                            if (lane == 0) tma_store_wait_read<1>();     // the box before the last one has left
+                            __syncwarp();
+                            stage_box(lanes + 256 * buf + 64 * c, box, lane);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) tma_store_3d(&a.out_map, n0 + kSub * sub + 64 * c, head, t0, box);
+                        }
+                    } else {
                         uint32_t v[32];
-                        tmem_ld32_wait(lanes + 256 * buf + 32 * c, v);
-                        if (t < a.p.tokens) {
-                            st_bf16x16(dst + kSub * sub + 32 * c, v, 1.0f);
-                            st_bf16x16(dst + kSub * sub + 32 * c + 16, v + 16, 1.0f);
+                        tmem_ld32_wait(lanes + 256 * buf, v);
+                        if (t0 + lane < a.p.tokens) {
+                            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.p.out) + (static_cast<int64_t>(t0 + lane) * a.p.heads + head) * kOutRow + n0;
+                            st_bf16x16(dst, v, 1.0f);
+                            st_bf16x16(dst + 16, v + 16, 1.0f);
                         }
                     }
                 }
@@ -272,17 +290,26 @@ __global__ void __launch_bounds__(kThreads<kAbsorb>, 1) head_product_kernel(cons
             }
             if (++tile == a.tiles) tile = 0, ++hp;
         }
+        if (lane == 0) tma_store_wait();
+        __syncwarp();
     } else if constexpr (kAbsorb) {
+        const int mine = 16 * (warp - kWarpRope);
+        int64_t pos[4], next[4];
+        rope_positions(a.p, static_cast<int64_t>(tile) * 128 + mine, lane, pos);
         for (int i = 0; i < n_jobs; ++i) {
             const int head = hp / a.pieces;
-            if (hp == head * a.pieces) {   // one of the head's pieces takes the RoPE dims along
-                const int64_t t0 = static_cast<int64_t>(tile) * 128 + 32 * (warp - kWarpRope);
-                if (a.p.rotate_half)
-                    rope_tile<true>(a.p, t0, head, lane);
-                else
-                    rope_tile<false>(a.p, t0, head, lane);
-            }
+            const int64_t t0 = static_cast<int64_t>(tile) * 128 + mine;
+            const bool takes = hp == head * a.pieces;   // one of the head's pieces takes the RoPE dims along
             if (++tile == a.tiles) tile = 0, ++hp;
+            rope_positions(a.p, static_cast<int64_t>(tile) * 128 + mine, lane, next);   // (a job ahead)
+            if (takes) {
+                if (a.p.rotate_half)
+                    rope_tile<true>(a.p, t0, head, lane, pos);
+                else
+                    rope_tile<false>(a.p, t0, head, lane, pos);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pos[e] = next[e];
         }
     }
     tc_fence_before_sync();
@@ -298,7 +325,8 @@ template <bool kAbsorb, int kPiece>
 cudaError_t launch_piece(KernelArgs& a, int sms, cudaStream_t stream) {
     const HeadProductArgs& p = a.p;
     if (!encode_map(&a.a_map, p.in, kAbsorb ? 192 : 512, p.heads, p.tokens, p.in_head_stride, p.in_token_stride, 1, 128) ||
-        !encode_map(&a.w_map, p.kv_b, 512, 256, p.heads, p.w_row_stride, p.w_head_stride, kAbsorb ? 128 : kPiece, 1))
+        !encode_map(&a.w_map, p.kv_b, 512, 256, p.heads, p.w_row_stride, p.w_head_stride, kAbsorb ? 128 : kPiece, 1) ||
+        !encode_map(&a.out_map, p.out, kAbsorb ? 576 : 128, p.heads, p.tokens, kAbsorb ? 576 : 128, static_cast<int64_t>(p.heads) * (kAbsorb ? 576 : 128), 1, 32))
         return cudaErrorInvalidValue;
     constexpr int kBytes = kSmem<kAbsorb, kPiece>;
     const cudaError_t err = allow_smem<head_product_kernel<kAbsorb, kPiece>>(kBytes);

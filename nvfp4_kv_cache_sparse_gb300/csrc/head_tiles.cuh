@@ -38,6 +38,35 @@ __device__ __forceinline__ void tma_load_3d_cg2(uint32_t dst_saddr, const void* 
 
 __device__ __forceinline__ void prefetch_map(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
 
+// TMA 3-D tiled store of a box from shared memory; rows outside the tensor are not written. One bulk group per call.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_t y, int32_t z, uint32_t src_saddr) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap), "r"(x), "r"(y), "r"(z),
+                 "r"(src_saddr)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the latest kPending stores of this thread have read their shared memory / have been written.
+template <int kPending>
+__device__ __forceinline__ void tma_store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A warp's 32 rows of 64 accumulator columns as a bf16 box with the 128B swizzle (4 KB, 1024-byte aligned).
+__device__ __forceinline__ void stage_box(uint32_t tmem_addr, uint32_t saddr, int lane) {
+    uint32_t v[64];
+    tmem_ld32(tmem_addr, *reinterpret_cast<uint32_t(*)[32]>(v));
+    tmem_ld32(tmem_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * e]), __uint_as_float(v[8 * c + 2 * e + 1]));
+        sts_u128(saddr + swz(lane, c), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
 // 32 bytes (a whole sector) to a 32-byte aligned address.
 __device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),

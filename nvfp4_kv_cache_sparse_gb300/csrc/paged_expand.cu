@@ -19,11 +19,13 @@ namespace {
 
 using namespace tiles;
 
-constexpr int kStages = 5;             // ring of weight boxes: 128 rows x 64 k
+constexpr int kStages = 4;             // ring of weight boxes: 128 rows x 64 k
 constexpr int kChunks = 8;             // K = 512 in steps of 64
 constexpr int kOffA = 1024;
 constexpr int kOffRing = kOffA + kChunks * kBox;
-constexpr int kSmem = kOffRing + kStages * kBox + 1024;
+constexpr int kStage = 4096;           // a warp's 32 tokens x 64 columns on the way out, two of them a warp
+constexpr int kOffStage = kOffRing + kStages * kBox;
+constexpr int kSmem = kOffStage + 8 * kStage + 1024;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr int kWarpLoad = 4, kWarpMma = 5, kWarpConvert = 6, kConvertWarps = 8;   // warps 0-3 read the accumulators out
 constexpr int kThreads = 32 * (kWarpConvert + kConvertWarps);
@@ -43,6 +45,7 @@ struct Ctl {
 
 struct KernelArgs {
     CUtensorMap w_map;                 // kv_b [heads, 256, 512], box 1 x 128 x 64
+    CUtensorMap kv_map;                // kv [rows, heads, 256], box 32 x 1 x 64
     ExpandArgs p;
 };
 
@@ -140,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_expand_kernel(const __grid_
     const ExpandArgs& p = a.p;
     if (warp == kWarpLoad && lane == 0) {
         prefetch_map(&a.w_map);
+        prefetch_map(&a.kv_map);
         for (int i = 0; i < kStages; ++i) mbar_init(&ctl->full[i], 1), mbar_init(&ctl->empty[i], 1);
         mbar_init(&ctl->a_full, 2 * kConvertWarps), mbar_init(&ctl->a_free, 1);
         for (int i = 0; i < 2; ++i) mbar_init(&ctl->acc_full[i], 1), mbar_init(&ctl->acc_empty[i], 8);
@@ -221,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_expand_kernel(const __grid_
         __syncwarp();
     } else if (warp < 4) {
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const uint32_t stage = sbase + kOffStage + 2 * warp * kStage;
         bool ok = true;
         for (int i = 0; i < n_units && ok; ++i) {
             const int buf = i & 1;
@@ -229,7 +234,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_expand_kernel(const __grid_
             ok = wait_warp(&ctl->acc_full[buf], (i >> 1) & 1, abort, status);
             if (!ok) break;
             tc_fence_after_sync();
-            if (t0 < total) {          // (the same for the whole warp)
+            if (t0 + 32 <= total) {    // (the same for the whole warp)
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t box = stage + (c & 1) * kStage;
+                    if (lane == 0) tma_store_wait_read<1>();     // the box before the last one has left
+                    __syncwarp();
+                    stage_box(lanes + 256 * buf + 64 * c, box, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&a.kv_map, 64 * c, head, static_cast<int32_t>(t0), box);
+                }
+            } else if (t0 < total) {   // rows behind the last sequence stay as they were
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     uint32_t v[32];
@@ -245,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_expand_kernel(const __grid_
             if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&ctl->acc_empty[buf]), 0));
             if (++head == p.heads) head = 0, ++tile;
         }
+        if (lane == 0) tma_store_wait();
+        __syncwarp();
     } else {
         const int w = warp - kWarpConvert, j = lane & 7;
         bool ok = true;
@@ -308,7 +326,9 @@ cudaError_t launch_records(const KernelArgs& a, int sms, cudaStream_t stream) {
 cudaError_t launch_paged_expand(const ExpandArgs& p, int sms, cudaStream_t stream) {
     KernelArgs a;
     a.p = p;
-    if (!encode_map(&a.w_map, p.kv_b, 512, 256, p.heads, p.w_row_stride, p.w_head_stride, 128, 1)) return cudaErrorInvalidValue;
+    if (!encode_map(&a.w_map, p.kv_b, 512, 256, p.heads, p.w_row_stride, p.w_head_stride, 128, 1) ||
+        !encode_map(&a.kv_map, p.kv, 256, p.heads, p.rows, 256, static_cast<int64_t>(p.heads) * 256, 1, 32))
+        return cudaErrorInvalidValue;
     if (p.record_bytes == 432) return launch_records<432, false>(a, sms, stream);
     return p.block_scales ? launch_records<352, true>(a, sms, stream) : launch_records<352, false>(a, sms, stream);
 }

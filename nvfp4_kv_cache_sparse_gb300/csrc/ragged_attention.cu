@@ -62,7 +62,7 @@ struct KernelArgs {
     CUtensorMap v_map;                 // the same, box 64 x 1 x 64
     CUtensorMap pe_map;                // [rows_k, 1, 64], box 128 x 1 x 64
     RaggedArgs p;
-    float* part_out;                   // [2 CTAs, 256, 128], each divided by its own sum
+    float* part_out;                   // [2 CTAs, 8 warps, 16, 32 lanes, 8]: eight dims of a row, divided by its own sum
     float* part_lse;                   // [2 CTAs, 256], log2
     int4* headers;                     // [CTAs]: first output row, rows, head, parts (0: no tile begins here and ends elsewhere)
 };
@@ -104,7 +104,7 @@ __device__ __forceinline__ int64_t units_of(const Seq& s, int m) {
 struct Item {
     Seq s;
     int head, row0;                    // rows row0 .. of the sequence
-    int from, count[2];                // first block; blocks of each half
+    int from, count0, count1;          // first block; blocks of each half
     bool used1;                        // the second half has rows
     bool cut;
     int slot;                          // of the part, where cut
@@ -124,8 +124,8 @@ __device__ __forceinline__ void for_items(const RaggedArgs& p, const Ctl* ctl, F
         it.row0 = 256 * tile;
         it.used1 = it.s.lq > it.row0 + 128;
         it.from = min(b0, n);
-        it.count[0] = max(min(b1, n0) - it.from, 0);
-        it.count[1] = it.used1 ? min(b1, n) - it.from : 0;
+        it.count0 = max(min(b1, n0) - it.from, 0);
+        it.count1 = it.used1 ? min(b1, n) - it.from : 0;
         it.cut = b0 > 0 || b1 < weight;
         it.slot = 2 * static_cast<int>(blockIdx.x) + (b0 > 0 ? 0 : 1);
         if (!f(it)) return;
@@ -227,6 +227,25 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
     a.headers[c] = header;
 }
 
+// Among eight lanes that hold eight 16-byte chunks of a row each: lane j's chunk e becomes lane e's chunk j, so that the lanes
+// then hold one chunk each of a whole 128-byte line (a warp's stores of 32 bytes in 32 lines take 130 cycles each, these a few).
+__device__ __forceinline__ void transpose8(uint32_t (&x)[8][4], int lane) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e & s) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[e][k] : x[e | s][k], s);
+                if (up) x[e][k] = got;
+                else x[e | s][k] = got;
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __grid_constant__ KernelArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -266,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kWarpLoad) {
             if (lane == 0) {
-                int unit = 0, items[2] = {0, 0};
-                uint32_t phase = 1;
+                int unit = 0;
+                uint32_t phase = 1, q_phase = 3;             // q_phase: one bit for each half
                 auto take = [&]() -> uint64_t* {            // the next unit of the ring, armed
                     if (!wait_or_give_up(&ctl->empty[unit], phase, abort, status)) return nullptr;
                     mbar_arrive_expect_tx(&ctl->full[unit], kBox);
@@ -277,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     if (++unit == kUnits) unit = 0, phase ^= 1;
                 };
                 for_items(p, ctl, [&](const Item& it) -> bool {
-                    const int n = max(it.count[0], it.count[1]);
+                    const int n = max(it.count0, it.count1);
                     if (n == 0) return true;
                     auto load_q = [&](int h) -> bool {
-                        if (it.count[h] == 0) return true;
-                        if (!wait_or_give_up(&ctl->q_free[h], (items[h] & 1) ^ 1, abort, status)) return false;
-                        ++items[h];
+                        if ((h == 0 ? it.count0 : it.count1) == 0) return true;
+                        if (!wait_or_give_up(&ctl->q_free[h], (q_phase >> h) & 1, abort, status)) return false;
+                        q_phase ^= 1u << h;
                         mbar_arrive_expect_tx(&ctl->q_full[h], 3 * kBox);
                         for (int c = 0; c < 3; ++c)
                             tma_load_3d(sbase + kOffQ + (3 * h + c) * kBox, &a.q_map, 64 * c, it.head, it.s.q0 + it.row0 + 128 * h, &ctl->q_full[h]);
@@ -323,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 const uint64_t q0 = sdesc_sw128(sbase + kOffQ, 16, 1024);                // K-major: rows x dims
                 const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);             // K-major: keys x dims
                 const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);       // MN-major: dims x keys
-                int unit = 0, items[2] = {0, 0}, ps[2] = {0, 0}, cleans = 0;
-                uint32_t phase = 0;
+                int unit = 0, cleans = 0;
+                uint32_t phase = 0, q_phase = 0, p_phase = 0;   // one bit for each half
                 auto wait_units = [&](int at, uint32_t ph, int n) -> bool {
                     for (int c = 0; c < n; ++c) {
                         if (!wait_or_give_up(&ctl->full[at], ph, abort, status)) return false;
@@ -363,15 +382,18 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     mma_commit(&ctl->o_done[h]);
                 };
                 for_items(p, ctl, [&](const Item& it) -> bool {
-                    const int n = max(it.count[0], it.count[1]);
+                    const int n = max(it.count0, it.count1);
                     if (n == 0) return true;
                     // the first block's scores
                     if (!wait_units(unit, phase, 3)) return false;
+#pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (it.count[h] == 0) continue;
-                        if (!wait_or_give_up(&ctl->q_full[h], items[h]++ & 1, abort, status)) return false;
+                        const int count = h == 0 ? it.count0 : it.count1;
+                        if (count == 0) continue;
+                        if (!wait_or_give_up(&ctl->q_full[h], (q_phase >> h) & 1, abort, status)) return false;
+                        q_phase ^= 1u << h;
                         scores(h, unit);
-                        if (it.count[h] == 1) mma_commit(&ctl->q_free[h]);
+                        if (count == 1) mma_commit(&ctl->q_free[h]);
                     }
                     commit_units(unit, 3);
                     unit += 3;
@@ -392,16 +414,18 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         bool keys_here = false;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            if (i < it.count[h]) {
-                                if (!wait_or_give_up(&ctl->p_full[h], ps[h]++ & 1, abort, status)) return false;
+                            const int count = h == 0 ? it.count0 : it.count1;
+                            if (i < count) {
+                                if (!wait_or_give_up(&ctl->p_full[h], (p_phase >> h) & 1, abort, status)) return false;
+                                p_phase ^= 1u << h;
                                 outputs(h, vat, i == 0);
                             }
                             if (h == 1) commit_units(vat, 2);
-                            if (i + 1 < it.count[h]) {
+                            if (i + 1 < count) {
                                 if (!keys_here && !wait_units(kat, kph, 3)) return false;
                                 keys_here = true;
                                 scores(h, kat);
-                                if (i + 2 == it.count[h]) mma_commit(&ctl->q_free[h]);
+                                if (i + 2 == count) mma_commit(&ctl->q_free[h]);
                             }
                         }
                         if (more) {
@@ -422,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             int unit = 0, cleans = 0;
             uint32_t phase = 0;
             for_items(p, ctl, [&](const Item& it) -> bool {
-                const int n = max(it.count[0], it.count[1]);
+                const int n = max(it.count0, it.count1);
                 for (int i = 0; i < n; ++i) {
                     const int left = it.s.lk - 128 * (it.from + i);
                     for (int c = -3; c < 2; ++c) {         // three units of keys, two of values
@@ -460,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             const int row = it.row0 + 128 * h + 32 * w + lane;          // of the sequence
             const int limit = min(it.s.lk - it.s.lq + row + 1, it.s.lk);   // keys that the row sees
             const int first_limit = it.s.lk - it.s.lq + it.row0 + 128 * h + 1;
+            const int n = h == 0 ? it.count0 : it.count1;
             float m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < it.count[h]; ++i, ++seen) {
+            for (int i = 0; i < n; ++i, ++seen) {
                 if (!wait_warp(&ctl->s_full[h], seen & 1, abort, status)) return false;
                 tc_fence_after_sync();
                 uint32_t s[128];
@@ -539,33 +564,54 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->p_full[h]);
             }
-            const int n = it.count[h];
             if (n > 0) {
                 if (!wait_warp(&ctl->o_done[h], (seen - 1) & 1, abort, status)) return false;
                 tc_fence_after_sync();
             }
-            const bool valid = row < it.s.lq, empty = l == 0.0f;
+            const int rows = it.s.lq - (it.row0 + 128 * h + 32 * w);    // rows of this warp (32 and more: all)
+            const bool empty = l == 0.0f;
             const float lse2 = empty ? -INFINITY : m + log2f(l);
             float f = empty ? 0.0f : 1.0f / l;
             if (!it.cut && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + it.head) * kLog2e - m));
-            const int64_t at = static_cast<int64_t>(it.s.q0 + row) * p.heads + it.head;
-            const int64_t part = static_cast<int64_t>(it.slot) * 256 + 128 * h + 32 * w + lane;
-            if (it.cut) a.part_lse[part] = lse2;
-            else if (valid) p.lse[at] = lse2 * kLn2;
+            const bool none = n == 0 || empty;
+            if (it.cut) {
+                if (rows <= 0) return true;
+                a.part_lse[static_cast<int64_t>(it.slot) * 256 + 128 * h + 32 * w + lane] = lse2;
+                float* dst = a.part_out + (static_cast<int64_t>(it.slot) * 8 + warp) * 4096 + 8 * lane;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                if (n > 0) tmem_ld32_wait(o_addr + 32 * c, o);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) tmem_ld32_wait(o_addr + 32 * c, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = n == 0 || empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
-                if (it.cut) {
-                    float* dst = a.part_out + part * 128 + 32 * c;
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st_sector(dst + 8 * e, o + 8 * e);
-                } else if (valid) {
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at * 128 + 32 * c;
-                    st_bf16x16(dst, o, 1.0f);
-                    st_bf16x16(dst + 16, o + 16, 1.0f);
+                    for (int e = 0; e < 4; ++e) st_sector(dst + (4 * c + e) * 256, o + 8 * e);
+                }
+            } else {
+                const int64_t at = static_cast<int64_t>(it.s.q0 + it.row0 + 128 * h + 32 * w) * p.heads + it.head;   // of lane 0's row
+                if (lane < rows) p.lse[at + static_cast<int64_t>(lane) * p.heads] = lse2 * kLn2;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[8][4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        uint32_t o[16];
+                        if (n > 0) {
+                            tmem_ld16(o_addr + 64 * c + 16 * d, o);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[2 * d + (e >> 2)][e & 3] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+                    }
+                    transpose8(x, lane);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = (lane & 24) + e;
+                        if (r < rows)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (at + static_cast<int64_t>(r) * p.heads) * 128 + 64 * c +
+                                                      8 * (lane & 7)) = make_uint4(x[e][0], x[e][1], x[e][2], x[e][3]);
+                    }
                 }
             }
             tc_fence_before_sync();
@@ -583,38 +629,42 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
 
 // Joins the parts of a tile that was cut: with part s's lse L_s (log2) and output O_s, w_s = 2^(L_s - max L),
 // out = sum_s w_s O_s / (sum_s w_s + 2^(sink - max L)). The first part of header c lies in slot 2c + 1, the others in slots
-// 2 (c + 1), 2 (c + 2), ... A warp per row, in the parts' order.
+// 2 (c + 1), 2 (c + 2), ... A lane per row and 16 dims, in the parts' order.
 __global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restrict__ part_out, const float* __restrict__ part_lse,
                                                           const int4* __restrict__ headers, const float* __restrict__ sink, int heads,
                                                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, lane = threadIdx.x & 31, r = 8 * blockIdx.y + (threadIdx.x >> 5);
+    const int c = blockIdx.x, lane = threadIdx.x & 31, dims = threadIdx.x >> 5, r = 32 * blockIdx.y + lane;
     const int4 hd = __ldcg(headers + c);
     if (hd.w == 0 || r >= hd.y) return;
-    auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * 256 + r; };
+    auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)); };
+    auto lse_of = [&](int s) { return __ldcg(part_lse + slot(s) * 256 + r); };
     float m = -INFINITY;
-    for (int s = lane; s < hd.w; s += 32) m = fmaxf(m, __ldcg(part_lse + slot(s)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int s = 0; s < hd.w; ++s) m = fmaxf(m, lse_of(s));
     if (m == -INFINITY) m = 0.0f;
-    float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+    float sum = 0.0f, acc[16] = {};
+#pragma unroll 2
     for (int s = 0; s < hd.w; ++s) {
-        const float w = exp2f(__ldcg(part_lse + slot(s)) - m);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_out + slot(s) * 128 + 4 * lane));
+        const float w = exp2f(lse_of(s) - m);
+        const float4* x = reinterpret_cast<const float4*>(part_out + (slot(s) * 8 + blockIdx.y) * 4096 + 512 * dims + 8 * lane);
+        const float4 v[4] = {__ldcg(x), __ldcg(x + 1), __ldcg(x + 64), __ldcg(x + 65)};
         sum += w;
-        acc[0] = fmaf(w, x.x, acc[0]);
-        acc[1] = fmaf(w, x.y, acc[1]);
-        acc[2] = fmaf(w, x.z, acc[2]);
-        acc[3] = fmaf(w, x.w, acc[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[4 * e] = fmaf(w, v[e].x, acc[4 * e]);
+            acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1]);
+            acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2]);
+            acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3]);
+        }
     }
     const float denom = sink != nullptr ? sum + exp2f(__ldg(sink + hd.z) * kLog2e - m) : sum;
     const float f = sum == 0.0f ? 0.0f : 1.0f / denom;
+    uint32_t o[16];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? acc[e] * f : 0.0f;
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(f != 0.0f ? acc[e] * f : 0.0f);
     const int64_t at = static_cast<int64_t>(hd.x + r) * heads + hd.z;
-    *reinterpret_cast<uint2*>(out + at * 128 + 4 * lane) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
-    if (lane == 0) lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    st_bf16x16(out + at * 128 + 16 * dims, o, 1.0f);
+    if (dims == 0) lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 constexpr size_t kPartsBytes = static_cast<size_t>(2 * kMaxCtas) * 256 * 128 * sizeof(float);
@@ -641,7 +691,7 @@ cudaError_t launch_ragged_attention(const RaggedArgs& p, void* workspace, int sm
     const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
     err = launch_dependent(ragged_attention_kernel, dim3(ctas), kThreads, kSmem, 1, stream, a);
     if (err != cudaSuccess) return err;
-    return launch_dependent(ragged_join_kernel, dim3(ctas, 32), 256, 0, 1, stream, static_cast<const float*>(a.part_out),
+    return launch_dependent(ragged_join_kernel, dim3(ctas, 8), 256, 0, 1, stream, static_cast<const float*>(a.part_out),
                             static_cast<const float*>(a.part_lse), static_cast<const int4*>(a.headers), p.attn_sink, p.heads,
                             static_cast<__nv_bfloat16*>(p.out), p.lse);
 }
