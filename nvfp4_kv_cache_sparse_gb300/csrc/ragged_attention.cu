@@ -42,12 +42,13 @@ constexpr int kMinRun = 2;
 constexpr int kMaxCtas = kPagedMaxSms;
 
 struct Ctl {
-    uint64_t full[kUnits], empty[kUnits];   // a unit is handed back by the products and by the warp that cleans values
+    // Block g of the CTA's run uses entry g & 1 of each; the values are handed back by the products and by the warp that cleans them.
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t q_full[2], q_free[2];     // a half's queries landed; its last scores are done
     uint64_t s_full[2];                // scores in tensor memory
     uint64_t p_full[2];                // 4 warps: P written, O rescaled
-    uint64_t o_done[2];                // a block's P V is done
-    uint64_t v_clean[2];               // rows behind a sequence's end were zeroed (in turn: the ring has room for the values of two tiles)
+    uint64_t o_done[2];                // a tile's last P V is done
+    uint64_t v_clean[2];               // rows behind a sequence's end were zeroed (in turn: there may be the values of two tiles)
     uint64_t drain;
     uint32_t tmem_base, abort;
     // the first item of the CTA's run
@@ -258,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         prefetch_map(&a.k_map);
         prefetch_map(&a.v_map);
         prefetch_map(&a.pe_map);
-        for (int i = 0; i < kUnits; ++i) mbar_init(&ctl->full[i], 1), mbar_init(&ctl->empty[i], 2);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_empty[i], 1), mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_empty[i], 2);
             mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
             mbar_init(&ctl->s_full[i], 1), mbar_init(&ctl->p_full[i], 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->v_clean[i], 1);
         }
@@ -285,16 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kWarpLoad) {
             if (lane == 0) {
-                int unit = 0;
-                uint32_t phase = 1, q_phase = 3;             // q_phase: one bit for each half
-                auto take = [&]() -> uint64_t* {            // the next unit of the ring, armed
-                    if (!wait_or_give_up(&ctl->empty[unit], phase, abort, status)) return nullptr;
-                    mbar_arrive_expect_tx(&ctl->full[unit], kBox);
-                    return &ctl->full[unit];
-                };
-                auto step = [&] {
-                    if (++unit == kUnits) unit = 0, phase ^= 1;
-                };
+                // Eight units hold three groups in flight: the keys of block g lie where the values of block g - 2 and what came before lay,
+                // the values of block g where the keys of block g - 1 lay.
+                int unit = 0, g = 0;
+                uint32_t q_phase = 3;                        // one bit for each half
+                auto step = [&] { unit = unit + 1 == kUnits ? 0 : unit + 1; };
                 for_items(p, ctl, [&](const Item& it) -> bool {
                     const int n = max(it.count0, it.count1);
                     if (n == 0) return true;
@@ -308,25 +304,26 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         return true;
                     };
                     auto load_k = [&](int i) -> bool {
+                        if (g >= 2 && !wait_or_give_up(&ctl->v_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) return false;
                         const int row = it.s.k0 + 128 * (it.from + i);
-                        for (int c = 0; c < 3; ++c) {
-                            uint64_t* bar = take();
-                            if (bar == nullptr) return false;
+                        uint64_t* bar = &ctl->k_full[g & 1];
+                        mbar_arrive_expect_tx(bar, 3 * kBox);
+                        for (int c = 0; c < 3; ++c, step()) {
                             if (c < 2) tma_load_3d(sbase + kOffRing + unit * kBox, &a.k_map, 64 * c, it.head, row, bar);
                             else tma_load_3d(sbase + kOffRing + unit * kBox, &a.pe_map, 0, 0, row, bar);
-                            step();
                         }
                         return true;
                     };
                     auto load_v = [&](int i) -> bool {
+                        if (g >= 1 && !wait_or_give_up(&ctl->k_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, status)) return false;
                         const int row = it.s.k0 + 128 * (it.from + i);
-                        for (int c = 0; c < 2; ++c) {
-                            uint64_t* bar = take();
-                            if (bar == nullptr) return false;
+                        uint64_t* bar = &ctl->v_full[g & 1];
+                        mbar_arrive_expect_tx(bar, 2 * kBox);
+                        for (int c = 0; c < 2; ++c, step()) {
                             tma_load_3d(sbase + kOffRing + unit * kBox, &a.v_map, 128, it.head, row + 64 * c, bar);
                             tma_load_3d(sbase + kOffRing + unit * kBox + kBox / 2, &a.v_map, 192, it.head, row + 64 * c, bar);
-                            step();
                         }
+                        ++g;
                         return true;
                     };
                     if (!load_q(0) || !load_k(0) || !load_q(1) || !load_v(0)) return false;
@@ -338,55 +335,44 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             __syncwarp();
         } else if (warp == kWarpMma) {
             if (lane == 0) {
-                constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false), idesc_o = idesc_bf16_f32(128, 128, false, true);
+                // (a negative scale negates the queries in the product: bit 13)
+                const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false) | (p.sm_scale < 0.0f ? 1u << 13 : 0u);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
                 const uint64_t q0 = sdesc_sw128(sbase + kOffQ, 16, 1024);                // K-major: rows x dims
                 const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);             // K-major: keys x dims
                 const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);       // MN-major: dims x keys
-                int unit = 0, cleans = 0;
-                uint32_t phase = 0, q_phase = 0, p_phase = 0;   // one bit for each half
-                auto wait_units = [&](int at, uint32_t ph, int n) -> bool {
-                    for (int c = 0; c < n; ++c) {
-                        if (!wait_or_give_up(&ctl->full[at], ph, abort, status)) return false;
-                        if (++at == kUnits) at = 0, ph ^= 1;
-                    }
-                    return true;
-                };
-                auto commit_units = [&](int at, int n) {
-                    for (int c = 0; c < n; ++c) {
-                        mma_commit(&ctl->empty[at]);
-                        if (++at == kUnits) at = 0;
-                    }
-                };
+                int unit = 0, g = 0, cleans = 0;                                         // g: blocks whose values were waited for
+                uint32_t q_phase = 0, p_phase = 0;                                       // one bit for each half
+                auto after = [](int at, int n) { return at + n >= kUnits ? at + n - kUnits : at + n; };
+                // (short loops: unrolled as a whole, the two chains of a block do not stay in the instruction caches beside the softmax)
                 auto scores = [&](int h, int at) {          // S of half h from the three units at `at`
                     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 3; ++c) {
+                        const uint64_t qd = q0 + static_cast<uint32_t>((3 * h + c) * (kBox >> 4)), kd = k0 + static_cast<uint32_t>(at * (kBox >> 4));
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ss(tmem + kColS + 128 * h, q0 + static_cast<uint64_t>(((3 * h + c) * kBox + ks * 32) >> 4),
-                                   k0 + static_cast<uint64_t>((at * kBox + ks * 32) >> 4), idesc_s, c > 0 || ks > 0 ? 1u : 0u);
-                        if (++at == kUnits) at = 0;
+                        for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + kColS + 128 * h, qd + 2 * ks, kd + 2 * ks, idesc_s, c > 0 || ks > 0 ? 1u : 0u);
+                        at = after(at, 1);
                     }
                     mma_commit(&ctl->s_full[h]);
                 };
                 auto outputs = [&](int h, int at, bool first) {   // O of half h (+)= P V from the two units at `at`
                     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
+                        const uint64_t vd = v0 + static_cast<uint32_t>(at * (kBox >> 4));
+                        const uint32_t pa = tmem + kColS + 128 * h + 32 * c;
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(tmem + kColO + 128 * h, tmem + kColS + 128 * h + 8 * (4 * c + ks),
-                                   v0 + static_cast<uint64_t>((at * kBox + ks * 2048) >> 4), idesc_o, first && c == 0 && ks == 0 ? 0u : 1u);
-                        if (++at == kUnits) at = 0;
+                        for (int ks = 0; ks < 4; ++ks) mma_ts(tmem + kColO + 128 * h, pa + 8 * ks, vd + 128 * ks, idesc_o, first && c == 0 && ks == 0 ? 0u : 1u);
+                        at = after(at, 1);
                     }
-                    mma_commit(&ctl->o_done[h]);
                 };
                 for_items(p, ctl, [&](const Item& it) -> bool {
                     const int n = max(it.count0, it.count1);
                     if (n == 0) return true;
                     // the first block's scores
-                    if (!wait_units(unit, phase, 3)) return false;
-#pragma unroll
+                    if (!wait_or_give_up(&ctl->k_full[g & 1], (g >> 1) & 1, abort, status)) return false;
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const int count = h == 0 ? it.count0 : it.count1;
                         if (count == 0) continue;
@@ -395,44 +381,35 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         scores(h, unit);
                         if (count == 1) mma_commit(&ctl->q_free[h]);
                     }
-                    commit_units(unit, 3);
-                    unit += 3;
-                    if (unit >= kUnits) unit -= kUnits, phase ^= 1;
-                    for (int i = 0; i < n; ++i) {
-                        const int vat = unit;
-                        const uint32_t vph = phase;
-                        unit += 2;
-                        if (unit >= kUnits) unit -= kUnits, phase ^= 1;
-                        const int kat = unit;
-                        const uint32_t kph = phase;
+                    mma_commit(&ctl->k_empty[g & 1]);
+                    unit = after(unit, 3);
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i, ++g) {
+                        const int vat = unit, kat = after(unit, 2);
                         const bool more = i + 1 < n;
-                        if (!wait_units(vat, vph, 2)) return false;
+                        if (!wait_or_give_up(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status)) return false;
                         if (128 * (it.from + i + 1) > it.s.lk) {
                             if (!wait_or_give_up(&ctl->v_clean[cleans & 1], (cleans >> 1) & 1, abort, status)) return false;
                             ++cleans;
                         }
-                        bool keys_here = false;
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
                             const int count = h == 0 ? it.count0 : it.count1;
                             if (i < count) {
                                 if (!wait_or_give_up(&ctl->p_full[h], (p_phase >> h) & 1, abort, status)) return false;
                                 p_phase ^= 1u << h;
                                 outputs(h, vat, i == 0);
+                                if (i + 1 == count) mma_commit(&ctl->o_done[h]);
                             }
-                            if (h == 1) commit_units(vat, 2);
+                            if (h == 1) mma_commit(&ctl->v_empty[g & 1]);
                             if (i + 1 < count) {
-                                if (!keys_here && !wait_units(kat, kph, 3)) return false;
-                                keys_here = true;
+                                if (!wait_or_give_up(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, status)) return false;
                                 scores(h, kat);
                                 if (i + 2 == count) mma_commit(&ctl->q_free[h]);
                             }
                         }
-                        if (more) {
-                            commit_units(kat, 3);
-                            unit += 3;
-                            if (unit >= kUnits) unit -= kUnits, phase ^= 1;
-                        }
+                        if (more) mma_commit(&ctl->k_empty[(g + 1) & 1]);
+                        unit = more ? after(kat, 3) : kat;
                     }
                     return true;
                 });
@@ -442,32 +419,30 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             __syncwarp();
         } else if (warp == kWarpFix) {
             // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN.
-            // (The warp takes note of every unit and hands it back beside the products, so that it stays within the ring.)
-            int unit = 0, cleans = 0;
-            uint32_t phase = 0;
+            // (The warp takes note of every block and hands it back beside the products, so that it stays within the ring.)
+            int unit = 0, g = 0, cleans = 0;
             for_items(p, ctl, [&](const Item& it) -> bool {
                 const int n = max(it.count0, it.count1);
-                for (int i = 0; i < n; ++i) {
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, ++g) {
                     const int left = it.s.lk - 128 * (it.from + i);
-                    for (int c = -3; c < 2; ++c) {         // three units of keys, two of values
-                        if (!wait_warp(&ctl->full[unit], phase, abort, status)) return false;
-                        if (c >= 0 && left < 128) {
-                            const uint32_t base = sbase + kOffRing + unit * kBox;
+                    unit = (unit + 3) & (kUnits - 1);
+                    if (!wait_warp(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status)) return false;
+                    if (left < 128) {
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t base = sbase + kOffRing + ((unit + c) & (kUnits - 1)) * kBox;
                             for (int x = max(left - 64 * c, 0) * 8 + lane; x < 64 * 8; x += 32) {
                                 sts_u128(base + 16 * x, make_uint4(0u, 0u, 0u, 0u));
                                 sts_u128(base + kBox / 2 + 16 * x, make_uint4(0u, 0u, 0u, 0u));
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->empty[unit]);
-                        if (++unit == kUnits) unit = 0, phase ^= 1;
-                    }
-                    if (left < 128) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ctl->v_clean[cleans & 1]);
                         ++cleans;
                     }
+                    unit = (unit + 2) & (kUnits - 1);
+                    if (lane == 0) mbar_arrive(&ctl->v_empty[g & 1]);
                 }
                 return true;
             });
@@ -477,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         const int h = warp >> 2, w = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w) << 16);
         const uint32_t s_addr = lanes + kColS + 128 * h, o_addr = lanes + kColO + 128 * h;
-        const float mul = p.sm_scale == 0.0f ? 1e-30f : p.sm_scale * kLog2e;   // (0 x -inf would be NaN where a key is masked)
-        int seen = 0;                  // blocks of this half so far: scores, P and P V count alike
+        const float mul = p.sm_scale == 0.0f ? 1e-30f : fabsf(p.sm_scale) * kLog2e;   // (0 x -inf would be NaN where a key is masked)
+        int seen = 0, done = 0;        // blocks and tiles of this half so far
         for_items(p, ctl, [&](const Item& it) -> bool {
             if (h == 1 && !it.used1) return true;
             const int row = it.row0 + 128 * h + 32 * w + lane;          // of the sequence
@@ -494,29 +469,20 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
                 tmem_wait_ld();
                 const int key0 = 128 * (it.from + i);
-                const uint32_t nothing = __float_as_uint(mul < 0.0f ? INFINITY : -INFINITY);   // times mul: a weight of 0
                 if (key0 + 128 > first_limit) {
                     const int keep = limit - key0;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = c < keep ? s[c] : nothing;
+                    for (int c = 0; c < 128; ++c) s[c] = c < keep ? s[c] : __float_as_uint(-INFINITY);
                 }
-                float top;
-                if (mul >= 0.0f) {
-                    float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
+                float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
-                    for (int c = 0; c < 128; c += 8) {
-                        t0 = fmax3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                        t1 = fmax3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-                        t2 = fmax3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-                        t3 = fmax3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-                    }
-                    top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-                } else {
-                    top = INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) top = fminf(top, __uint_as_float(s[c]));
+                for (int c = 0; c < 128; c += 8) {
+                    t0 = fmax3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                    t1 = fmax3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+                    t2 = fmax3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+                    t3 = fmax3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
                 }
-                top = top == __uint_as_float(nothing) ? -INFINITY : top * mul;
+                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * mul;
                 if (__any_sync(0xffffffffu, top > m + kMoveLog2 || (m == -INFINITY && top > m))) {
                     float alpha = 1.0f;
                     if (top > m + kMoveLog2 || m == -INFINITY) {
@@ -524,9 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         m = top;
                     }
                     l *= alpha;
-                    if (i > 0) {
-                        if (!wait_warp(&ctl->o_done[h], (seen - 1) & 1, abort, status)) return false;
-                        tc_fence_after_sync();
+                    if (i > 0) {                           // (these scores are there, so the last P V is done)
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
                             uint32_t o[16];
@@ -565,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 if (lane == 0) mbar_arrive(&ctl->p_full[h]);
             }
             if (n > 0) {
-                if (!wait_warp(&ctl->o_done[h], (seen - 1) & 1, abort, status)) return false;
+                if (!wait_warp(&ctl->o_done[h], done++ & 1, abort, status)) return false;
                 tc_fence_after_sync();
             }
             const int rows = it.s.lq - (it.row0 + 128 * h + 32 * w);    // rows of this warp (32 and more: all)
