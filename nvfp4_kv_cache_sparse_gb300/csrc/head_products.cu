@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads<kAbsorb>, 1) head_product_kernel(cons
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
+        if (elect_one_in_warp()) {
             constexpr uint32_t idesc = idesc_bf16_f32(128, kSub, false, kAbsorb);
             const uint64_t a0 = sdesc_sw128(sbase + kOffRing, 16, 1024);                                        // K-major: tokens x dims
             const uint64_t w0 = sdesc_sw128(sbase + kOffW, kAbsorb ? kBox : 16, 1024);   // absorb MN-major: n x k, else K-major

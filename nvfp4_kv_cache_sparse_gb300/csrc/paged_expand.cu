@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_expand_kernel(const __grid_
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && elect_one_in_warp()) {
             constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, false);
             const uint64_t a0 = sdesc_sw128(sbase + kOffA, 16, 1024), w0 = sdesc_sw128(sbase + kOffRing, 16, 1024);
             int stage = 0, tiles_seen = 0;

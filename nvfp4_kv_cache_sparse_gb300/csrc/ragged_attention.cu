@@ -5,8 +5,8 @@
 //   out[i, h] = sum_n e^z kv[n, h, 128:256] / (sum_n e^z + e^sink[h]),   lse[i, h] = log sum_n e^z
 // 640 FLOP per query, key and head against 2176 in the absorbed form, which works on the latents themselves: the tensor cores
 // bound it. One pass over the keys with a running reference m of each row: P = 2^(z log2 e - m) in bf16, whose range
-// is that of fp32, so that no weight is lost however far it lies below the largest; row sums and outputs in fp32. m moves
-// only when a score passes it by 2^8 (the output in tensor memory is rescaled then).
+// is that of fp32, so that no weight is lost however far it lies below the largest; row sums and outputs in fp32. m, a whole number in log2
+// units, moves only when a score passes it by 2^8 (the output in tensor memory is rescaled then).
 //
 // A tile is 256 query rows of one sequence and head, in two halves of 128. S = Q K^T of a half is one tcgen05.mma chain
 // (M = 128 rows, N = 128 keys, K = 192) into tensor memory; a warpgroup per half turns it into P, which overwrites S
@@ -30,7 +30,7 @@ constexpr int kOffQ = 1024;
 constexpr int kOffRing = kOffQ + 6 * kBox;
 constexpr int kSmem = kOffRing + kUnits * kBox + 1024;
 static_assert(kSmem <= 232448, "shared memory");
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10;   // warps 0-3 and 4-7: softmax of the two halves
+constexpr int kWarpLoad = 8, kWarpFix = 9, kWarpMma = 10;    // 10 and 11: products of the two halves; 0-3 and 4-7: their softmax
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;      // 2 x 128 x 208 + 128 x 88 = 384 x 168, the registers at launch
 constexpr int kTmemCols = 512;
@@ -42,7 +42,7 @@ constexpr int kMinRun = 2;
 constexpr int kMaxCtas = kPagedMaxSms;
 
 struct Ctl {
-    // Block g of the CTA's run uses entry g & 1 of each; the values are handed back by the products and by the warp that cleans them.
+    // Block g of the CTA's run uses entry g & 1 of each; both issuers hand a block back, the values also the warp that cleans them.
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t q_full[2], q_free[2];     // a half's queries landed; its last scores are done
     uint64_t s_full[2];                // scores in tensor memory
@@ -247,6 +247,48 @@ __device__ __forceinline__ void transpose8(uint32_t (&x)[8][4], int lane) {
     }
 }
 
+// A warp's rows whose largest score so far (top, in log2 units) passes their reference m by 2^kMoveLog2 move it up to the next whole
+// number, and what was weighed against the old one is scaled: the row's sum l, this block's la and lb, its output (where there is
+// one) and the quarters of P that are written. The factors are powers of two, so nothing is rounded by it.
+__device__ __forceinline__ void move_reference(float top, float& m, float& l, uint64_t& la, uint64_t& lb, bool outputs, int quarters, uint32_t s_addr,
+                                            uint32_t o_addr) {
+    float alpha = 1.0f;
+    if (top > m + kMoveLog2) {
+        const float to = ceilf(top);
+        alpha = m - to >= -126.0f ? __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(m - to)) << 23) : 0.0f;
+        m = to;
+    }
+    l *= alpha;
+    const uint64_t alpha2 = f32x2_pack(alpha, alpha), zero2 = f32x2_pack(0.0f, 0.0f);
+    la = f32x2_fma(la, alpha2, zero2);
+    lb = f32x2_fma(lb, alpha2, zero2);
+    if (outputs) {                             // (these scores are there, so the last P V is done)
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(o_addr + 16 * c, o);
+        }
+    }
+    const __nv_bfloat162 a2 = __float2bfloat162_rn(alpha);
+#pragma unroll 1
+    for (int c = 0; c < quarters; ++c) {
+        tmem_wait_st();
+        uint32_t w[16];
+        tmem_ld16(s_addr + 16 * c, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), a2);
+            w[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        tmem_st16(s_addr + 16 * c, w);
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __grid_constant__ KernelArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -260,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         prefetch_map(&a.v_map);
         prefetch_map(&a.pe_map);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_empty[i], 1), mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_empty[i], 2);
+            mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_empty[i], 2), mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_empty[i], 3);
             mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
             mbar_init(&ctl->s_full[i], 1), mbar_init(&ctl->p_full[i], 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->v_clean[i], 1);
         }
-        mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
         fence_barrier_init();
     }
@@ -333,83 +375,69 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 });
             }
             __syncwarp();
-        } else if (warp == kWarpMma) {
-            if (lane == 0) {
+        } else if (warp >= kWarpMma) {
+            // Each half has an issuer of its own: a product's issue blocks until the tensor cores take it, and what lies between two chains (waits,
+            // commits, instruction fetches: 150 to 300 cycles each) would leave them idle; now the other half's chain runs meanwhile.
+            if (elect_one_in_warp()) {
+                const int h = warp - kWarpMma;
                 // (a negative scale negates the queries in the product: bit 13)
                 const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false) | (p.sm_scale < 0.0f ? 1u << 13 : 0u);
                 constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
-                const uint64_t q0 = sdesc_sw128(sbase + kOffQ, 16, 1024);                // K-major: rows x dims
-                const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);             // K-major: keys x dims
-                const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);       // MN-major: dims x keys
-                int unit = 0, g = 0, cleans = 0;                                         // g: blocks whose values were waited for
-                uint32_t q_phase = 0, p_phase = 0;                                       // one bit for each half
-                auto after = [](int at, int n) { return at + n >= kUnits ? at + n - kUnits : at + n; };
-                // (short loops: unrolled as a whole, the two chains of a block do not stay in the instruction caches beside the softmax)
-                auto scores = [&](int h, int at) {          // S of half h from the three units at `at`
+                const uint64_t q0 = sdesc_sw128(sbase + kOffQ + 3 * h * kBox, 16, 1024);   // K-major: rows x dims
+                const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);               // K-major: keys x dims
+                const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);         // MN-major: dims x keys
+                const uint32_t s_addr = tmem + kColS + 128 * h, o_addr = tmem + kColO + 128 * h;
+                int unit = 0, g = 0, cleans = 0;                                           // g: blocks whose values were waited for
+                uint32_t q_phase = 0, p_phase = 0;
+                auto scores = [&](int at) {                 // S from the three units at `at`
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 3; ++c) {
-                        const uint64_t qd = q0 + static_cast<uint32_t>((3 * h + c) * (kBox >> 4)), kd = k0 + static_cast<uint32_t>(at * (kBox >> 4));
+                        const uint64_t qd = q0 + static_cast<uint32_t>(c * (kBox >> 4)), kd = k0 + static_cast<uint32_t>(((at + c) & (kUnits - 1)) * (kBox >> 4));
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + kColS + 128 * h, qd + 2 * ks, kd + 2 * ks, idesc_s, c > 0 || ks > 0 ? 1u : 0u);
-                        at = after(at, 1);
+                        for (int ks = 0; ks < 4; ++ks) mma_ss(s_addr, qd + 2 * ks, kd + 2 * ks, idesc_s, c > 0 || ks > 0 ? 1u : 0u);
                     }
                     mma_commit(&ctl->s_full[h]);
                 };
-                auto outputs = [&](int h, int at, bool first) {   // O of half h (+)= P V from the two units at `at`
-                    tc_fence_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        const uint64_t vd = v0 + static_cast<uint32_t>(at * (kBox >> 4));
-                        const uint32_t pa = tmem + kColS + 128 * h + 32 * c;
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) mma_ts(tmem + kColO + 128 * h, pa + 8 * ks, vd + 128 * ks, idesc_o, first && c == 0 && ks == 0 ? 0u : 1u);
-                        at = after(at, 1);
-                    }
-                };
                 for_items(p, ctl, [&](const Item& it) -> bool {
-                    const int n = max(it.count0, it.count1);
+                    const int n = max(it.count0, it.count1), count = h == 0 ? it.count0 : it.count1;
                     if (n == 0) return true;
-                    // the first block's scores
-                    if (!wait_or_give_up(&ctl->k_full[g & 1], (g >> 1) & 1, abort, status)) return false;
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const int count = h == 0 ? it.count0 : it.count1;
-                        if (count == 0) continue;
-                        if (!wait_or_give_up(&ctl->q_full[h], (q_phase >> h) & 1, abort, status)) return false;
-                        q_phase ^= 1u << h;
-                        scores(h, unit);
+                    if (count > 0) {                        // the first block's scores
+                        if (!wait_or_give_up(&ctl->k_full[g & 1], (g >> 1) & 1, abort, status)) return false;
+                        if (!wait_or_give_up(&ctl->q_full[h], q_phase, abort, status)) return false;
+                        q_phase ^= 1u;
+                        scores(unit);
                         if (count == 1) mma_commit(&ctl->q_free[h]);
                     }
                     mma_commit(&ctl->k_empty[g & 1]);
-                    unit = after(unit, 3);
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++g) {
-                        const int vat = unit, kat = after(unit, 2);
-                        const bool more = i + 1 < n;
                         if (!wait_or_give_up(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status)) return false;
                         if (128 * (it.from + i + 1) > it.s.lk) {
                             if (!wait_or_give_up(&ctl->v_clean[cleans & 1], (cleans >> 1) & 1, abort, status)) return false;
                             ++cleans;
                         }
+                        if (i < count) {                    // O (+)= P V
+                            if (!wait_or_give_up(&ctl->p_full[h], p_phase, abort, status)) return false;
+                            p_phase ^= 1u;
+                            tc_fence_after_sync();
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            const int count = h == 0 ? it.count0 : it.count1;
-                            if (i < count) {
-                                if (!wait_or_give_up(&ctl->p_full[h], (p_phase >> h) & 1, abort, status)) return false;
-                                p_phase ^= 1u << h;
-                                outputs(h, vat, i == 0);
-                                if (i + 1 == count) mma_commit(&ctl->o_done[h]);
+                            for (int c = 0; c < 2; ++c) {
+                                const uint64_t vd = v0 + static_cast<uint32_t>(((unit + 3 + c) & (kUnits - 1)) * (kBox >> 4));
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    mma_ts(o_addr, s_addr + 32 * c + 8 * ks, vd + 128 * ks, idesc_o, i == 0 && c == 0 && ks == 0 ? 0u : 1u);
                             }
-                            if (h == 1) mma_commit(&ctl->v_empty[g & 1]);
-                            if (i + 1 < count) {
-                                if (!wait_or_give_up(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, status)) return false;
-                                scores(h, kat);
-                                if (i + 2 == count) mma_commit(&ctl->q_free[h]);
-                            }
+                            if (i + 1 == count) mma_commit(&ctl->o_done[h]);
                         }
-                        if (more) mma_commit(&ctl->k_empty[(g + 1) & 1]);
-                        unit = more ? after(kat, 3) : kat;
+                        mma_commit(&ctl->v_empty[g & 1]);
+                        unit = (unit + 5) & (kUnits - 1);
+                        if (i + 1 < count) {
+                            if (!wait_or_give_up(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, status)) return false;
+                            scores(unit);
+                            if (i + 2 == count) mma_commit(&ctl->q_free[h]);
+                        }
+                        if (i + 1 < n) mma_commit(&ctl->k_empty[(g + 1) & 1]);
                     }
                     return true;
                 });
@@ -464,62 +492,42 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             for (int i = 0; i < n; ++i, ++seen) {
                 if (!wait_warp(&ctl->s_full[h], seen & 1, abort, status)) return false;
                 tc_fence_after_sync();
-                uint32_t s[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-                tmem_wait_ld();
                 const int key0 = 128 * (it.from + i);
-                if (key0 + 128 > first_limit) {
-                    const int keep = limit - key0;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = c < keep ? s[c] : __float_as_uint(-INFINITY);
-                }
-                float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
-#pragma unroll
-                for (int c = 0; c < 128; c += 8) {
-                    t0 = fmax3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                    t1 = fmax3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-                    t2 = fmax3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-                    t3 = fmax3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-                }
-                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * mul;
-                if (__any_sync(0xffffffffu, top > m + kMoveLog2 || (m == -INFINITY && top > m))) {
-                    float alpha = 1.0f;
-                    if (top > m + kMoveLog2 || m == -INFINITY) {
-                        alpha = m == -INFINITY ? 0.0f : ex2_approx(m - top);
-                        m = top;
-                    }
-                    l *= alpha;
-                    if (i > 0) {                           // (these scores are there, so the last P V is done)
-#pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(o_addr + 16 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(o_addr + 16 * c, o);
-                        }
-                    }
-                }
-                const float neg_m = m == -INFINITY ? 0.0f : -m;
-                const uint64_t mul2 = f32x2_pack(mul, mul), neg2 = f32x2_pack(neg_m, neg_m);
                 uint64_t la = f32x2_pack(0.0f, 0.0f), lb = la;
+                // 32 keys at a time in a short loop (unrolled as a whole, the code would push the issuer's out of the instruction caches); P of a
+                // quarter goes over scores that were read already.
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32_wait(s_addr + 32 * c, s);
+                    if (key0 + 32 * c + 32 > first_limit) {
+                        const int keep = limit - key0 - 32 * c;
 #pragma unroll
-                for (int part = 0; part < 4; ++part) {
+                        for (int e = 0; e < 32; ++e) s[e] = e < keep ? s[e] : __float_as_uint(-INFINITY);
+                    }
+                    float t0 = -INFINITY, t1 = t0;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        t0 = fmax3(t0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                        t1 = fmax3(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                    }
+                    const float top = fmaxf(t0, t1) * mul;
+                    if (__any_sync(0xffffffffu, top > m + kMoveLog2))
+                        move_reference(top, m, l, la, lb, i > 0, c, s_addr, o_addr);
+                    const float neg_m = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t mul2 = f32x2_pack(mul, mul), neg2 = f32x2_pack(neg_m, neg_m);
                     uint32_t pw[16];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const uint32_t* v = s + 32 * part + c;
-                        const float2 z0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2, neg2));
-                        const float2 z1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[2]), __uint_as_float(v[3])), mul2, neg2));
+                    for (int e = 0; e < 32; e += 4) {
+                        const float2 z0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul2, neg2));
+                        const float2 z1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), mul2, neg2));
                         const float e0 = ex2_approx(z0.x), e1 = ex2_approx(z0.y), e2 = ex2_approx(z1.x), e3 = ex2_approx(z1.y);
                         la = f32x2_add(la, f32x2_pack(e0, e1));
                         lb = f32x2_add(lb, f32x2_pack(e2, e3));
-                        pw[c / 2] = pack_bf16x2(e0, e1);
-                        pw[c / 2 + 1] = pack_bf16x2(e2, e3);
+                        pw[e / 2] = pack_bf16x2(e0, e1);
+                        pw[e / 2 + 1] = pack_bf16x2(e2, e3);
                     }
-                    tmem_st16(s_addr + 16 * part, pw);
+                    tmem_st16(s_addr + 16 * c, pw);
                 }
                 const float2 sa = f32x2_unpack(la), sb = f32x2_unpack(lb);
                 l += (sa.x + sa.y) + (sb.x + sb.y);
