@@ -147,13 +147,14 @@ __device__ __forceinline__ void for_items(const RaggedArgs& p, const Ctl* ctl, F
 __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane) {
     const RaggedArgs& p = a.p;
     const unsigned full = 0xffffffffu;
-    int64_t total = 0;
+    int64_t total = 0, mine = 0;
     for (int b = 0; b < p.batch; b += 32) {
         int64_t n = 0;
         if (b + lane < p.batch) {
             const Seq s = seq_at(p, b + lane);
             n = units_of(s, tiles_of(s));
         }
+        mine = n;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(full, n, o);
         total += n;
@@ -170,10 +171,13 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
         int64_t before = 0;
         bool found[2] = {false, false};
         for (int b = 0; b < p.batch && !(found[0] && found[1]); b += 32) {
-            int64_t n = 0;
-            if (b + lane < p.batch) {
-                const Seq s = seq_at(p, b + lane);
-                n = units_of(s, tiles_of(s)) * p.heads;
+            int64_t n = mine * p.heads;                     // (of the only 32 sequences, or else read again)
+            if (p.batch > 32) {
+                n = 0;
+                if (b + lane < p.batch) {
+                    const Seq s = seq_at(p, b + lane);
+                    n = units_of(s, tiles_of(s)) * p.heads;
+                }
             }
             int64_t sum = n;
 #pragma unroll
@@ -228,20 +232,21 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
     a.headers[c] = header;
 }
 
-// Among eight lanes that hold eight 16-byte chunks of a row each: lane j's chunk e becomes lane e's chunk j, so that the lanes
-// then hold one chunk each of a whole 128-byte line (a warp's stores of 32 bytes in 32 lines take 130 cycles each, these a few).
-__device__ __forceinline__ void transpose8(uint32_t (&x)[8][4], int lane) {
+// Among four lanes that hold four 16-byte chunks of a row each: lane j's chunk e becomes lane e's chunk j, so that the lanes then hold
+// 64 bytes of one row (a warp's stores of 32 bytes in 32 rows take 130 cycles each; and this code, which runs once a tile, has
+// to be short, as it comes from beyond the instruction caches).
+__device__ __forceinline__ void transpose4(uint32_t (&x)[4][4], int lane) {
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1) {
+    for (int s = 1; s < 4; s <<= 1) {
         const bool up = (lane & s) != 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
             if (e & s) continue;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[e][k] : x[e | s][k], s);
-                if (up) x[e][k] = got;
-                else x[e | s][k] = got;
+                x[e][k] = up ? got : x[e][k];
+                x[e | s][k] = up ? x[e | s][k] : got;
             }
         }
     }
@@ -563,27 +568,17 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 const int64_t at = static_cast<int64_t>(it.s.q0 + it.row0 + 128 * h + 32 * w) * p.heads + it.head;   // of lane 0's row
                 if (lane < rows) p.lse[at + static_cast<int64_t>(lane) * p.heads] = lse2 * kLn2;
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t x[8][4];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32], x[4][4];
+                    if (n > 0) tmem_ld32_wait(o_addr + 32 * c, o);
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        uint32_t o[16];
-                        if (n > 0) {
-                            tmem_ld16(o_addr + 64 * c + 16 * d, o);
-                            tmem_wait_ld();
-                        }
+                    for (int e = 0; e < 16; ++e)
+                        x[e >> 2][e & 3] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+                    transpose4(x, lane);
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (at + static_cast<int64_t>(lane & 28) * p.heads) * 128 + 32 * c + 8 * (lane & 3);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            x[2 * d + (e >> 2)][e & 3] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
-                    }
-                    transpose8(x, lane);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = (lane & 24) + e;
-                        if (r < rows)
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (at + static_cast<int64_t>(r) * p.heads) * 128 + 64 * c +
-                                                      8 * (lane & 7)) = make_uint4(x[e][0], x[e][1], x[e][2], x[e][3]);
-                    }
+                    for (int e = 0; e < 4; ++e, dst += 128 * p.heads)
+                        if ((lane & 28) + e < rows) *reinterpret_cast<uint4*>(dst) = make_uint4(x[e][0], x[e][1], x[e][2], x[e][3]);
                 }
             }
             tc_fence_before_sync();
@@ -606,6 +601,7 @@ __global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restric
                                                           const int4* __restrict__ headers, const float* __restrict__ sink, int heads,
                                                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");   // (all CTAs of this grid are resident at once: nothing of it waits for an SM)
     const int c = blockIdx.x, lane = threadIdx.x & 31, dims = threadIdx.x >> 5, r = 32 * blockIdx.y + lane;
     const int4 hd = __ldcg(headers + c);
     if (hd.w == 0 || r >= hd.y) return;
