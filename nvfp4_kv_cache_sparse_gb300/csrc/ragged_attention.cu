@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
-                    if (n > 0) tmem_ld32_wait(o_addr + 32 * c, o);
+                    tmem_ld32_wait(o_addr + 32 * c, o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
 #pragma unroll
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32], x[4][4];
-                    if (n > 0) tmem_ld32_wait(o_addr + 32 * c, o);
+                    tmem_ld32_wait(o_addr + 32 * c, o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         x[e >> 2][e & 3] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
