@@ -28,18 +28,30 @@ using namespace tiles;
 constexpr int kUnits = 8;              // ring
 constexpr int kOffQ = 1024;
 constexpr int kOffRing = kOffQ + 6 * kBox;
-constexpr int kSmem = kOffRing + kUnits * kBox + 1024;
+constexpr int kSmem = kOffRing + kUnits * kBox;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr int kWarpLoad = 8, kWarpFix = 9, kWarpMma = 10;    // 10 and 11: products of the two halves; 0-3 and 4-7: their softmax
 constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;      // 2 x 128 x 208 + 128 x 88 = 384 x 168, the registers at launch
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;              // two halves of 128 columns each
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMoveLog2 = 8.0f;      // a reference moves when a score passes it by 2^8
+constexpr float kMoveLog2 = 8.0f;      // a reference moves, a block later, when a score passes it by 2^8,
+constexpr float kFarLog2 = 64.0f;      // and at once when one passes it by 2^64
 constexpr int kExtra = 1;              // what a tile costs besides its blocks, in blocks
 constexpr int kMinRun = 2;
+constexpr int kItems = 4;              // items that are known ahead
 constexpr int kMaxCtas = kPagedMaxSms;
+
+// A tile's part in a run.
+struct Item {
+    int q0, k0;                        // first query row of the tile and first key of its sequence, of all rows
+    int rows;                          // rows of the tile from its first one to the sequence's end
+    int seen;                          // keys that the tile's first row sees (negative: rows before the first key)
+    int keys;                          // of the sequence
+    int head, from, count0, count1;    // first block; blocks of each half
+    int slot;                          // of the part where the tile is cut, else -1
+    int valid;                         // 0: no more items
+};
 
 struct Ctl {
     // Block g of the CTA's run uses entry g & 1 of each; both issuers hand a block back, the values also the warp that cleans them.
@@ -47,13 +59,13 @@ struct Ctl {
     uint64_t q_full[2], q_free[2];     // a half's queries landed; its last scores are done
     uint64_t s_full[2];                // scores in tensor memory
     uint64_t p_full[2];                // 4 warps: P written, O rescaled
+    uint64_t turn[2];                  // the other half's chain of products is issued
     uint64_t o_done[2];                // a tile's last P V is done
     uint64_t v_clean[2];               // rows behind a sequence's end were zeroed (in turn: there may be the values of two tiles)
     uint64_t drain;
+    uint64_t item_full[kItems], item_empty[kItems];
     uint32_t tmem_base, abort;
-    // the first item of the CTA's run
-    int64_t u0, u1, total;
-    int seq, tile, head, b0;
+    Item items[kItems];                // what the CTA works on, one behind the other
 };
 static_assert(sizeof(Ctl) <= kOffQ, "control block");
 
@@ -101,50 +113,60 @@ __device__ __forceinline__ int64_t units_of(const Seq& s, int m) {
     return sum + static_cast<int64_t>(kExtra) * (m < count ? m : count);
 }
 
-// A tile's part in a run.
-struct Item {
+// The items of a CTA's run, in order.
+struct Walk {
+    int64_t left;
+    int seq, tile, head, b0;
     Seq s;
-    int head, row0;                    // rows row0 .. of the sequence
-    int from, count0, count1;          // first block; blocks of each half
-    bool used1;                        // the second half has rows
-    bool cut;
-    int slot;                          // of the part, where cut
-};
-
-// Calls f(item) for the items of the CTA's run, in order.
-template <typename F>
-__device__ __forceinline__ void for_items(const RaggedArgs& p, const Ctl* ctl, F f) {
-    int64_t left = ctl->u1 - ctl->u0;
-    int seq = ctl->seq, tile = ctl->tile, head = ctl->head, b0 = ctl->b0;
-    Item it;
-    if (left > 0) it.s = seq_at(p, seq);
-    while (left > 0) {
-        const int n0 = blocks_of(it.s, 256 * tile + 128), n = blocks_of(it.s, 256 * tile + 256), weight = n + kExtra;
+    __device__ __forceinline__ Item next(const RaggedArgs& p) {
+        Item it = {};
+        if (left <= 0) return it;
+        while (tile >= tiles_of(s)) {                       // (there is another one, as units are left)
+            s = seq_at(p, ++seq);
+            tile = 0;
+        }
+        const int row0 = 256 * tile;
+        const int n0 = blocks_of(s, row0 + 128), n = blocks_of(s, row0 + 256), weight = n + kExtra;
         const int take = static_cast<int>(min(left, static_cast<int64_t>(weight - b0))), b1 = b0 + take;
+        it.q0 = s.q0 + row0;
+        it.k0 = s.k0;
+        it.rows = s.lq - row0;
+        it.seen = s.lk - s.lq + row0 + 1;
+        it.keys = s.lk;
         it.head = head;
-        it.row0 = 256 * tile;
-        it.used1 = it.s.lq > it.row0 + 128;
         it.from = min(b0, n);
         it.count0 = max(min(b1, n0) - it.from, 0);
-        it.count1 = it.used1 ? min(b1, n) - it.from : 0;
-        it.cut = b0 > 0 || b1 < weight;
-        it.slot = 2 * static_cast<int>(blockIdx.x) + (b0 > 0 ? 0 : 1);
-        if (!f(it)) return;
+        it.count1 = it.rows > 128 ? min(b1, n) - it.from : 0;
+        it.slot = b0 > 0 || b1 < weight ? 2 * static_cast<int>(blockIdx.x) + (b0 > 0 ? 0 : 1) : -1;
+        it.valid = 1;
         left -= take;
         b0 = 0;
-        if (++head == p.heads) {
-            head = 0;
-            ++tile;
-            while (left > 0 && tile >= tiles_of(it.s)) {
-                it.s = seq_at(p, ++seq);
-                tile = 0;
-            }
-        }
+        if (++head == p.heads) head = 0, ++tile;
+        return it;
     }
-}
+};
+
+// What the warps read of the items: each takes them one behind the other and hands them back.
+struct Items {
+    Ctl* ctl;
+    int at = 0;
+    uint32_t phase = 0;
+    // nullptr: no more, or given up
+    __device__ __forceinline__ const Item* next(uint32_t* status) {
+        if (!wait_or_give_up(&ctl->item_full[at], phase, &ctl->abort, status) || ctl->items[at].valid == 0) return nullptr;
+        return &ctl->items[at];
+    }
+    __device__ __forceinline__ void step() {
+        if (++at == kItems) at = 0, phase ^= 1u;
+    }
+    __device__ __forceinline__ void done() {
+        mbar_arrive(&ctl->item_empty[at]);
+        step();
+    }
+};
 
 // One warp: where the CTA's run begins. Also its header, where the run's last tile goes on in the next run.
-__device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane) {
+__device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
     const RaggedArgs& p = a.p;
     const unsigned full = 0xffffffffu;
     int64_t total = 0, mine = 0;
@@ -164,13 +186,12 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
     const int64_t most = (total + kMinRun - 1) / kMinRun, g = most < gridDim.x ? most : gridDim.x, c = blockIdx.x;
     const int64_t u0 = c < g ? total * c / g : 0, u1 = c < g ? total * (c + 1) / g : 0;
     // the sequences that the first and the last unit lie in
-    int seq_of[2] = {0, 0};
-    int64_t at[2] = {0, 0};
-    const int64_t want[2] = {u0, u1 - 1};
+    int seq0 = 0, seq1 = 0;
+    int64_t at0 = 0, at1 = 0;
     if (u1 > u0) {
         int64_t before = 0;
-        bool found[2] = {false, false};
-        for (int b = 0; b < p.batch && !(found[0] && found[1]); b += 32) {
+        bool found0 = false, found1 = false;
+        for (int b = 0; b < p.batch && !(found0 && found1); b += 32) {
             int64_t n = mine * p.heads;                     // (of the only 32 sequences, or else read again)
             if (p.batch > 32) {
                 n = 0;
@@ -185,27 +206,30 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
                 const int64_t v = __shfl_up_sync(full, sum, o);
                 if (lane >= o) sum += v;
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const unsigned m = __ballot_sync(full, before + sum > want[e]);
-                if (!found[e] && m != 0u) {
-                    const int l = __ffs(m) - 1;
-                    seq_of[e] = b + l;
-                    at[e] = before + __shfl_sync(full, sum - n, l);
-                    found[e] = true;
-                }
+            const unsigned m0 = __ballot_sync(full, before + sum > u0), m1 = __ballot_sync(full, before + sum > u1 - 1);
+            if (!found0 && m0 != 0u) {
+                const int lane0 = __ffs(m0) - 1;
+                seq0 = b + lane0;
+                at0 = before + __shfl_sync(full, sum - n, lane0);
+                found0 = true;
+            }
+            if (!found1 && m1 != 0u) {
+                const int lane1 = __ffs(m1) - 1;
+                seq1 = b + lane1;
+                at1 = before + __shfl_sync(full, sum - n, lane1);
+                found1 = true;
             }
             before += __shfl_sync(full, sum, 31);
         }
     }
-    if (lane != 0) return;
+    Walk first = {};
     int4 header = make_int4(0, 0, 0, 0);
-    int first[4] = {0, 0, 0, 0};
     if (u1 > u0) {
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            const Seq s = seq_at(p, seq_of[e]);
-            const int64_t off = want[e] - at[e];
+            const int seq = e == 0 ? seq0 : seq1;
+            const Seq s = seq_at(p, seq);
+            const int64_t off = e == 0 ? u0 - at0 : u1 - 1 - at1;
             int lo = 0, hi = tiles_of(s);                   // units_of(lo) * heads <= off < units_of(hi) * heads
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -216,9 +240,11 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
             const int weight = blocks_of(s, 256 * lo + 256) + kExtra;
             const int head = static_cast<int>(in_tile / weight), b = static_cast<int>(in_tile - static_cast<int64_t>(head) * weight);
             if (e == 0) {
-                first[0] = seq_of[0], first[1] = lo, first[2] = head, first[3] = b;
+                first.left = u1 - u0;
+                first.seq = seq, first.tile = lo, first.head = head, first.b0 = b;
+                first.s = s;
             } else {
-                const int64_t begin = want[1] - b, end = begin + weight;
+                const int64_t begin = u1 - 1 - b, end = begin + weight;
                 if (begin >= u0 && end > u1) {
                     int parts = 1;
                     for (int64_t n = c + 1; n < g && total * n / g < end; ++n) ++parts;
@@ -227,9 +253,8 @@ __device__ __forceinline__ void find_run(const KernelArgs& a, Ctl* ctl, int lane
             }
         }
     }
-    ctl->u0 = u0, ctl->u1 = u1, ctl->total = total;
-    ctl->seq = first[0], ctl->tile = first[1], ctl->head = first[2], ctl->b0 = first[3];
-    a.headers[c] = header;
+    if (lane == 0) a.headers[c] = header;
+    return first;
 }
 
 // Among four lanes that hold four 16-byte chunks of a row each: lane j's chunk e becomes lane e's chunk j, so that the lanes then hold
@@ -252,22 +277,18 @@ __device__ __forceinline__ void transpose4(uint32_t (&x)[4][4], int lane) {
     }
 }
 
-// A warp's rows whose largest score so far (top, in log2 units) passes their reference m by 2^kMoveLog2 move it up to the next whole
-// number, and what was weighed against the old one is scaled: the row's sum l, this block's la and lb, its output (where there is
-// one) and the quarters of P that are written. The factors are powers of two, so nothing is rounded by it.
-__device__ __forceinline__ void move_reference(float top, float& m, float& l, uint64_t& la, uint64_t& lb, bool outputs, int quarters, uint32_t s_addr,
-                                            uint32_t o_addr) {
+// Moves the references m of a warp's rows up to `top` (log2 units; -inf: they stay), to the next whole number, and scales what was weighed
+// against the old ones: the row's sum l, its output (where there is one) and the quarters of P that are written. The factors
+// are powers of two, so nothing is rounded by it.
+__device__ __forceinline__ void move_reference(float top, float& m, float& l, bool outputs, int quarters, uint32_t s_addr, uint32_t o_addr) {
     float alpha = 1.0f;
-    if (top > m + kMoveLog2) {
+    if (top > m) {
         const float to = ceilf(top);
         alpha = m - to >= -126.0f ? __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(m - to)) << 23) : 0.0f;
         m = to;
     }
     l *= alpha;
-    const uint64_t alpha2 = f32x2_pack(alpha, alpha), zero2 = f32x2_pack(0.0f, 0.0f);
-    la = f32x2_fma(la, alpha2, zero2);
-    lb = f32x2_fma(lb, alpha2, zero2);
-    if (outputs) {                             // (these scores are there, so the last P V is done)
+    if (outputs) {
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -295,8 +316,8 @@ __device__ __forceinline__ void move_reference(float top, float& m, float& l, ui
 }
 
 __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __grid_constant__ KernelArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];   // (there is no static shared memory: it begins at a multiple of 1024)
+    uint8_t* smem = smem_raw;
     Ctl* ctl = reinterpret_cast<Ctl*>(smem);
     const uint32_t sbase = smem_addr(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -309,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_empty[i], 2), mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_empty[i], 3);
             mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
-            mbar_init(&ctl->s_full[i], 1), mbar_init(&ctl->p_full[i], 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->v_clean[i], 1);
+            mbar_init(&ctl->s_full[i], 1), mbar_init(&ctl->p_full[i], 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->turn[i], 1), mbar_init(&ctl->v_clean[i], 1);
         }
+        for (int i = 0; i < kItems; ++i) mbar_init(&ctl->item_full[i], 1), mbar_init(&ctl->item_empty[i], 11);   // 8 softmax warps, two issuers, loads
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
         fence_barrier_init();
@@ -321,7 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    if (warp == kWarpFix) find_run(a, ctl, lane);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -329,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
     uint32_t* abort = &ctl->abort;
     uint32_t* status = p.status;
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp >= kWarpLoad) {
         if (warp == kWarpLoad) {
             if (lane == 0) {
                 // Eight units hold three groups in flight: the keys of block g lie where the values of block g - 2 and what came before lay,
@@ -338,21 +358,23 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 int unit = 0, g = 0;
                 uint32_t q_phase = 3;                        // one bit for each half
                 auto step = [&] { unit = unit + 1 == kUnits ? 0 : unit + 1; };
-                for_items(p, ctl, [&](const Item& it) -> bool {
+                Items items = {ctl};
+                for (const Item* next = items.next(status); next != nullptr; items.done(), next = items.next(status)) {
+                    const Item it = *next;
                     const int n = max(it.count0, it.count1);
-                    if (n == 0) return true;
+                    if (n == 0) continue;
                     auto load_q = [&](int h) -> bool {
                         if ((h == 0 ? it.count0 : it.count1) == 0) return true;
                         if (!wait_or_give_up(&ctl->q_free[h], (q_phase >> h) & 1, abort, status)) return false;
                         q_phase ^= 1u << h;
                         mbar_arrive_expect_tx(&ctl->q_full[h], 3 * kBox);
                         for (int c = 0; c < 3; ++c)
-                            tma_load_3d(sbase + kOffQ + (3 * h + c) * kBox, &a.q_map, 64 * c, it.head, it.s.q0 + it.row0 + 128 * h, &ctl->q_full[h]);
+                            tma_load_3d(sbase + kOffQ + (3 * h + c) * kBox, &a.q_map, 64 * c, it.head, it.q0 + 128 * h, &ctl->q_full[h]);
                         return true;
                     };
                     auto load_k = [&](int i) -> bool {
                         if (g >= 2 && !wait_or_give_up(&ctl->v_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) return false;
-                        const int row = it.s.k0 + 128 * (it.from + i);
+                        const int row = it.k0 + 128 * (it.from + i);
                         uint64_t* bar = &ctl->k_full[g & 1];
                         mbar_arrive_expect_tx(bar, 3 * kBox);
                         for (int c = 0; c < 3; ++c, step()) {
@@ -363,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     };
                     auto load_v = [&](int i) -> bool {
                         if (g >= 1 && !wait_or_give_up(&ctl->k_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, status)) return false;
-                        const int row = it.s.k0 + 128 * (it.from + i);
+                        const int row = it.k0 + 128 * (it.from + i);
                         uint64_t* bar = &ctl->v_full[g & 1];
                         mbar_arrive_expect_tx(bar, 2 * kBox);
                         for (int c = 0; c < 2; ++c, step()) {
@@ -373,11 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         ++g;
                         return true;
                     };
-                    if (!load_q(0) || !load_k(0) || !load_q(1) || !load_v(0)) return false;
-                    for (int i = 1; i < n; ++i)
-                        if (!load_k(i) || !load_v(i)) return false;
-                    return true;
-                });
+                    bool ok = load_q(0) && load_k(0) && load_q(1) && load_v(0);
+                    for (int i = 1; i < n && ok; ++i) ok = load_k(i) && load_v(i);
+                    if (!ok) break;
+                }
             }
             __syncwarp();
         } else if (warp >= kWarpMma) {
@@ -393,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);         // MN-major: dims x keys
                 const uint32_t s_addr = tmem + kColS + 128 * h, o_addr = tmem + kColO + 128 * h;
                 int unit = 0, g = 0, cleans = 0;                                           // g: blocks whose values were waited for
-                uint32_t q_phase = 0, p_phase = 0;
+                uint32_t q_phase = 0, p_phase = 0, turn_phase = h == 0 ? 1u : 0u;
                 auto scores = [&](int at) {                 // S from the three units at `at`
                     tc_fence_after_sync();
 #pragma unroll 1
@@ -404,27 +425,46 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     }
                     mma_commit(&ctl->s_full[h]);
                 };
-                for_items(p, ctl, [&](const Item& it) -> bool {
-                    const int n = max(it.count0, it.count1), count = h == 0 ? it.count0 : it.count1;
-                    if (n == 0) return true;
+                Items items = {ctl};
+                bool ok = true;
+                for (const Item* next = items.next(status); next != nullptr; items.done(), next = items.next(status)) {
+                    const int n = max(next->count0, next->count1), count = h == 0 ? next->count0 : next->count1;
+                    const int whole = (next->keys >> 7) - next->from;      // blocks before the one that the sequence ends in
+                    if (n == 0) continue;
                     if (count > 0) {                        // the first block's scores
-                        if (!wait_or_give_up(&ctl->k_full[g & 1], (g >> 1) & 1, abort, status)) return false;
-                        if (!wait_or_give_up(&ctl->q_full[h], q_phase, abort, status)) return false;
+                        ok = wait_or_give_up(&ctl->k_full[g & 1], (g >> 1) & 1, abort, status) && wait_or_give_up(&ctl->q_full[h], q_phase, abort, status);
+                        if (!ok) break;
                         q_phase ^= 1u;
+                    }
+                    ok = wait_or_give_up(&ctl->turn[h], turn_phase, abort, status);
+                    if (!ok) break;
+                    turn_phase ^= 1u;
+                    if (count > 0) {
                         scores(unit);
                         if (count == 1) mma_commit(&ctl->q_free[h]);
                     }
+                    mbar_arrive(&ctl->turn[h ^ 1]);
                     mma_commit(&ctl->k_empty[g & 1]);
 #pragma unroll 1
                     for (int i = 0; i < n; ++i, ++g) {
-                        if (!wait_or_give_up(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status)) return false;
-                        if (128 * (it.from + i + 1) > it.s.lk) {
-                            if (!wait_or_give_up(&ctl->v_clean[cleans & 1], (cleans >> 1) & 1, abort, status)) return false;
+                        ok = wait_or_give_up(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status);
+                        if (ok && i >= whole) {
+                            ok = wait_or_give_up(&ctl->v_clean[cleans & 1], (cleans >> 1) & 1, abort, status);
                             ++cleans;
                         }
+                        if (!ok) break;
+                        bool keys_here = false;
                         if (i < count) {                    // O (+)= P V
-                            if (!wait_or_give_up(&ctl->p_full[h], p_phase, abort, status)) return false;
+                            // (the next keys are mostly there already: seen to while P is not)
+                            keys_here = i + 1 < count && mbar_test_wait(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+                            ok = wait_or_give_up(&ctl->p_full[h], p_phase, abort, status);
+                            if (!ok) break;
                             p_phase ^= 1u;
+                        }
+                        ok = wait_or_give_up(&ctl->turn[h], turn_phase, abort, status);
+                        if (!ok) break;
+                        turn_phase ^= 1u;
+                        if (i < count) {
                             tc_fence_after_sync();
 #pragma unroll 1
                             for (int c = 0; c < 2; ++c) {
@@ -438,29 +478,49 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         mma_commit(&ctl->v_empty[g & 1]);
                         unit = (unit + 5) & (kUnits - 1);
                         if (i + 1 < count) {
-                            if (!wait_or_give_up(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, status)) return false;
+                            ok = keys_here || wait_or_give_up(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, status);
+                            if (!ok) break;
                             scores(unit);
                             if (i + 2 == count) mma_commit(&ctl->q_free[h]);
                         }
+                        mbar_arrive(&ctl->turn[h ^ 1]);
                         if (i + 1 < n) mma_commit(&ctl->k_empty[(g + 1) & 1]);
                     }
-                    return true;
-                });
+                    if (!ok) break;
+                }
                 mma_commit(&ctl->drain);
                 wait_or_give_up(&ctl->drain, 0, abort, status);
             }
             __syncwarp();
         } else if (warp == kWarpFix) {
+            // The CTA's items, one ahead of the one that is worked on.
+            Walk walk = find_run(a, lane);
+            int slot = 0;
+            uint32_t slot_phase = 1;
+            auto publish = [&](const Item& it) -> bool {
+                if (!wait_warp(&ctl->item_empty[slot], slot_phase, abort, status)) return false;
+                if (lane == 0) {
+                    ctl->items[slot] = it;
+                    mbar_arrive(&ctl->item_full[slot]);
+                }
+                if (++slot == kItems) slot = 0, slot_phase ^= 1u;
+                return true;
+            };
             // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN.
             // (The warp takes note of every block and hands it back beside the products, so that it stays within the ring.)
             int unit = 0, g = 0, cleans = 0;
-            for_items(p, ctl, [&](const Item& it) -> bool {
+            Item it = walk.next(p);
+            bool ok = publish(it);
+            while (ok && it.valid) {
+                const Item ahead = walk.next(p);
+                ok = publish(ahead);
                 const int n = max(it.count0, it.count1);
 #pragma unroll 1
-                for (int i = 0; i < n; ++i, ++g) {
-                    const int left = it.s.lk - 128 * (it.from + i);
+                for (int i = 0; i < n && ok; ++i, ++g) {
+                    const int left = it.keys - 128 * (it.from + i);
                     unit = (unit + 3) & (kUnits - 1);
-                    if (!wait_warp(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status)) return false;
+                    ok = wait_warp(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status);
+                    if (!ok) break;
                     if (left < 128) {
                         for (int c = 0; c < 2; ++c) {
                             const uint32_t base = sbase + kOffRing + ((unit + c) & (kUnits - 1)) * kBox;
@@ -477,63 +537,77 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     unit = (unit + 2) & (kUnits - 1);
                     if (lane == 0) mbar_arrive(&ctl->v_empty[g & 1]);
                 }
-                return true;
-            });
+                it = ahead;
+            }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int h = warp >> 2, w = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w) << 16);
         const uint32_t s_addr = lanes + kColS + 128 * h, o_addr = lanes + kColO + 128 * h;
         const float mul = p.sm_scale == 0.0f ? 1e-30f : fabsf(p.sm_scale) * kLog2e;   // (0 x -inf would be NaN where a key is masked)
-        int seen = 0, done = 0;        // blocks and tiles of this half so far
-        for_items(p, ctl, [&](const Item& it) -> bool {
-            if (h == 1 && !it.used1) return true;
-            const int row = it.row0 + 128 * h + 32 * w + lane;          // of the sequence
-            const int limit = min(it.s.lk - it.s.lq + row + 1, it.s.lk);   // keys that the row sees
-            const int first_limit = it.s.lk - it.s.lq + it.row0 + 128 * h + 1;
-            const int n = h == 0 ? it.count0 : it.count1;
-            float m = -INFINITY, l = 0.0f;
+        int seen = 0;                  // blocks of this half so far
+        uint32_t done = 0;             // and tiles
+        Items items = {ctl};
+        bool ok = true;
+        for (;;) {
+            const Item* const it = items.next(status);
+            if (it == nullptr) break;
+            const int n = h == 0 ? it->count0 : it->count1;
+            // keys that the row, and the half's first row, see of those from the first block on
+            const int limit = min(it->seen + 128 * h + 32 * w + lane, it->keys) - 128 * it->from;
+            const int first_limit = it->seen + 128 * h - 128 * it->from;
+            float m = -INFINITY, l = 0.0f, top = -INFINITY;   // top: what the reference moves up to, if anything
             for (int i = 0; i < n; ++i, ++seen) {
-                if (!wait_warp(&ctl->s_full[h], seen & 1, abort, status)) return false;
+                ok = wait_warp(&ctl->s_full[h], seen & 1, abort, status);
+                if (!ok) break;
                 tc_fence_after_sync();
-                const int key0 = 128 * (it.from + i);
+                // The reference follows a block behind: weights up to 2^kMoveLog2 above it are as good as others in bf16 and fp32, so that nobody
+                // has to wait for a block's largest score before its weights. (These scores are there, so the last P V is done.)
+                float most = -INFINITY;
+                if (__any_sync(0xffffffffu, top > m)) move_reference(top, m, l, i > 0, 0, s_addr, o_addr);
                 uint64_t la = f32x2_pack(0.0f, 0.0f), lb = la;
-                // 32 keys at a time in a short loop (unrolled as a whole, the code would push the issuer's out of the instruction caches); P of a
+                // 32 keys at a time in a short loop (unrolled as a whole, the code would push the issuers' out of the instruction caches); P of a
                 // quarter goes over scores that were read already.
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32];
+                    uint32_t s[32], pw[16];
                     tmem_ld32_wait(s_addr + 32 * c, s);
-                    if (key0 + 32 * c + 32 > first_limit) {
-                        const int keep = limit - key0 - 32 * c;
+                    if (128 * i + 32 * c + 32 > first_limit) {
+                        const int keep = limit - 128 * i - 32 * c;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[e] = e < keep ? s[e] : __float_as_uint(-INFINITY);
                     }
                     float t0 = -INFINITY, t1 = t0;
+                    uint64_t pa, pb;
+                    for (;;) {
+                        const float neg_m = m == -INFINITY ? 0.0f : -m;
+                        const uint64_t mul2 = f32x2_pack(mul, mul), neg2 = f32x2_pack(neg_m, neg_m);
+                        pa = la, pb = lb;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        t0 = fmax3(t0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                        t1 = fmax3(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                        for (int e = 0; e < 32; e += 4) {
+                            const float2 z0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul2, neg2));
+                            const float2 z1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), mul2, neg2));
+                            const float e0 = ex2_approx(z0.x), e1 = ex2_approx(z0.y), e2 = ex2_approx(z1.x), e3 = ex2_approx(z1.y);
+                            pa = f32x2_add(pa, f32x2_pack(e0, e1));
+                            pb = f32x2_add(pb, f32x2_pack(e2, e3));
+                            pw[e / 2] = pack_bf16x2(e0, e1);
+                            pw[e / 2 + 1] = pack_bf16x2(e2, e3);
+                            t0 = fmax3(t0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                            t1 = fmax3(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                        }
+                        top = fmaxf(t0, t1) * mul;
+                        if (!__any_sync(0xffffffffu, top > m + kFarLog2)) break;
+                        // too far above (or the first keys that the row sees): the reference moves now, and these weights are worked out again
+                        const float2 sa = f32x2_unpack(la), sb = f32x2_unpack(lb);
+                        l += (sa.x + sa.y) + (sb.x + sb.y);
+                        la = lb = f32x2_pack(0.0f, 0.0f);
+                        move_reference(top > m + kFarLog2 ? top : -INFINITY, m, l, i > 0, c, s_addr, o_addr);
                     }
-                    const float top = fmaxf(t0, t1) * mul;
-                    if (__any_sync(0xffffffffu, top > m + kMoveLog2))
-                        move_reference(top, m, l, la, lb, i > 0, c, s_addr, o_addr);
-                    const float neg_m = m == -INFINITY ? 0.0f : -m;
-                    const uint64_t mul2 = f32x2_pack(mul, mul), neg2 = f32x2_pack(neg_m, neg_m);
-                    uint32_t pw[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float2 z0 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul2, neg2));
-                        const float2 z1 = f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), mul2, neg2));
-                        const float e0 = ex2_approx(z0.x), e1 = ex2_approx(z0.y), e2 = ex2_approx(z1.x), e3 = ex2_approx(z1.y);
-                        la = f32x2_add(la, f32x2_pack(e0, e1));
-                        lb = f32x2_add(lb, f32x2_pack(e2, e3));
-                        pw[e / 2] = pack_bf16x2(e0, e1);
-                        pw[e / 2 + 1] = pack_bf16x2(e2, e3);
-                    }
+                    la = pa, lb = pb;
+                    most = fmaxf(most, top);
                     tmem_st16(s_addr + 16 * c, pw);
                 }
+                top = most > m + kMoveLog2 ? most : -INFINITY;
                 const float2 sa = f32x2_unpack(la), sb = f32x2_unpack(lb);
                 l += (sa.x + sa.y) + (sb.x + sb.y);
                 tmem_wait_st();
@@ -542,19 +616,20 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 if (lane == 0) mbar_arrive(&ctl->p_full[h]);
             }
             if (n > 0) {
-                if (!wait_warp(&ctl->o_done[h], done++ & 1, abort, status)) return false;
+                ok = ok && wait_warp(&ctl->o_done[h], done++ & 1, abort, status);
+                if (!ok) break;
                 tc_fence_after_sync();
             }
-            const int rows = it.s.lq - (it.row0 + 128 * h + 32 * w);    // rows of this warp (32 and more: all)
+            const int rows = it->rows - 128 * h - 32 * w;      // of this warp (32 and more: all)
+            const int head = it->head, slot = it->slot;
             const bool empty = l == 0.0f;
             const float lse2 = empty ? -INFINITY : m + log2f(l);
             float f = empty ? 0.0f : 1.0f / l;
-            if (!it.cut && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + it.head) * kLog2e - m));
+            if (slot < 0 && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + head) * kLog2e - m));
             const bool none = n == 0 || empty;
-            if (it.cut) {
-                if (rows <= 0) return true;
-                a.part_lse[static_cast<int64_t>(it.slot) * 256 + 128 * h + 32 * w + lane] = lse2;
-                float* dst = a.part_out + (static_cast<int64_t>(it.slot) * 8 + warp) * 4096 + 8 * lane;
+            if (slot >= 0 && rows > 0) {
+                a.part_lse[static_cast<int64_t>(slot) * 256 + 128 * h + 32 * w + lane] = lse2;
+                float* dst = a.part_out + (static_cast<int64_t>(slot) * 8 + 4 * h + w) * 4096 + 8 * lane;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
@@ -564,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st_sector(dst + (4 * c + e) * 256, o + 8 * e);
                 }
-            } else {
-                const int64_t at = static_cast<int64_t>(it.s.q0 + it.row0 + 128 * h + 32 * w) * p.heads + it.head;   // of lane 0's row
+            } else if (rows > 0) {
+                const int64_t at = static_cast<int64_t>(it->q0 + 128 * h + 32 * w) * p.heads + head;   // of lane 0's row
                 if (lane < rows) p.lse[at + static_cast<int64_t>(lane) * p.heads] = lse2 * kLn2;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -582,8 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 }
             }
             tc_fence_before_sync();
-            return true;
-        });
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->item_empty[items.at]);
+            items.step();
+        }
     }
     tc_fence_before_sync();
     __syncthreads();
