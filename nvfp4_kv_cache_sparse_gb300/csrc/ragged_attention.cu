@@ -10,13 +10,21 @@
 //
 // A tile is 256 query rows of one sequence and head, in two halves of 128. S = Q K^T of a half is one tcgen05.mma chain
 // (M = 128 rows, N = 128 keys, K = 192) into tensor memory; a warpgroup per half turns it into P, which overwrites S
-// and feeds P V from tensor memory. While one half's softmax runs, the tensor cores work for the other. Keys and
-// values come through a ring of eight 16 KB units (a key block is three units of 128 keys x 64 dims, its values two
-// units of 64 keys x 128 dims).
+// and feeds P V from tensor memory. While one half's softmax runs, the tensor cores work for the other: the halves' chains (P V of a
+// block, S of the next) take turns. Keys and values come through a ring of eight 16 KB units (a key block is three units of 128 keys x
+// 64 dims, its values two units of 64 keys x 128 dims).
+// What bounds one CTA is that ring: a block's keys can be sent for only when both halves are done with the values of the block
+// before the last, some 1300 cycles before they are needed (waits of 500 to 1000 cycles a block of 3550, of which the products
+// take 2560). So long sequences go to CTA pairs (kPair): tiles of 512 rows in halves of 256 (M = 256, tcgen05.mma on the pair), each CTA
+// with its own 128 rows of either half and half of the keys and values, three blocks of them in flight, and half the reads from L2.
 //
-// Tiles are of very different lengths and often fewer than SMs, so the CTAs, one per SM, take equal runs of (tile, head, block
+// Tiles are of very different lengths and often fewer than SMs, so the CTAs (or pairs), one per SM, take equal runs of (tile, head, block
 // of 128 keys) units, heads inside tiles: neighbouring tiles of a head are then read by several CTAs at about the same
 // time, from L2. A tile that two runs share leaves fp32 parts in the workspace, which a second kernel joins.
+//
+// 2048 rows over 16640 keys, 64 heads: 760 us, 1.72 PFLOP/s (one CTA each: 868); 4 chunks of 512 rows over 500 to 16000 keys, 16 heads:
+// 139 us, 1.45 PFLOP/s (159); 16 prompts of 30 to 700 tokens, 16 heads: 47 us on one CTA each, where a tile's first loads, its softmax and
+// its way out (4 us) count more than its few blocks.
 #include "head_tiles.cuh"
 #include "launch.h"
 
@@ -25,11 +33,17 @@ namespace {
 
 using namespace tiles;
 
-constexpr int kUnits = 8;              // ring
+constexpr int kUnits = 8;              // ring of one CTA
 constexpr int kOffQ = 1024;
 constexpr int kOffRing = kOffQ + 6 * kBox;
 constexpr int kSmem = kOffRing + kUnits * kBox;
 static_assert(kSmem <= 232448, "shared memory");
+// One CTA or a pair (kPair): rows of a half and of a tile, blocks of keys, and of values, that the ring holds.
+template <bool kPair> constexpr int kHalf = kPair ? 256 : 128;
+template <bool kPair> constexpr int kTile = 2 * kHalf<kPair>;
+template <bool kPair> constexpr int kDepth = kPair ? 3 : 2;
+constexpr int kPairK = 3 * kBox / 2, kOffPairV = kOffRing + 3 * kPairK;   // a pair's CTA: 64 keys x 192 dims, then 128 keys x 64 dims of values
+static_assert(kOffPairV + 3 * kBox <= kSmem, "shared memory");
 constexpr int kWarpLoad = 8, kWarpFix = 9, kWarpMma = 10;    // 10 and 11: products of the two halves; 0-3 and 4-7: their softmax
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
@@ -54,14 +68,15 @@ struct Item {
 };
 
 struct Ctl {
-    // Block g of the CTA's run uses entry g & 1 of each; both issuers hand a block back, the values also the warp that cleans them.
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    // Block g of the run uses entry g % kDepth of each. k_full, v_ready, q_full, p_full, turn and drain count in CTA 0 of a pair, where the
+    // products are issued; what those hand back is counted in both CTAs.
+    uint64_t k_full[3], k_empty[3], v_empty[3];   // (both issuers hand a block back)
+    uint64_t v_full[3], v_ready[3];    // this CTA's values landed; they are clean (from each CTA)
     uint64_t q_full[2], q_free[2];     // a half's queries landed; its last scores are done
     uint64_t s_full[2];                // scores in tensor memory
-    uint64_t p_full[2];                // 4 warps: P written, O rescaled
+    uint64_t p_full[2];                // 4 warps of each CTA: P written, O rescaled
     uint64_t turn[2];                  // the other half's chain of products is issued
     uint64_t o_done[2];                // a tile's last P V is done
-    uint64_t v_clean[2];               // rows behind a sequence's end were zeroed (in turn: there may be the values of two tiles)
     uint64_t drain;
     uint64_t item_full[kItems], item_empty[kItems];
     uint32_t tmem_base, abort;
@@ -71,13 +86,13 @@ static_assert(sizeof(Ctl) <= kOffQ, "control block");
 
 struct KernelArgs {
     CUtensorMap q_map;                 // [rows_q, heads, 192], box 128 x 1 x 64
-    CUtensorMap k_map;                 // kv [rows_k, heads, 256], box 128 x 1 x 64
-    CUtensorMap v_map;                 // the same, box 64 x 1 x 64
-    CUtensorMap pe_map;                // [rows_k, 1, 64], box 128 x 1 x 64
+    CUtensorMap k_map;                 // kv [rows_k, heads, 256], box 128 x 1 x 64; for a pair 64 x 1 x 64
+    CUtensorMap v_map;                 // the same, box 64 x 1 x 64; for a pair 128 x 1 x 64
+    CUtensorMap pe_map;                // [rows_k, 1, 64], box as k_map's
     RaggedArgs p;
-    float* part_out;                   // [2 CTAs, 8 warps, 16, 32 lanes, 8]: eight dims of a row, divided by its own sum
-    float* part_lse;                   // [2 CTAs, 256], log2
-    int4* headers;                     // [CTAs]: first output row, rows, head, parts (0: no tile begins here and ends elsewhere)
+    float* part_out;                   // [2 runs, rows of a tile / 32, 16, 32 lanes, 8]: eight dims of a row, divided by its own sum
+    float* part_lse;                   // [2 runs, rows of a tile], log2
+    int4* headers;                     // [runs]: first output row, rows, head, parts (0: no tile begins here and ends elsewhere)
 };
 
 struct Seq {
@@ -92,41 +107,45 @@ __device__ __forceinline__ Seq seq_at(const RaggedArgs& p, int b) {
     s.lk = max(clamp_start(__ldg(p.starts_k + b + 1), p.rows_k) - s.k0, 0);
     return s;
 }
-__device__ __forceinline__ int tiles_of(const Seq& s) { return (s.lq + 255) >> 8; }
+template <bool kPair>
+__device__ __forceinline__ int tiles_of(const Seq& s) { return (s.lq + kTile<kPair> - 1) / kTile<kPair>; }
 // Key blocks of rows [0, rows) of a sequence: its last row sees the first lk - lq + rows keys.
 __device__ __forceinline__ int blocks_of(const Seq& s, int rows) {
     const int keys = s.lk - s.lq + min(rows, s.lq);
     return keys <= 0 ? 0 : (keys + 127) >> 7;
 }
-// Units of the first m tiles: a tile before the last one ends on a multiple of 256 rows, tile j has max(0, p + 2 (j + 1)) blocks
-// with p = ceil((lk - lq) / 128), and kExtra.
+// Units of the first m tiles: a tile before the last one ends on a multiple of kTile rows, tile j has max(0, p + r (j + 1)) blocks
+// with p = ceil((lk - lq) / 128) and r = kTile / 128, and kExtra.
+template <bool kPair>
 __device__ __forceinline__ int64_t units_of(const Seq& s, int m) {
-    const int count = tiles_of(s);
+    constexpr int r = kTile<kPair> / 128;
+    const int count = tiles_of<kPair>(s);
     if (m <= 0) return 0;
     const int whole = m < count ? m : count - 1;            // tiles that are surely full
     const int64_t pre = (s.lk - s.lq + 127) >> 7;           // (rounds up for negative ones too)
-    int64_t none = pre < 0 ? (-pre) >> 1 : 0;               // tiles without keys
+    int64_t none = pre < 0 ? -pre / r : 0;                  // tiles without keys
     if (none > whole) none = whole;
     const int64_t a = none + 1, n = whole - none;           // j + 1 = a .. whole
-    int64_t sum = n * pre + n * (a + whole);
+    int64_t sum = n * pre + (r / 2) * n * (a + whole);
     if (m >= count) sum += blocks_of(s, s.lq);
     return sum + static_cast<int64_t>(kExtra) * (m < count ? m : count);
 }
 
-// The items of a CTA's run, in order.
+// The items of a run (a CTA's, or a pair's), in order.
+template <bool kPair>
 struct Walk {
     int64_t left;
     int seq, tile, head, b0;
     Seq s;
-    __device__ __forceinline__ Item next(const RaggedArgs& p) {
+    __device__ __forceinline__ Item next(const RaggedArgs& p, int run) {
         Item it = {};
         if (left <= 0) return it;
-        while (tile >= tiles_of(s)) {                       // (there is another one, as units are left)
+        while (tile >= tiles_of<kPair>(s)) {                       // (there is another one, as units are left)
             s = seq_at(p, ++seq);
             tile = 0;
         }
-        const int row0 = 256 * tile;
-        const int n0 = blocks_of(s, row0 + 128), n = blocks_of(s, row0 + 256), weight = n + kExtra;
+        const int row0 = kTile<kPair> * tile;
+        const int n0 = blocks_of(s, row0 + kHalf<kPair>), n = blocks_of(s, row0 + kTile<kPair>), weight = n + kExtra;
         const int take = static_cast<int>(min(left, static_cast<int64_t>(weight - b0))), b1 = b0 + take;
         it.q0 = s.q0 + row0;
         it.k0 = s.k0;
@@ -136,8 +155,8 @@ struct Walk {
         it.head = head;
         it.from = min(b0, n);
         it.count0 = max(min(b1, n0) - it.from, 0);
-        it.count1 = it.rows > 128 ? min(b1, n) - it.from : 0;
-        it.slot = b0 > 0 || b1 < weight ? 2 * static_cast<int>(blockIdx.x) + (b0 > 0 ? 0 : 1) : -1;
+        it.count1 = it.rows > kHalf<kPair> ? min(b1, n) - it.from : 0;
+        it.slot = b0 > 0 || b1 < weight ? 2 * run + (b0 > 0 ? 0 : 1) : -1;
         it.valid = 1;
         left -= take;
         b0 = 0;
@@ -165,8 +184,9 @@ struct Items {
     }
 };
 
-// One warp: where the CTA's run begins. Also its header, where the run's last tile goes on in the next run.
-__device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
+// One warp: where run c of `runs` begins. Also its header, where the run's last tile goes on in the next run.
+template <bool kPair>
+__device__ __forceinline__ Walk<kPair> find_run(const KernelArgs& a, int c, int runs, int lane) {
     const RaggedArgs& p = a.p;
     const unsigned full = 0xffffffffu;
     int64_t total = 0, mine = 0;
@@ -174,7 +194,7 @@ __device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
         int64_t n = 0;
         if (b + lane < p.batch) {
             const Seq s = seq_at(p, b + lane);
-            n = units_of(s, tiles_of(s));
+            n = units_of<kPair>(s, tiles_of<kPair>(s));
         }
         mine = n;
 #pragma unroll
@@ -183,7 +203,7 @@ __device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
     }
     total *= p.heads;
     // (a run has at least kMinRun units: shorter ones would be all parts and joining)
-    const int64_t most = (total + kMinRun - 1) / kMinRun, g = most < gridDim.x ? most : gridDim.x, c = blockIdx.x;
+    const int64_t most = (total + kMinRun - 1) / kMinRun, g = most < runs ? most : runs;
     const int64_t u0 = c < g ? total * c / g : 0, u1 = c < g ? total * (c + 1) / g : 0;
     // the sequences that the first and the last unit lie in
     int seq0 = 0, seq1 = 0;
@@ -197,7 +217,7 @@ __device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
                 n = 0;
                 if (b + lane < p.batch) {
                     const Seq s = seq_at(p, b + lane);
-                    n = units_of(s, tiles_of(s)) * p.heads;
+                    n = units_of<kPair>(s, tiles_of<kPair>(s)) * p.heads;
                 }
             }
             int64_t sum = n;
@@ -222,7 +242,7 @@ __device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
             before += __shfl_sync(full, sum, 31);
         }
     }
-    Walk first = {};
+    Walk<kPair> first = {};
     int4 header = make_int4(0, 0, 0, 0);
     if (u1 > u0) {
 #pragma unroll 1
@@ -230,14 +250,14 @@ __device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
             const int seq = e == 0 ? seq0 : seq1;
             const Seq s = seq_at(p, seq);
             const int64_t off = e == 0 ? u0 - at0 : u1 - 1 - at1;
-            int lo = 0, hi = tiles_of(s);                   // units_of(lo) * heads <= off < units_of(hi) * heads
+            int lo = 0, hi = tiles_of<kPair>(s);                   // units_of(lo) * heads <= off < units_of(hi) * heads
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (units_of(s, mid) * p.heads <= off) lo = mid;
+                if (units_of<kPair>(s, mid) * p.heads <= off) lo = mid;
                 else hi = mid;
             }
-            const int64_t in_tile = off - units_of(s, lo) * p.heads;
-            const int weight = blocks_of(s, 256 * lo + 256) + kExtra;
+            const int64_t in_tile = off - units_of<kPair>(s, lo) * p.heads;
+            const int weight = blocks_of(s, kTile<kPair> * (lo + 1)) + kExtra;
             const int head = static_cast<int>(in_tile / weight), b = static_cast<int>(in_tile - static_cast<int64_t>(head) * weight);
             if (e == 0) {
                 first.left = u1 - u0;
@@ -248,12 +268,12 @@ __device__ __forceinline__ Walk find_run(const KernelArgs& a, int lane) {
                 if (begin >= u0 && end > u1) {
                     int parts = 1;
                     for (int64_t n = c + 1; n < g && total * n / g < end; ++n) ++parts;
-                    header = make_int4(s.q0 + 256 * lo, min(256, s.lq - 256 * lo), head, parts);
+                    header = make_int4(s.q0 + kTile<kPair> * lo, min(kTile<kPair>, s.lq - kTile<kPair> * lo), head, parts);
                 }
             }
         }
     }
-    if (lane == 0) a.headers[c] = header;
+    if (lane == 0 && (!kPair || cluster_ctarank() == 0)) a.headers[c] = header;
     return first;
 }
 
@@ -315,48 +335,68 @@ __device__ __forceinline__ void move_reference(float top, float& m, float& l, bo
     }
 }
 
+template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __grid_constant__ KernelArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];   // (there is no static shared memory: it begins at a multiple of 1024)
     uint8_t* smem = smem_raw;
     Ctl* ctl = reinterpret_cast<Ctl*>(smem);
     const uint32_t sbase = smem_addr(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+    const int run = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x), runs = kPair ? gridDim.x >> 1 : gridDim.x;
     const RaggedArgs& p = a.p;
     if (warp == kWarpLoad && lane == 0) {
         prefetch_map(&a.q_map);
         prefetch_map(&a.k_map);
         prefetch_map(&a.v_map);
         prefetch_map(&a.pe_map);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_empty[i], 2), mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_empty[i], 3);
-            mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
-            mbar_init(&ctl->s_full[i], 1), mbar_init(&ctl->p_full[i], 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->turn[i], 1), mbar_init(&ctl->v_clean[i], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_empty[i], 2), mbar_init(&ctl->v_empty[i], 2);
+            mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_ready[i], kPair ? 2 : 1);
         }
-        for (int i = 0; i < kItems; ++i) mbar_init(&ctl->item_full[i], 1), mbar_init(&ctl->item_empty[i], 11);   // 8 softmax warps, two issuers, loads
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1), mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_full[i], kPair ? 8 : 4), mbar_init(&ctl->o_done[i], 1), mbar_init(&ctl->turn[i], 1);
+        }
+        // (an item is read by 8 softmax warps, the loads and, in CTA 0, two issuers)
+        for (int i = 0; i < kItems; ++i) mbar_init(&ctl->item_full[i], 1), mbar_init(&ctl->item_empty[i], rank == 0 ? 11 : 9);
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
         fence_barrier_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(&ctl->tmem_base, kTmemCols);
-        tmem_relinquish();
+        if (kPair) tmem_alloc_cg2(&ctl->tmem_base, kTmemCols), tmem_relinquish_cg2();
+        else tmem_alloc(&ctl->tmem_base, kTmemCols), tmem_relinquish();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     tc_fence_before_sync();
     __syncthreads();
+    if (kPair) cluster_sync();             // the peer's barriers are ready
     tc_fence_after_sync();
     const uint32_t tmem = ctl->tmem_base;
+    // a commit of the products, counted in both CTAs of a pair
+    auto commit = [](uint64_t* bar) {
+        if (kPair) mma_commit_cg2(bar, 0x3u);
+        else mma_commit(bar);
+    };
+    // An arrival on a barrier of CTA 0. Weights are in tensor memory, and their stores were waited for: nothing is left for a release at
+    // cluster scope to order, which takes about 1000 cycles.
+    auto arrive_first = [](uint64_t* bar, bool relaxed) {
+        if (!kPair) mbar_arrive(bar);
+        else if (relaxed) mbar_arrive_cluster_relaxed(mapa_shared(smem_addr(bar), 0));
+        else mbar_arrive_cluster(mapa_shared(smem_addr(bar), 0));
+    };
     uint32_t* abort = &ctl->abort;
     uint32_t* status = p.status;
 
     if (warp >= kWarpLoad) {
         if (warp == kWarpLoad) {
             if (lane == 0) {
-                // Eight units hold three groups in flight: the keys of block g lie where the values of block g - 2 and what came before lay,
-                // the values of block g where the keys of block g - 1 lay.
-                int unit = 0, g = 0;
-                uint32_t q_phase = 3;                        // one bit for each half
+                // One CTA: eight units of the ring hold three groups in flight: the keys of block g lie where the values of block g - 2 and what came before
+                // lay, the values of block g where the keys of block g - 1 lay. A pair's CTAs hold half of each block, three blocks of both.
+                int unit = 0, g = 0, e = 0;                  // e: g % kDepth
+                uint32_t q_phase = 3, phase = 0;             // q_phase: one bit for each half; phase: of entry e
                 auto step = [&] { unit = unit + 1 == kUnits ? 0 : unit + 1; };
                 Items items = {ctl};
                 for (const Item* next = items.next(status); next != nullptr; items.done(), next = items.next(status)) {
@@ -367,32 +407,51 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         if ((h == 0 ? it.count0 : it.count1) == 0) return true;
                         if (!wait_or_give_up(&ctl->q_free[h], (q_phase >> h) & 1, abort, status)) return false;
                         q_phase ^= 1u << h;
-                        mbar_arrive_expect_tx(&ctl->q_full[h], 3 * kBox);
-                        for (int c = 0; c < 3; ++c)
-                            tma_load_3d(sbase + kOffQ + (3 * h + c) * kBox, &a.q_map, 64 * c, it.head, it.q0 + 128 * h, &ctl->q_full[h]);
+                        if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full[h], (kPair ? 6 : 3) * kBox);
+                        for (int c = 0; c < 3; ++c) {
+                            const uint32_t to = sbase + kOffQ + (3 * h + c) * kBox;
+                            const int row = it.q0 + kHalf<kPair> * h + 128 * rank;
+                            if (kPair) tma_load_3d_cg2(to, &a.q_map, 64 * c, it.head, row, mapa_shared(smem_addr(&ctl->q_full[h]), 0));
+                            else tma_load_3d(to, &a.q_map, 64 * c, it.head, row, &ctl->q_full[h]);
+                        }
                         return true;
                     };
                     auto load_k = [&](int i) -> bool {
-                        if (g >= 2 && !wait_or_give_up(&ctl->v_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) return false;
-                        const int row = it.k0 + 128 * (it.from + i);
-                        uint64_t* bar = &ctl->k_full[g & 1];
-                        mbar_arrive_expect_tx(bar, 3 * kBox);
-                        for (int c = 0; c < 3; ++c, step()) {
-                            if (c < 2) tma_load_3d(sbase + kOffRing + unit * kBox, &a.k_map, 64 * c, it.head, row, bar);
-                            else tma_load_3d(sbase + kOffRing + unit * kBox, &a.pe_map, 0, 0, row, bar);
+                        // (one CTA: entry e of v_empty had block g - 2, so its phase is the same as for a pair's k_empty)
+                        if (g >= kDepth<kPair> && !wait_or_give_up(kPair ? &ctl->k_empty[e] : &ctl->v_empty[e], phase ^ 1, abort, status)) return false;
+                        const int row = it.k0 + 128 * (it.from + i) + 64 * rank;
+                        uint64_t* bar = &ctl->k_full[e];
+                        if (rank == 0) mbar_arrive_expect_tx(bar, 3 * kBox);
+                        for (int c = 0; c < 3; ++c) {
+                            const void* map = c < 2 ? &a.k_map : &a.pe_map;
+                            const int x = c < 2 ? 64 * c : 0, y = c < 2 ? it.head : 0;
+                            if (kPair) {
+                                tma_load_3d_cg2(sbase + kOffRing + e * kPairK + c * (kBox / 2), map, x, y, row, mapa_shared(smem_addr(bar), 0));
+                            } else {
+                                tma_load_3d(sbase + kOffRing + unit * kBox, map, x, y, row, bar);
+                                step();
+                            }
                         }
                         return true;
                     };
                     auto load_v = [&](int i) -> bool {
-                        if (g >= 1 && !wait_or_give_up(&ctl->k_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, status)) return false;
                         const int row = it.k0 + 128 * (it.from + i);
-                        uint64_t* bar = &ctl->v_full[g & 1];
-                        mbar_arrive_expect_tx(bar, 2 * kBox);
-                        for (int c = 0; c < 2; ++c, step()) {
-                            tma_load_3d(sbase + kOffRing + unit * kBox, &a.v_map, 128, it.head, row + 64 * c, bar);
-                            tma_load_3d(sbase + kOffRing + unit * kBox + kBox / 2, &a.v_map, 192, it.head, row + 64 * c, bar);
+                        uint64_t* bar = &ctl->v_full[e];
+                        if (kPair) {
+                            if (g >= kDepth<kPair> && !wait_or_give_up(&ctl->v_empty[e], phase ^ 1, abort, status)) return false;
+                            mbar_arrive_expect_tx(bar, kBox);
+                            tma_load_3d(sbase + kOffPairV + e * kBox, &a.v_map, 128 + 64 * rank, it.head, row, bar);
+                        } else {
+                            // the keys of block g - 1: the other entry, in this phase for e = 1, in the one before for e = 0
+                            if (g >= 1 && !wait_or_give_up(&ctl->k_empty[e ^ 1], e == 1 ? phase : phase ^ 1, abort, status)) return false;
+                            mbar_arrive_expect_tx(bar, 2 * kBox);
+                            for (int c = 0; c < 2; ++c, step()) {
+                                tma_load_3d(sbase + kOffRing + unit * kBox, &a.v_map, 128, it.head, row + 64 * c, bar);
+                                tma_load_3d(sbase + kOffRing + unit * kBox + kBox / 2, &a.v_map, 192, it.head, row + 64 * c, bar);
+                            }
                         }
                         ++g;
+                        if (++e == kDepth<kPair>) e = 0, phase ^= 1;
                         return true;
                     };
                     bool ok = load_q(0) && load_k(0) && load_q(1) && load_v(0);
@@ -404,97 +463,109 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         } else if (warp >= kWarpMma) {
             // Each half has an issuer of its own: a product's issue blocks until the tensor cores take it, and what lies between two chains (waits,
             // commits, instruction fetches: 150 to 300 cycles each) would leave them idle; now the other half's chain runs meanwhile.
-            if (elect_one_in_warp()) {
+            if (rank == 0 && elect_one_in_warp()) {
                 const int h = warp - kWarpMma;
                 // (a negative scale negates the queries in the product: bit 13)
-                const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false) | (p.sm_scale < 0.0f ? 1u << 13 : 0u);
-                constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
-                const uint64_t q0 = sdesc_sw128(sbase + kOffQ + 3 * h * kBox, 16, 1024);   // K-major: rows x dims
-                const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);               // K-major: keys x dims
-                const uint64_t v0 = sdesc_sw128(sbase + kOffRing, kBox / 2, 1024);         // MN-major: dims x keys
+                const uint32_t idesc_s = idesc_bf16_f32(kHalf<kPair>, 128, false, false) | (p.sm_scale < 0.0f ? 1u << 13 : 0u);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(kHalf<kPair>, 128, false, true);
+                const uint64_t q0 = sdesc_sw128(sbase + kOffQ + 3 * h * kBox, 16, 1024);                     // K-major: rows x dims
+                const uint64_t k0 = sdesc_sw128(sbase + kOffRing, 16, 1024);                                 // K-major: keys x dims
+                const uint64_t v0 = sdesc_sw128(sbase + (kPair ? kOffPairV : kOffRing), kBox / 2, 1024);     // MN-major: dims x keys
                 const uint32_t s_addr = tmem + kColS + 128 * h, o_addr = tmem + kColO + 128 * h;
-                int unit = 0, g = 0, cleans = 0;                                           // g: blocks whose values were waited for
-                uint32_t q_phase = 0, p_phase = 0, turn_phase = h == 0 ? 1u : 0u;
-                auto scores = [&](int at) {                 // S from the three units at `at`
+                int unit = 0, e = 0;                        // of the block at hand: first unit (one CTA), entry
+                uint32_t phase = 0, q_phase = 0, p_phase = 0, turn_phase = h == 0 ? 1u : 0u;
+                auto next_e = [](int x) { return x + 1 == kDepth<kPair> ? 0 : x + 1; };
+                auto scores = [&](int at, int entry) {      // S from the keys of that block
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 3; ++c) {
-                        const uint64_t qd = q0 + static_cast<uint32_t>(c * (kBox >> 4)), kd = k0 + static_cast<uint32_t>(((at + c) & (kUnits - 1)) * (kBox >> 4));
+                        const uint64_t qd = q0 + static_cast<uint32_t>(c * (kBox >> 4));
+                        const uint64_t kd = k0 + static_cast<uint32_t>(kPair ? entry * (kPairK >> 4) + c * (kBox >> 5) : ((at + c) & (kUnits - 1)) * (kBox >> 4));
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) mma_ss(s_addr, qd + 2 * ks, kd + 2 * ks, idesc_s, c > 0 || ks > 0 ? 1u : 0u);
+                        for (int ks = 0; ks < 4; ++ks) {
+                            if (kPair) mma_ss_cg2(s_addr, qd + 2 * ks, kd + 2 * ks, idesc_s, c > 0 || ks > 0 ? 1u : 0u);
+                            else mma_ss(s_addr, qd + 2 * ks, kd + 2 * ks, idesc_s, c > 0 || ks > 0 ? 1u : 0u);
+                        }
                     }
-                    mma_commit(&ctl->s_full[h]);
+                    commit(&ctl->s_full[h]);
+                };
+                // The halves take turns: chains that run at the same time would both be late, and their softmax would run at the same time too.
+                auto my_turn = [&]() -> bool {
+                    const bool mine = wait_or_give_up(&ctl->turn[h], turn_phase, abort, status);
+                    turn_phase ^= 1u;
+                    return mine;
                 };
                 Items items = {ctl};
                 bool ok = true;
                 for (const Item* next = items.next(status); next != nullptr; items.done(), next = items.next(status)) {
                     const int n = max(next->count0, next->count1), count = h == 0 ? next->count0 : next->count1;
-                    const int whole = (next->keys >> 7) - next->from;      // blocks before the one that the sequence ends in
                     if (n == 0) continue;
                     if (count > 0) {                        // the first block's scores
-                        ok = wait_or_give_up(&ctl->k_full[g & 1], (g >> 1) & 1, abort, status) && wait_or_give_up(&ctl->q_full[h], q_phase, abort, status);
+                        ok = wait_or_give_up<kPair>(&ctl->k_full[e], phase, abort, status) && wait_or_give_up<kPair>(&ctl->q_full[h], q_phase, abort, status);
                         if (!ok) break;
                         q_phase ^= 1u;
                     }
-                    ok = wait_or_give_up(&ctl->turn[h], turn_phase, abort, status);
+                    ok = my_turn();
                     if (!ok) break;
-                    turn_phase ^= 1u;
                     if (count > 0) {
-                        scores(unit);
-                        if (count == 1) mma_commit(&ctl->q_free[h]);
+                        scores(unit, e);
+                        if (count == 1) commit(&ctl->q_free[h]);
                     }
                     mbar_arrive(&ctl->turn[h ^ 1]);
-                    mma_commit(&ctl->k_empty[g & 1]);
+                    commit(&ctl->k_empty[e]);
 #pragma unroll 1
-                    for (int i = 0; i < n; ++i, ++g) {
-                        ok = wait_or_give_up(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status);
-                        if (ok && i >= whole) {
-                            ok = wait_or_give_up(&ctl->v_clean[cleans & 1], (cleans >> 1) & 1, abort, status);
-                            ++cleans;
-                        }
+                    for (int i = 0; i < n; ++i) {
+                        const int e1 = next_e(e);           // the next block's entry and its phase
+                        const uint32_t phase1 = e1 == 0 ? phase ^ 1u : phase;
+                        ok = wait_or_give_up<kPair>(&ctl->v_ready[e], phase, abort, status);
                         if (!ok) break;
                         bool keys_here = false;
-                        if (i < count) {                    // O (+)= P V
+                        if (i < count) {
                             // (the next keys are mostly there already: seen to while P is not)
-                            keys_here = i + 1 < count && mbar_test_wait(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
-                            ok = wait_or_give_up(&ctl->p_full[h], p_phase, abort, status);
+                            keys_here = !kPair && i + 1 < count && mbar_test_wait(&ctl->k_full[e1], phase1);
+                            ok = wait_or_give_up<kPair>(&ctl->p_full[h], p_phase, abort, status);
                             if (!ok) break;
                             p_phase ^= 1u;
                         }
-                        ok = wait_or_give_up(&ctl->turn[h], turn_phase, abort, status);
+                        ok = my_turn();
                         if (!ok) break;
-                        turn_phase ^= 1u;
-                        if (i < count) {
+                        if (i < count) {                    // O (+)= P V
                             tc_fence_after_sync();
 #pragma unroll 1
                             for (int c = 0; c < 2; ++c) {
-                                const uint64_t vd = v0 + static_cast<uint32_t>(((unit + 3 + c) & (kUnits - 1)) * (kBox >> 4));
+                                const uint64_t vd = v0 + static_cast<uint32_t>(kPair ? e * (kBox >> 4) + 512 * c : ((unit + 3 + c) & (kUnits - 1)) * (kBox >> 4));
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks)
-                                    mma_ts(o_addr, s_addr + 32 * c + 8 * ks, vd + 128 * ks, idesc_o, i == 0 && c == 0 && ks == 0 ? 0u : 1u);
+                                for (int ks = 0; ks < 4; ++ks) {
+                                    const uint32_t add = i == 0 && c == 0 && ks == 0 ? 0u : 1u;
+                                    if (kPair) mma_ts_cg2(o_addr, s_addr + 32 * c + 8 * ks, vd + 128 * ks, idesc_o, add);
+                                    else mma_ts(o_addr, s_addr + 32 * c + 8 * ks, vd + 128 * ks, idesc_o, add);
+                                }
                             }
-                            if (i + 1 == count) mma_commit(&ctl->o_done[h]);
+                            if (i + 1 == count) commit(&ctl->o_done[h]);
                         }
-                        mma_commit(&ctl->v_empty[g & 1]);
+                        commit(&ctl->v_empty[e]);
                         unit = (unit + 5) & (kUnits - 1);
                         if (i + 1 < count) {
-                            ok = keys_here || wait_or_give_up(&ctl->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, status);
+                            ok = keys_here || wait_or_give_up<kPair>(&ctl->k_full[e1], phase1, abort, status);
                             if (!ok) break;
-                            scores(unit);
-                            if (i + 2 == count) mma_commit(&ctl->q_free[h]);
+                            scores(unit, e1);
+                            if (i + 2 == count) commit(&ctl->q_free[h]);
                         }
                         mbar_arrive(&ctl->turn[h ^ 1]);
-                        if (i + 1 < n) mma_commit(&ctl->k_empty[(g + 1) & 1]);
+                        if (i + 1 < n) commit(&ctl->k_empty[e1]);
+                        e = e1;
+                        phase = phase1;
                     }
                     if (!ok) break;
                 }
-                mma_commit(&ctl->drain);
+                if (kPair) mma_commit_cg2(&ctl->drain, 0x1u);
+                else mma_commit(&ctl->drain);
                 wait_or_give_up(&ctl->drain, 0, abort, status);
             }
             __syncwarp();
         } else if (warp == kWarpFix) {
-            // The CTA's items, one ahead of the one that is worked on.
-            Walk walk = find_run(a, lane);
+            // The run's items, one ahead of the one that is worked on (in both CTAs of a pair alike).
+            Walk<kPair> walk = find_run<kPair>(a, run, runs, lane);
             int slot = 0;
             uint32_t slot_phase = 1;
             auto publish = [&](const Item& it) -> bool {
@@ -507,35 +578,38 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 return true;
             };
             // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN.
-            // (The warp takes note of every block and hands it back beside the products, so that it stays within the ring.)
-            int unit = 0, g = 0, cleans = 0;
-            Item it = walk.next(p);
+            int unit = 0, e = 0;
+            uint32_t phase = 0;
+            Item it = walk.next(p, run);
             bool ok = publish(it);
             while (ok && it.valid) {
-                const Item ahead = walk.next(p);
+                const Item ahead = walk.next(p, run);
                 ok = publish(ahead);
                 const int n = max(it.count0, it.count1);
 #pragma unroll 1
-                for (int i = 0; i < n && ok; ++i, ++g) {
+                for (int i = 0; i < n && ok; ++i) {
                     const int left = it.keys - 128 * (it.from + i);
                     unit = (unit + 3) & (kUnits - 1);
-                    ok = wait_warp(&ctl->v_full[g & 1], (g >> 1) & 1, abort, status);
+                    ok = wait_warp(&ctl->v_full[e], phase, abort, status);
                     if (!ok) break;
                     if (left < 128) {
-                        for (int c = 0; c < 2; ++c) {
-                            const uint32_t base = sbase + kOffRing + ((unit + c) & (kUnits - 1)) * kBox;
-                            for (int x = max(left - 64 * c, 0) * 8 + lane; x < 64 * 8; x += 32) {
-                                sts_u128(base + 16 * x, make_uint4(0u, 0u, 0u, 0u));
-                                sts_u128(base + kBox / 2 + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                        if (kPair) {
+                            for (int x = max(left, 0) * 8 + lane; x < 128 * 8; x += 32) sts_u128(sbase + kOffPairV + e * kBox + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                        } else {
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t base = sbase + kOffRing + ((unit + c) & (kUnits - 1)) * kBox;
+                                for (int x = max(left - 64 * c, 0) * 8 + lane; x < 64 * 8; x += 32) {
+                                    sts_u128(base + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                                    sts_u128(base + kBox / 2 + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                                }
                             }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->v_clean[cleans & 1]);
-                        ++cleans;
                     }
                     unit = (unit + 2) & (kUnits - 1);
-                    if (lane == 0) mbar_arrive(&ctl->v_empty[g & 1]);
+                    if (lane == 0) arrive_first(&ctl->v_ready[e], false);
+                    if (++e == kDepth<kPair>) e = 0, phase ^= 1;
                 }
                 it = ahead;
             }
@@ -554,8 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             if (it == nullptr) break;
             const int n = h == 0 ? it->count0 : it->count1;
             // keys that the row, and the half's first row, see of those from the first block on
-            const int limit = min(it->seen + 128 * h + 32 * w + lane, it->keys) - 128 * it->from;
-            const int first_limit = it->seen + 128 * h - 128 * it->from;
+            const int first = kHalf<kPair> * h + 128 * rank;          // row of the tile that this CTA's half begins with
+            const int limit = min(it->seen + first + 32 * w + lane, it->keys) - 128 * it->from;
+            const int first_limit = it->seen + first - 128 * it->from;
             float m = -INFINITY, l = 0.0f, top = -INFINITY;   // top: what the reference moves up to, if anything
             for (int i = 0; i < n; ++i, ++seen) {
                 ok = wait_warp(&ctl->s_full[h], seen & 1, abort, status);
@@ -613,14 +688,14 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->p_full[h]);
+                if (lane == 0) arrive_first(&ctl->p_full[h], true);
             }
             if (n > 0) {
                 ok = ok && wait_warp(&ctl->o_done[h], done++ & 1, abort, status);
                 if (!ok) break;
                 tc_fence_after_sync();
             }
-            const int rows = it->rows - 128 * h - 32 * w;      // of this warp (32 and more: all)
+            const int rows = it->rows - first - 32 * w;      // of this warp (32 and more: all)
             const int head = it->head, slot = it->slot;
             const bool empty = l == 0.0f;
             const float lse2 = empty ? -INFINITY : m + log2f(l);
@@ -628,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             if (slot < 0 && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + head) * kLog2e - m));
             const bool none = n == 0 || empty;
             if (slot >= 0 && rows > 0) {
-                a.part_lse[static_cast<int64_t>(slot) * 256 + 128 * h + 32 * w + lane] = lse2;
-                float* dst = a.part_out + (static_cast<int64_t>(slot) * 8 + 4 * h + w) * 4096 + 8 * lane;
+                a.part_lse[static_cast<int64_t>(slot) * kTile<kPair> + first + 32 * w + lane] = lse2;
+                float* dst = a.part_out + (static_cast<int64_t>(slot) * (kTile<kPair> / 32) + first / 32 + w) * 4096 + 8 * lane;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
@@ -640,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     for (int e = 0; e < 4; ++e) st_sector(dst + (4 * c + e) * 256, o + 8 * e);
                 }
             } else if (rows > 0) {
-                const int64_t at = static_cast<int64_t>(it->q0 + 128 * h + 32 * w) * p.heads + head;   // of lane 0's row
+                const int64_t at = static_cast<int64_t>(it->q0 + first + 32 * w) * p.heads + head;   // of lane 0's row
                 if (lane < rows) p.lse[at + static_cast<int64_t>(lane) * p.heads] = lse2 * kLn2;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -665,15 +740,18 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
     tc_fence_before_sync();
     __syncthreads();
     if (*reinterpret_cast<volatile uint32_t*>(abort) != 0u) let_copies_land();
+    if (kPair) cluster_sync();             // no CTA leaves while the other's products may read its shared or tensor memory
     if (warp == kWarpMma) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, kTmemCols);
+        if (kPair) tmem_dealloc_cg2(tmem, kTmemCols);
+        else tmem_dealloc(tmem, kTmemCols);
     }
 }
 
 // Joins the parts of a tile that was cut: with part s's lse L_s (log2) and output O_s, w_s = 2^(L_s - max L),
 // out = sum_s w_s O_s / (sum_s w_s + 2^(sink - max L)). The first part of header c lies in slot 2c + 1, the others in slots
 // 2 (c + 1), 2 (c + 2), ... A lane per row and 16 dims, in the parts' order.
+template <bool kPair>
 __global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restrict__ part_out, const float* __restrict__ part_lse,
                                                           const int4* __restrict__ headers, const float* __restrict__ sink, int heads,
                                                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
@@ -683,7 +761,7 @@ __global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restric
     const int4 hd = __ldcg(headers + c);
     if (hd.w == 0 || r >= hd.y) return;
     auto slot = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)); };
-    auto lse_of = [&](int s) { return __ldcg(part_lse + slot(s) * 256 + r); };
+    auto lse_of = [&](int s) { return __ldcg(part_lse + slot(s) * kTile<kPair> + r); };
     float m = -INFINITY;
     for (int s = 0; s < hd.w; ++s) m = fmaxf(m, lse_of(s));
     if (m == -INFINITY) m = 0.0f;
@@ -691,7 +769,7 @@ __global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restric
 #pragma unroll 2
     for (int s = 0; s < hd.w; ++s) {
         const float w = exp2f(lse_of(s) - m);
-        const float4* x = reinterpret_cast<const float4*>(part_out + (slot(s) * 8 + blockIdx.y) * 4096 + 512 * dims + 8 * lane);
+        const float4* x = reinterpret_cast<const float4*>(part_out + (slot(s) * (kTile<kPair> / 32) + blockIdx.y) * 4096 + 512 * dims + 8 * lane);
         const float4 v[4] = {__ldcg(x), __ldcg(x + 1), __ldcg(x + 64), __ldcg(x + 65)};
         sum += w;
 #pragma unroll
@@ -719,26 +797,47 @@ constexpr size_t kLseBytes = static_cast<size_t>(2 * kMaxCtas) * 256 * sizeof(fl
 
 size_t ragged_workspace_bytes() { return kPartsBytes + kLseBytes + kMaxCtas * sizeof(int4); }
 
+namespace {
+
+template <bool kPair>
+cudaError_t launch_runs(KernelArgs& a, int sms, cudaStream_t stream) {
+    const RaggedArgs& p = a.p;
+    const int64_t rows_k = p.rows_k > 0 ? p.rows_k : 1;      // (no row is read where there is none)
+    constexpr int kKeyBox = kPair ? 64 : 128;
+    if (!encode_map(&a.q_map, p.q, 192, p.heads, p.rows_q, p.q_head_stride, p.q_token_stride, 1, 128) ||
+        !encode_map(&a.k_map, p.kv, 256, p.heads, rows_k, p.kv_head_stride, p.kv_token_stride, 1, kKeyBox) ||
+        !encode_map(&a.v_map, p.kv, 256, p.heads, rows_k, p.kv_head_stride, p.kv_token_stride, 1, 192 - kKeyBox) ||
+        !encode_map(&a.pe_map, p.k_pe, 64, 1, rows_k, 64, p.pe_stride, 1, kKeyBox))
+        return cudaErrorInvalidValue;
+    cudaError_t err = allow_smem<ragged_attention_kernel<kPair>>(kSmem);
+    if (err != cudaSuccess) return err;
+    const int runs = (sms < kMaxCtas ? sms : kMaxCtas) / (kPair ? 2 : 1);
+    err = launch_dependent(ragged_attention_kernel<kPair>, dim3(kPair ? 2 * runs : runs), kThreads, kSmem, kPair ? 2 : 1, stream, a);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(ragged_join_kernel<kPair>, dim3(runs, kTile<kPair> / 32), 256, 0, 1, stream, static_cast<const float*>(a.part_out),
+                            static_cast<const float*>(a.part_lse), static_cast<const int4*>(a.headers), p.attn_sink, p.heads,
+                            static_cast<__nv_bfloat16*>(p.out), p.lse);
+}
+
+// A block of keys takes a tile of 256 rows on one CTA about as long as (7 to 6) a tile of 512 rows on two; a tile costs what one and three
+// blocks cost besides. So pairs are for long sequences whose rows fill their tiles, by the average rows and keys of a sequence (one CTA / pairs, us):
+// 4 chunks of 512 rows over 4512 keys, 64 heads 276 / 246, of 384 rows 259 / 236, of 256 rows 148 / 210; one of 700 rows over 16700 keys
+// 355 / 390; 16 prompts of 512, 16 heads 51 / 55; 2 prompts of 4096, 64 heads 509 / 498; 2048 rows over 16640 keys, 64 heads 868 / 760.
+bool pairs_are_faster(const RaggedArgs& p) {
+    const int64_t rows = (p.rows_q + p.batch - 1) / p.batch, keys = p.rows_k / p.batch;
+    const int64_t blocks = keys > rows / 2 ? (keys - rows / 2) / 128 : 0;
+    return 12 * ((rows + 511) / 512) * (blocks + 3) < 7 * ((rows + 255) / 256) * (blocks + 1);
+}
+
+}  // namespace
+
 cudaError_t launch_ragged_attention(const RaggedArgs& p, void* workspace, int sms, cudaStream_t stream) {
     KernelArgs a;
     a.p = p;
     a.part_out = static_cast<float*>(workspace);
     a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPartsBytes);
     a.headers = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + kPartsBytes + kLseBytes);
-    const int64_t rows_k = p.rows_k > 0 ? p.rows_k : 1;      // (no row is read where there is none)
-    if (!encode_map(&a.q_map, p.q, 192, p.heads, p.rows_q, p.q_head_stride, p.q_token_stride, 1, 128) ||
-        !encode_map(&a.k_map, p.kv, 256, p.heads, rows_k, p.kv_head_stride, p.kv_token_stride, 1, 128) ||
-        !encode_map(&a.v_map, p.kv, 256, p.heads, rows_k, p.kv_head_stride, p.kv_token_stride, 1, 64) ||
-        !encode_map(&a.pe_map, p.k_pe, 64, 1, rows_k, 64, p.pe_stride, 1, 128))
-        return cudaErrorInvalidValue;
-    cudaError_t err = allow_smem<ragged_attention_kernel>(kSmem);
-    if (err != cudaSuccess) return err;
-    const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-    err = launch_dependent(ragged_attention_kernel, dim3(ctas), kThreads, kSmem, 1, stream, a);
-    if (err != cudaSuccess) return err;
-    return launch_dependent(ragged_join_kernel, dim3(ctas, 8), 256, 0, 1, stream, static_cast<const float*>(a.part_out),
-                            static_cast<const float*>(a.part_lse), static_cast<const int4*>(a.headers), p.attn_sink, p.heads,
-                            static_cast<__nv_bfloat16*>(p.out), p.lse);
+    return pairs_are_faster(p) ? launch_runs<true>(a, sms, stream) : launch_runs<false>(a, sms, stream);
 }
 
 }  // namespace nvfp4mla

@@ -177,6 +177,27 @@ def test_tiles_that_several_ctas_share(h, lq, lk):
     attend(rng, [lq, 1], [lk, 40], h, sink=2 * rng.standard_normal(h).astype(np.float32))
 
 
+# (long sequences whose rows fill tiles of 512 go to CTA pairs)
+@pytest.mark.parametrize("h,q_lens,k_lens", [(1, [512], [4000]), (3, [512, 384], [3500, 4001]), (2, [1000, 40, 500], [5000, 3000, 4000]), (5, [2048], [2500]),
+                                             (4, [511, 0, 513, 640], [3000, 7000, 2900, 640]), (2, [400, 400], [9000, 130])])
+def test_long_sequences(h, q_lens, k_lens):
+    rng = np.random.default_rng(sum(k_lens))
+    attend(rng, q_lens, k_lens, h, sink=rng.standard_normal(h).astype(np.float32), pad=0)
+
+
+def test_scores_that_jump_far_above_the_reference():
+    # within a block, and between blocks, by more than the 2^64 that the reference may lag behind
+    rng = np.random.default_rng(12)
+    for lq, lk in ((130, 700), (512, 3000)):
+        kv = bf16(rng, lk, 2, 256)
+        jump = torch.zeros(lk)
+        jump[20], jump[100:110], jump[300], jump[lk // 2:] = 90.0, 200.0, 420.0, 600.0
+        kv[:, :, 0] = jump[:, None].to(torch.bfloat16)
+        q = (0.05 * bf16(rng, lq, 2, 192).float()).to(torch.bfloat16)
+        q[..., 0] = torch.tensor([1.0, -1.0], dtype=torch.bfloat16)
+        attend(rng, [lq], [lk], 2, scale=1.0, q=q, kv=kv)
+
+
 def test_rising_and_falling_scores_move_the_reference():
     rng = np.random.default_rng(8)
     n, h = 1200, 4
