@@ -53,6 +53,7 @@ constexpr float kMoveLog2 = 8.0f;      // a reference moves, a block later, when
 constexpr float kFarLog2 = 64.0f;      // and at once when one passes it by 2^64
 constexpr int kExtra = 1;              // what a tile costs besides its blocks, in blocks
 constexpr int kMinRun = 2;
+constexpr int kWhole = 6;              // tiles of up to so many units are not cut
 constexpr int kItems = 4;              // items that are known ahead
 constexpr int kMaxCtas = kPagedMaxSms;
 
@@ -184,96 +185,107 @@ struct Items {
     }
 };
 
-// One warp: where run c of `runs` begins. Also its header, where the run's last tile goes on in the next run.
+// One warp: where run c of `runs` begins and ends. Also its header, where the run's last tile goes on in the next run. Runs are equal in units, but
+// where a border falls into a tile of at most kWhole units it goes to the nearer end of that tile: writing and joining parts costs more.
 template <bool kPair>
 __device__ __forceinline__ Walk<kPair> find_run(const KernelArgs& a, int c, int runs, int lane) {
     const RaggedArgs& p = a.p;
     const unsigned full = 0xffffffffu;
-    int64_t total = 0, mine = 0;
+    Seq mine = {};
+    int64_t total = 0, n = 0;
     for (int b = 0; b < p.batch; b += 32) {
-        int64_t n = 0;
+        n = 0;
         if (b + lane < p.batch) {
-            const Seq s = seq_at(p, b + lane);
-            n = units_of<kPair>(s, tiles_of<kPair>(s));
+            mine = seq_at(p, b + lane);
+            n = units_of<kPair>(mine, tiles_of<kPair>(mine));
         }
-        mine = n;
+        int64_t sum = n;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(full, n, o);
-        total += n;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
+        total += sum;
     }
     total *= p.heads;
     // (a run has at least kMinRun units: shorter ones would be all parts and joining)
     const int64_t most = (total + kMinRun - 1) / kMinRun, g = most < runs ? most : runs;
-    const int64_t u0 = c < g ? total * c / g : 0, u1 = c < g ? total * (c + 1) / g : 0;
-    // the sequences that the first and the last unit lie in
-    int seq0 = 0, seq1 = 0;
-    int64_t at0 = 0, at1 = 0;
-    if (u1 > u0) {
+    // Lanes 0 and 1 (the others like them) look for the two borders.
+    const int64_t border = c >= g ? total : total * (c + (lane & 1)) / g;
+    const int64_t u0 = __shfl_sync(full, border, 0), u1 = __shfl_sync(full, border, 1);
+    int seq = 0;                                            // of this lane's border
+    int64_t at = 0;                                         // units before it
+    {
         int64_t before = 0;
         bool found0 = false, found1 = false;
         for (int b = 0; b < p.batch && !(found0 && found1); b += 32) {
-            int64_t n = mine * p.heads;                     // (of the only 32 sequences, or else read again)
-            if (p.batch > 32) {
+            if (p.batch > 32) {                             // (else known already)
                 n = 0;
                 if (b + lane < p.batch) {
                     const Seq s = seq_at(p, b + lane);
-                    n = units_of<kPair>(s, tiles_of<kPair>(s)) * p.heads;
+                    n = units_of<kPair>(s, tiles_of<kPair>(s));
                 }
             }
-            int64_t sum = n;
+            int64_t sum = n * p.heads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(full, sum, o);
                 if (lane >= o) sum += v;
             }
-            const unsigned m0 = __ballot_sync(full, before + sum > u0), m1 = __ballot_sync(full, before + sum > u1 - 1);
-            if (!found0 && m0 != 0u) {
-                const int lane0 = __ffs(m0) - 1;
-                seq0 = b + lane0;
-                at0 = before + __shfl_sync(full, sum - n, lane0);
-                found0 = true;
-            }
-            if (!found1 && m1 != 0u) {
-                const int lane1 = __ffs(m1) - 1;
-                seq1 = b + lane1;
-                at1 = before + __shfl_sync(full, sum - n, lane1);
-                found1 = true;
-            }
+            const unsigned m0 = __ballot_sync(full, before + sum > u0), m1 = __ballot_sync(full, before + sum > u1);
+            const bool here0 = !found0 && m0 != 0u, here1 = !found1 && m1 != 0u;
+            const unsigned m = (lane & 1) == 0 ? m0 : m1;
+            const int64_t first = before + __shfl_sync(full, sum - n * p.heads, (__ffs(m) - 1) & 31);
+            if ((lane & 1) == 0 ? here0 : here1) seq = b + __ffs(m) - 1, at = first;
+            found0 |= here0, found1 |= here1;
             before += __shfl_sync(full, sum, 31);
         }
     }
-    Walk<kPair> first = {};
-    int4 header = make_int4(0, 0, 0, 0);
-    if (u1 > u0) {
-#pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            const int seq = e == 0 ? seq0 : seq1;
-            const Seq s = seq_at(p, seq);
-            const int64_t off = e == 0 ? u0 - at0 : u1 - 1 - at1;
-            int lo = 0, hi = tiles_of<kPair>(s);                   // units_of(lo) * heads <= off < units_of(hi) * heads
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (units_of<kPair>(s, mid) * p.heads <= off) lo = mid;
-                else hi = mid;
-            }
-            const int64_t in_tile = off - units_of<kPair>(s, lo) * p.heads;
-            const int weight = blocks_of(s, kTile<kPair> * (lo + 1)) + kExtra;
-            const int head = static_cast<int>(in_tile / weight), b = static_cast<int>(in_tile - static_cast<int64_t>(head) * weight);
-            if (e == 0) {
-                first.left = u1 - u0;
-                first.seq = seq, first.tile = lo, first.head = head, first.b0 = b;
-                first.s = s;
-            } else {
-                const int64_t begin = u1 - 1 - b, end = begin + weight;
-                if (begin >= u0 && end > u1) {
-                    int parts = 1;
-                    for (int64_t n = c + 1; n < g && total * n / g < end; ++n) ++parts;
-                    header = make_int4(s.q0 + kTile<kPair> * lo, min(kTile<kPair>, s.lq - kTile<kPair> * lo), head, parts);
-                }
-            }
+    Seq s;
+    if (p.batch > 32) {
+        s = seq_at(p, seq);
+    } else {
+        s.q0 = __shfl_sync(full, mine.q0, seq), s.lq = __shfl_sync(full, mine.lq, seq);
+        s.k0 = __shfl_sync(full, mine.k0, seq), s.lk = __shfl_sync(full, mine.lk, seq);
+    }
+    int tile = 0, head = 0, b = 0, weight = 0;
+    int64_t snapped = total;
+    if (border < total) {
+        const int64_t off = border - at;
+        int lo = 0, hi = tiles_of<kPair>(s);                // units_of(lo) * heads <= off < units_of(hi) * heads
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (units_of<kPair>(s, mid) * p.heads <= off) lo = mid;
+            else hi = mid;
+        }
+        tile = lo;
+        const int64_t in_tile = off - units_of<kPair>(s, lo) * p.heads;
+        weight = blocks_of(s, kTile<kPair> * (lo + 1)) + kExtra;
+        if (in_tile <= 0x7FFFFFFF) head = static_cast<int>(in_tile) / weight;
+        else head = static_cast<int>(in_tile / weight);
+        b = static_cast<int>(in_tile - static_cast<int64_t>(head) * weight);
+        snapped = border;
+        if (weight <= kWhole && b > 0) {
+            if (2 * b >= weight) snapped += weight - b, ++head;
+            else snapped -= b;
+            b = 0;
         }
     }
-    if (lane == 0 && (!kPair || cluster_ctarank() == 0)) a.headers[c] = header;
+    const int64_t s0 = __shfl_sync(full, snapped, 0), s1 = __shfl_sync(full, snapped, 1);
+    Walk<kPair> first = {};
+    first.left = s1 - s0;
+    first.seq = __shfl_sync(full, seq, 0), first.tile = __shfl_sync(full, tile, 0);
+    first.head = __shfl_sync(full, head, 0), first.b0 = __shfl_sync(full, b, 0);
+    first.s.q0 = __shfl_sync(full, s.q0, 0), first.s.lq = __shfl_sync(full, s.lq, 0);
+    first.s.k0 = __shfl_sync(full, s.k0, 0), first.s.lk = __shfl_sync(full, s.lk, 0);
+    if (first.head == p.heads) first.head = 0, ++first.tile;
+    if (lane == 1 && (!kPair || cluster_ctarank() == 0)) {
+        int4 header = make_int4(0, 0, 0, 0);
+        const int64_t begin = s1 - b, end = begin + weight;
+        if (b > 0 && begin >= s0) {                         // the run's last tile begins here and ends elsewhere
+            int parts = 1;
+            for (int64_t r = c + 1; r < g && total * r / g < end; ++r) ++parts;
+            header = make_int4(s.q0 + kTile<kPair> * tile, min(kTile<kPair>, s.lq - kTile<kPair> * tile), head, parts);
+        }
+        a.headers[c] = header;
+    }
     return first;
 }
 
@@ -702,11 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             float f = empty ? 0.0f : 1.0f / l;
             if (slot < 0 && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + head) * kLog2e - m));
             const bool none = n == 0 || empty;
-            if (slot >= 0 && rows > 0) {
+            if (slot >= 0 && rows > 0) {                   // (where a part has no keys the join does not look at its outputs)
                 a.part_lse[static_cast<int64_t>(slot) * kTile<kPair> + first + 32 * w + lane] = lse2;
                 float* dst = a.part_out + (static_cast<int64_t>(slot) * (kTile<kPair> / 32) + first / 32 + w) * 4096 + 8 * lane;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = n > 0 ? 0 : 4; c < 4; ++c) {
                     uint32_t o[32];
                     tmem_ld32_wait(o_addr + 32 * c, o);
 #pragma unroll
@@ -768,7 +780,8 @@ __global__ void __launch_bounds__(256) ragged_join_kernel(const float* __restric
     float sum = 0.0f, acc[16] = {};
 #pragma unroll 2
     for (int s = 0; s < hd.w; ++s) {
-        const float w = exp2f(lse_of(s) - m);
+        const float part = lse_of(s), w = exp2f(part - m);
+        if (part == -INFINITY) continue;
         const float4* x = reinterpret_cast<const float4*>(part_out + (slot(s) * (kTile<kPair> / 32) + blockIdx.y) * 4096 + 512 * dims + 8 * lane);
         const float4 v[4] = {__ldcg(x), __ldcg(x + 1), __ldcg(x + 64), __ldcg(x + 65)};
         sum += w;
