@@ -404,7 +404,8 @@ NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_ca
  * NVFP4_MLA_ERR_UNSUPPORTED. Strides are in elements and multiples of 8, inner strides 1; inputs are 16-byte aligned, outputs
  * contiguous and 32-byte aligned. The stride of a dimension of one entry is not looked at. Row counts stay below 2^31 - 4096.
  * Sequences lie packed, one behind the other: sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32
- * [batch + 1], device, not decreasing; entries are read as clamped to [0, rows], a decrease as an empty sequence).
+ * [batch + 1], device, from 0 on and not decreasing; entries are read as clamped to [0, rows], and other values give
+ * unspecified rows but touch nothing outside the tensors).
  * Rows from cu_seqlens[batch] on are neither read nor written, so buffers may be larger than what a batch fills, and a
  * captured call follows the lengths of its replay. A pipeline wait that gives up sets NVFP4_MLA_DEV_TIMEOUT.
  */
@@ -456,10 +457,10 @@ NVFP4_MLA_API int nvfp4_ragged_mla_attention_workspace_size(size_t* bytes);
  *   out              [num_q, h_q, 128].
  *   workspace        at least ..._workspace_size bytes, 256-byte aligned; needs no initialization. Calls that may overlap on
  *                    the GPU need one each.
- * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^24.
+ * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^24, num_k below 2^26.
  * Precision: weights e^z are rounded to bf16 (2^-8 of themselves, however small), row sums are of the unrounded ones.
  * A NaN or infinity in a query or a key makes NaN the rows that see it, one in a value the rows of its sequence that see it and
- * those up to 255 rows before them; other sequences' rows never.
+ * may make NaN those up to 383 rows before them; other sequences' rows never.
  */
 NVFP4_MLA_API int nvfp4_ragged_mla_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_q,
                                              const void* kv, int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe,

@@ -240,3 +240,38 @@ def test_attention_of_strided_inputs():
         d.copy_(s)
     out, lse = lib.ragged_mla_attention(dq, dkv, dpe, starts(q_lens).to(DEV), starts(k_lens).to(DEV), SCALE)
     ref.check_attention(out, lse, ref.attention(q, kv, pe, q_lens, k_lens, SCALE))
+
+
+def test_offsets_beyond_32_bits():
+    # 128 heads: the queries' results and the keys pass 2^31 elements; a few rows at the end are looked at
+    rng = np.random.default_rng(13)
+    h, T, last = 128, 30000, 3
+    kv_b = weights(rng, h)
+    q = bf16(rng, last, h, 192)
+    dq = torch.zeros(T, h, 192, dtype=torch.bfloat16, device=DEV)
+    dq[-last:] = q.to(DEV)
+    out = lib.mla_absorb_query(dq, kv_b.to(DEV))
+    assert out.numel() > 2 ** 31
+    ref.check(out[-last:], *ref.absorb(q, kv_b))
+    assert torch.all(out[-200:-last] == 0)
+    del out, dq
+    lat = torch.zeros(36000, h, 512, dtype=torch.bfloat16, device=DEV)
+    assert lat.numel() > 2 ** 31
+    o = bf16(rng, last, h, 512)
+    lat[-last:] = o.to(DEV)
+    ref.check(lib.mla_project_values(lat, kv_b.to(DEV))[-last:], *ref.project(o, kv_b))
+    del lat
+    # the last of many sequences in pages, and attention over its keys
+    recs, table, lens, _ = pages.random_batch(rng, [130], 64)
+    n = 66000
+    starts_k = torch.tensor([0] + [n - 130] * 1 + [n], dtype=torch.int32, device=DEV)
+    wide = torch.full((2, -(-n // 64)), 0, dtype=torch.int32, device=DEV)
+    wide[1, :table.shape[1]] = torch.from_numpy(table[0]).to(DEV)
+    kv, pe = lib.paged_mla_expand(torch.from_numpy(recs).to(DEV), wide, starts_k, kv_b.to(DEV), n)
+    assert kv.numel() > 2 ** 31
+    r, tol, r_pe = ref.expand(recs, False, table, lens, 64, kv_b)
+    ref.check(kv[-130:], r, tol)
+    assert np.array_equal(ref.f64(pe[-130:]), r_pe)
+    q = bf16(rng, 5, h, 192)
+    out, lse = lib.ragged_mla_attention(q.to(DEV), kv, pe, torch.tensor([0, 0, 5], dtype=torch.int32, device=DEV), starts_k, SCALE)
+    ref.check_attention(out, lse, ref.attention(q, kv[-130:].cpu(), pe[-130:].cpu(), [5], [130], SCALE))
