@@ -12,7 +12,10 @@
 // is that every byte moves once. A job is a tile of 128 tokens of one head (and one piece of N, below). CTAs, one per SM, take
 // equal runs of jobs, all tiles of a head one behind the other, and keep the head's weights (128 KB) in
 // shared memory while the tokens' boxes of 64 dims stream through a ring; accumulators alternate between two
-// halves of the tensor memory, so that loads, products and stores of neighbouring tiles overlap.
+// halves of the tensor memory, so that loads, products and stores of neighbouring tiles overlap. Results leave through shared
+// memory as boxes (32-byte stores of 32 rows at once take 130 cycles a warp).
+// 4001 tokens x 128 heads: absorb 160 us, 5.0 TB/s (73% of a copy's rate; two thirds are writes, and writes alone reach 4.07 TB/s), project 114 us,
+// 5.9 TB/s (87%). One token x 16 heads: 3.5 and 3.9 us on the device.
 #include "head_tiles.cuh"
 #include "launch.h"
 
@@ -87,8 +90,8 @@ __device__ __forceinline__ void rope_positions(const HeadProductArgs& p, int64_t
     }
 }
 
-// The RoPE dims of a tile's tokens: all of a lane's loads are in flight at once (one latency a tile instead of two for the
-// tables behind the positions: 262 -> see the header's figures).
+// The RoPE dims of a tile's tokens: all of a lane's loads are in flight at once (in four rounds of loads a tile,
+// positions ahead of tables, these warps bound the kernel: 262 against 161 us at 4001 tokens x 128 heads, 154 without rotation).
 template <bool kHalf>
 __device__ __forceinline__ void rope_tile(const HeadProductArgs& p, int64_t t0, int head, int lane, const int64_t (&pos)[4]) {
     const int j = lane & 7;
@@ -143,7 +146,6 @@ __global__ void __launch_bounds__(kThreads<kAbsorb>, 1) head_product_kernel(cons
     constexpr int kWBox = kAbsorb ? kBox : kPiece * 128;     // bytes of a weight box: 128 k x 64 n, or kPiece n x 64 k
     constexpr int kWBoxes = kWBytes<kAbsorb, kPiece> / kWBox;
     constexpr int kOffRing = kOffW + kWBytes<kAbsorb, kPiece>;
-    constexpr int kOutRow = kAbsorb ? 576 : 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Ctl* ctl = reinterpret_cast<Ctl*>(smem);
@@ -263,25 +265,15 @@ __global__ void __launch_bounds__(kThreads<kAbsorb>, 1) head_product_kernel(cons
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (t0 < a.p.tokens) {   // (the same for the whole warp)
-                    if constexpr (kSub >= 64) {
 #pragma unroll 1
-                        for (int c = 0; c < kSub / 64; ++c, ++boxes) {
-                            const uint32_t box = stage + (boxes & 1) * kStage;
-                            if (lane == 0) tma_store_wait_read<1>();     // the box before the last one has left
-                            __syncwarp();
-                            stage_box(lanes + 256 * buf + 64 * c, box, lane);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) tma_store_3d(&a.out_map, n0 + kSub * sub + 64 * c, head, t0, box);
-                        }
-                    } else {
-                        uint32_t v[32];
-                        tmem_ld32_wait(lanes + 256 * buf, v);
-                        if (t0 + lane < a.p.tokens) {
-                            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.p.out) + (static_cast<int64_t>(t0 + lane) * a.p.heads + head) * kOutRow + n0;
-                            st_bf16x16(dst, v, 1.0f);
-                            st_bf16x16(dst + 16, v + 16, 1.0f);
-                        }
+                    for (int c = 0; c < kSub / 64; ++c, ++boxes) {
+                        const uint32_t box = stage + (boxes & 1) * kStage;
+                        if (lane == 0) tma_store_wait_read<1>();     // the box before the last one has left
+                        __syncwarp();
+                        stage_box(lanes + 256 * buf + 64 * c, box, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tma_store_3d(&a.out_map, n0 + kSub * sub + 64 * c, head, t0, box);
                     }
                 }
                 tc_fence_before_sync();
@@ -343,11 +335,13 @@ cudaError_t launch_piece(KernelArgs& a, int sms, cudaStream_t stream) {
 cudaError_t launch_head_product(const HeadProductArgs& p, bool absorb, int sms, cudaStream_t stream) {
     KernelArgs a;
     a.p = p;
-    // With few jobs the weights are cut into pieces of N, so that more SMs load them.
+    // With few jobs the weights are cut into pieces of N, so that more SMs load them (cut / whole, device time of one token: absorb 16 heads 3.5 / 5.5 us,
+    // 64 heads in two 4.7 / 5.9, 128 heads in two 7.3 / 6.9; project 16 heads in two 3.9 / 4.6, in four 3.9 to 4.3, 64 heads in two 4.5 / 4.8,
+    // 128 heads in two 7.8 / 6.2).
     const int64_t jobs = ((p.tokens + 127) / 128) * p.heads;
     const int cut = 4 * jobs <= sms ? 4 : 2 * jobs <= sms ? 2 : 1;
     if (absorb) return cut == 4 ? launch_piece<true, 128>(a, sms, stream) : cut == 2 ? launch_piece<true, 256>(a, sms, stream) : launch_piece<true, 512>(a, sms, stream);
-    return cut == 4 ? launch_piece<false, 32>(a, sms, stream) : cut == 2 ? launch_piece<false, 64>(a, sms, stream) : launch_piece<false, 128>(a, sms, stream);
+    return cut > 1 ? launch_piece<false, 64>(a, sms, stream) : launch_piece<false, 128>(a, sms, stream);
 }
 
 }  // namespace nvfp4mla
