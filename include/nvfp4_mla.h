@@ -401,7 +401,7 @@ NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_ca
  *   expanded  nvfp4_paged_mla_expand -> nvfp4_ragged_mla_attention. 640 instead of 2176 FLOP per query, key and head,
  *             after 262144 per key and head: for chunks of some 200 tokens and more.
  * All tensors are bf16, sums run in fp32 and are rounded once; h_q is 1 to 128, other values return
- * NVFP4_MLA_ERR_UNSUPPORTED. Strides are in elements and multiples of 8, inner strides 1; inputs are 16-byte aligned, outputs
+ * NVFP4_MLA_ERR_UNSUPPORTED. Strides are in elements and positive multiples of 8, inner strides 1; inputs are 16-byte aligned, outputs
  * contiguous and 32-byte aligned. The stride of a dimension of one entry is not looked at. Row counts stay below 2^31 - 4096.
  * Sequences lie packed, one behind the other: sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32
  * [batch + 1], device, from 0 on and not decreasing; entries are read as clamped to [0, rows], and other values give
@@ -457,7 +457,7 @@ NVFP4_MLA_API int nvfp4_ragged_mla_attention_workspace_size(size_t* bytes);
  *   out              [num_q, h_q, 128].
  *   workspace        at least ..._workspace_size bytes, 256-byte aligned; needs no initialization. Calls that may overlap on
  *                    the GPU need one each.
- * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^24, num_k below 2^26.
+ * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^20, num_k below 2^26.
  * Precision: weights e^z are rounded to bf16 (2^-8 of themselves, however small), row sums are of the unrounded ones.
  * A NaN or infinity in a query or a key makes NaN the rows that see it, one in a value the rows of its sequence that see it and
  * may make NaN those up to 383 rows before them; other sequences' rows never.

@@ -636,8 +636,8 @@ NVFP4_MLA_API int nvfp4_ragged_mla_attention(const void* q, int64_t q_token_stri
     int st = check_heads(num_q, h_q);
     if (st == NVFP4_MLA_OK) st = check_heads(num_k, h_q);
     if (st != NVFP4_MLA_OK) return st;
-    // (a tile's keys have to be through within the second that a wait may take: 2^19 blocks in 0.9 s)
-    if (batch < 0 || batch > (1 << 24) || num_k >= (int64_t(1) << 26)) return NVFP4_MLA_ERR_INVALID_ARG;
+    // (a tile's keys, and the lengths of the batch, have to be through within the second that a wait may take)
+    if (batch < 0 || batch > (1 << 20) || num_k >= (int64_t(1) << 26)) return NVFP4_MLA_ERR_INVALID_ARG;
     if (batch == 0 || num_q == 0) return NVFP4_MLA_OK;
     if (!cu_seqlens_q || !cu_seqlens_k || !out || !lse) return NVFP4_MLA_ERR_INVALID_ARG;
     if (!aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(attn_sink, 4) || !aligned(out, 32) || !aligned(lse, 4))

@@ -138,12 +138,18 @@ struct Walk {
     int64_t left;
     int seq, tile, head, b0;
     Seq s;
-    __device__ __forceinline__ Item next(const RaggedArgs& p, int run) {
+    __device__ __forceinline__ Item next(const RaggedArgs& p, int run, int lane) {   // (of the whole warp)
         Item it = {};
         if (left <= 0) return it;
-        while (tile >= tiles_of<kPair>(s)) {                       // (there is another one, as units are left)
-            s = seq_at(p, ++seq);
-            tile = 0;
+        while (tile >= tiles_of<kPair>(s)) {                       // the next sequence with rows, 32 lengths at a time
+            if (seq + 1 >= p.batch) {
+                left = 0;
+                return it;
+            }
+            const int b = seq + 1 + lane;
+            const unsigned rows = __ballot_sync(0xffffffffu, b < p.batch && seq_at(p, b).lq > 0);
+            seq += rows != 0u ? __ffs(rows) : 32;
+            if (rows != 0u) s = seq_at(p, seq), tile = 0;
         }
         const int row0 = kTile<kPair> * tile;
         const int n0 = blocks_of(s, row0 + kHalf<kPair>), n = blocks_of(s, row0 + kTile<kPair>), weight = n + kExtra;
@@ -592,10 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN.
             int unit = 0, e = 0;
             uint32_t phase = 0;
-            Item it = walk.next(p, run);
+            Item it = walk.next(p, run, lane);
             bool ok = publish(it);
             while (ok && it.valid) {
-                const Item ahead = walk.next(p, run);
+                const Item ahead = walk.next(p, run, lane);
                 ok = publish(ahead);
                 const int n = max(it.count0, it.count1);
 #pragma unroll 1

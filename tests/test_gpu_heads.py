@@ -171,6 +171,12 @@ def test_many_short_sequences():
     attend(rng, q_lens, k_lens, 2)
 
 
+def test_padding_between_two_sequences():
+    rng = np.random.default_rng(14)
+    gap = [0] * 50000
+    attend(rng, gap + [130, 3] + gap + [40] + gap, gap + [200, 3] + [7] * 50000 + [41] + gap, 3)
+
+
 @pytest.mark.parametrize("h,lq,lk", [(1, 3, 9001), (2, 256, 6000), (5, 700, 3333)])
 def test_tiles_that_several_ctas_share(h, lq, lk):
     rng = np.random.default_rng(lk)

@@ -100,7 +100,7 @@ def test_c_status_codes_before_any_device_query(cdll):
     def attend(q=A, qt=576, qh=192, nq=4, kv=A, kt=768, kh=256, pe=A, ps=64, nk=9, cq=A, ck=A, b=2, h=3, sink=None, out=A, lse=A, ws=A, wb=size):
         return cdll.nvfp4_ragged_mla_attention(q, qt, qh, nq, kv, kt, kh, pe, ps, nk, cq, ck, b, h, 0.1, sink, out, lse, ws, wb, None, None)
 
-    for change, st in (({"h": 0}, U), ({"h": 129}, U), ({"nq": -1}, D), ({"nk": -1}, D), ({"nq": big}, D), ({"nk": big}, D), ({"nk": 1 << 26}, D), ({"b": -1}, D), ({"b": (1 << 24) + 1}, D),
+    for change, st in (({"h": 0}, U), ({"h": 129}, U), ({"nq": -1}, D), ({"nk": -1}, D), ({"nq": big}, D), ({"nk": big}, D), ({"nk": 1 << 26}, D), ({"b": -1}, D), ({"b": (1 << 20) + 1}, D),
                        ({"q": None}, D), ({"q": A + 4}, D), ({"qt": 4}, D), ({"qh": 100}, D), ({"kv": None}, D), ({"kt": 0}, D), ({"kh": 4}, D), ({"pe": None}, D),
                        ({"ps": 60}, D), ({"cq": None}, D), ({"ck": A + 2}, D), ({"sink": A + 2}, D), ({"out": A + 16}, D), ({"lse": None}, D), ({"ws": None}, W),
                        ({"wb": size - 1}, W), ({"ws": A + 128}, W), ({"nq": 0, "q": None}, lib.OK), ({"b": 0, "cq": None}, lib.OK)):
