@@ -459,8 +459,8 @@ NVFP4_MLA_API int nvfp4_ragged_mla_attention_workspace_size(size_t* bytes);
  *                    the GPU need one each.
  * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^20, num_k below 2^26.
  * Precision: weights e^z are rounded to bf16 (2^-8 of themselves, however small), row sums are of the unrounded ones.
- * A NaN or infinity in a query or a key makes NaN the rows that see it, one in a value the rows of its sequence that see it and
- * may make NaN those up to 383 rows before them; other sequences' rows never.
+ * A NaN or infinity in a query or a key makes NaN the rows that see it, one in a value makes its dim, and may make all dims, of the
+ * rows that see it NaN or infinite; rows that do not see it, and log-sum-exps, never.
  */
 NVFP4_MLA_API int nvfp4_ragged_mla_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_q,
                                              const void* kv, int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe,

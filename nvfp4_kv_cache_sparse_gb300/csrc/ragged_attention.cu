@@ -23,7 +23,7 @@
 // time, from L2. A tile that two runs share leaves fp32 parts in the workspace, which a second kernel joins.
 //
 // 2048 rows over 16640 keys, 64 heads: 760 us, 1.72 PFLOP/s (one CTA each: 868); 4 chunks of 512 rows over 500 to 16000 keys, 16 heads:
-// 139 us, 1.45 PFLOP/s (159); 16 prompts of 30 to 700 tokens, 16 heads: 47 us on one CTA each, where a tile's first loads, its softmax and
+// 139 us, 1.45 PFLOP/s (159); 16 prompts of 30 to 700 tokens, 16 heads: 48 us on one CTA each, where a tile's first loads, its softmax and
 // its way out (4 us) count more than its few blocks.
 #include "head_tiles.cuh"
 #include "launch.h"
@@ -82,6 +82,7 @@ struct Ctl {
     uint64_t item_full[kItems], item_empty[kItems];
     uint32_t tmem_base, abort;
     Item items[kItems];                // what the CTA works on, one behind the other
+    int bad[16];                       // of item k with blocks (entry k % 16): its first key with a value that is not finite and was taken out
 };
 static_assert(sizeof(Ctl) <= kOffQ, "control block");
 
@@ -353,6 +354,43 @@ __device__ __forceinline__ void move_reference(float top, float& m, float& l, bo
     }
 }
 
+__device__ __forceinline__ void red_min_cluster(uint32_t cluster_saddr, int v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(cluster_saddr), "r"(v) : "memory");
+}
+
+// A warp looks through 16 KB of bf16 values, rows of 128 bytes (row & last_row is the key's): values that are not finite become zeros.
+// Returns the first key that had one, or INT32_MAX.
+__device__ __forceinline__ int clean_values(uint32_t base, int last_row, int lane) {
+    auto odd = [](uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };   // bit 15 and 31: exponent all ones
+    uint32_t any = 0;
+#pragma unroll 8
+    for (int x = lane; x < 1024; x += 32) {
+        const uint4 v = lds_u128(base + 16 * x);
+        any |= odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w);
+    }
+    if (!__any_sync(0xffffffffu, any != 0u)) return INT32_MAX;
+    int key = INT32_MAX;
+#pragma unroll 1
+    for (int x = lane; x < 1024; x += 32) {
+        const uint4 v = lds_u128(base + 16 * x);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        bool here = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t o = odd(w[e]);
+            here |= o != 0u;
+            w[e] &= ((o & 0x8000u) != 0u ? 0u : 0x0000FFFFu) | ((o & 0x80000000u) != 0u ? 0u : 0xFFFF0000u);
+        }
+        if (here) {
+            sts_u128(base + 16 * x, make_uint4(w[0], w[1], w[2], w[3]));
+            key = min(key, (x >> 3) & last_row);
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    return __reduce_min_sync(0xffffffffu, key);
+}
+
 template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __grid_constant__ KernelArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];   // (there is no static shared memory: it begins at a multiple of 1024)
@@ -378,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         }
         // (an item is read by 8 softmax warps, the loads and, in CTA 0, two issuers)
         for (int i = 0; i < kItems; ++i) mbar_init(&ctl->item_full[i], 1), mbar_init(&ctl->item_empty[i], rank == 0 ? 11 : 9);
+        for (int i = 0; i < 16; ++i) ctl->bad[i] = INT32_MAX;
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0u;
         fence_barrier_init();
@@ -595,8 +634,11 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 if (++slot == kItems) slot = 0, slot_phase ^= 1u;
                 return true;
             };
-            // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN.
-            int unit = 0, e = 0;
+            // Values behind a sequence's end belong to other sequences or to nobody and may be anything: zeros, as 0 x NaN is NaN. Where some
+            // rows of the tile do not see all keys of a block, values that are not finite would reach them in the same way: they
+            // become zeros too, and the rows that see such a key are made NaN on their way out. (The values are there long before the
+            // weights, so the look at them costs little: 16 short prompts, where it is all blocks, 45.8 -> 47.6 us, long chunks 0.5%.)
+            int unit = 0, e = 0, number = 0;               // number: of items with blocks
             uint32_t phase = 0;
             Item it = walk.next(p, run, lane);
             bool ok = publish(it);
@@ -604,6 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                 const Item ahead = walk.next(p, run, lane);
                 ok = publish(ahead);
                 const int n = max(it.count0, it.count1);
+                int* const bad = &ctl->bad[number & 15];
+                if (n > 0) {
+                    // (items that lie 8 apart are never at work together: values are at most three blocks ahead of the products)
+                    if (lane == 0) ctl->bad[(number + 8) & 15] = INT32_MAX;
+                    ++number;
+                }
 #pragma unroll 1
                 for (int i = 0; i < n && ok; ++i) {
                     const int left = it.keys - 128 * (it.from + i);
@@ -625,6 +673,22 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
+                    if (128 * (it.from + i + 1) > it.seen) {
+                        int key = INT32_MAX;
+                        if (kPair) {
+                            key = clean_values(sbase + kOffPairV + e * kBox, 127, lane);
+                        } else {
+                            for (int c = 0; c < 2; ++c) {
+                                const int k = clean_values(sbase + kOffRing + ((unit + c) & (kUnits - 1)) * kBox, 63, lane);
+                                if (k != INT32_MAX) key = min(key, 64 * c + k);
+                            }
+                        }
+                        if (key != INT32_MAX && lane == 0) {
+                            key += 128 * (it.from + i);
+                            atomicMin(bad, key);
+                            if (kPair) red_min_cluster(mapa_shared(smem_addr(bad), rank ^ 1), key);
+                        }
+                    }
                     unit = (unit + 2) & (kUnits - 1);
                     if (lane == 0) arrive_first(&ctl->v_ready[e], false);
                     if (++e == kDepth<kPair>) e = 0, phase ^= 1;
@@ -637,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w) << 16);
         const uint32_t s_addr = lanes + kColS + 128 * h, o_addr = lanes + kColO + 128 * h;
         const float mul = p.sm_scale == 0.0f ? 1e-30f : fabsf(p.sm_scale) * kLog2e;   // (0 x -inf would be NaN where a key is masked)
-        int seen = 0;                  // blocks of this half so far
+        int seen = 0, number = 0;      // blocks of this half, items with blocks so far
         uint32_t done = 0;             // and tiles
         Items items = {ctl};
         bool ok = true;
@@ -720,6 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
             float f = empty ? 0.0f : 1.0f / l;
             if (slot < 0 && !empty && p.attn_sink != nullptr) f = 1.0f / (l + exp2f(__ldg(p.attn_sink + head) * kLog2e - m));
             const bool none = n == 0 || empty;
+            // a value that was taken out, of a key that the row sees
+            const bool spoilt = max(it->count0, it->count1) > 0 && min(it->seen + first + 32 * w + lane, it->keys) > ctl->bad[number++ & 15];
+            if (spoilt) f = __uint_as_float(0x7FC00000u);
             if (slot >= 0 && rows > 0) {                   // (where a part has no keys the join does not look at its outputs)
                 a.part_lse[static_cast<int64_t>(slot) * kTile<kPair> + first + 32 * w + lane] = lse2;
                 float* dst = a.part_out + (static_cast<int64_t>(slot) * (kTile<kPair> / 32) + first / 32 + w) * 4096 + 8 * lane;

@@ -235,6 +235,27 @@ def test_what_lies_behind_a_sequence_does_not_reach_it():
     assert torch.isnan(out[130:200].float()).all()
 
 
+@pytest.mark.parametrize("lq,lk", [(300, 300), (140, 500), (600, 3100), (1100, 4000)])   # (the last two on CTA pairs)
+def test_values_that_are_not_finite_reach_the_rows_that_see_them_only(lq, lk):
+    rng = np.random.default_rng(lk)
+    h, odd = 3, lk - lq + 2 * lq // 3                                  # a key that the last third of the rows sees
+    q, kv, pe = bf16(rng, lq + 50, h, 192), bf16(rng, lk + 80, h, 256), bf16(rng, lk + 80, 64)
+    dirty = kv.clone()
+    dirty[odd, 0, 133], dirty[odd + 1, 0, 250], dirty[odd + 2, 1, 255], dirty[odd + 9, 1, 128] = float("nan"), float("inf"), -float("inf"), float("nan")
+    st = zero_status()
+    out, lse = lib.ragged_mla_attention(q.to(DEV), dirty.to(DEV), pe.to(DEV), starts([lq, 50]).to(DEV), starts([lk, 80]).to(DEV), SCALE, dev_status=st)
+    assert int(st.item()) == 0
+    r = ref.attention(q, kv, pe, [lq, 50], [lk, 80], SCALE)
+    first = odd - (lk - lq)                                            # the first row that sees the NaN
+    ref.check_attention(out[:first], lse[:first], tuple(x[:first] for x in r))
+    ref.check_attention(out[lq:], lse[lq:], tuple(x[lq:] for x in r))  # another sequence
+    ref.check_attention(out[:, 2], lse[:, 2], tuple(x[:, 2] for x in r))   # another head
+    assert torch.isnan(out[first:lq, 0, 5].float()).all() and not torch.isfinite(out[first + 1:lq, 0, 122].float()).any()
+    assert not torch.isfinite(out[first + 2:lq, 1, 127].float()).any() and torch.isnan(out[first + 9:lq, 1, 0].float()).all()
+    ref.check_attention(out[:first + 2, 1], lse[:first + 2, 1], tuple(x[:first + 2, 1] for x in r))
+    ref.check(lse.cpu().numpy().astype(np.float64), r[1], r[3], "lse")  # the weights are what they are
+
+
 def test_attention_of_strided_inputs():
     rng = np.random.default_rng(11)
     h, q_lens, k_lens = 3, [150, 20], [180, 90]
