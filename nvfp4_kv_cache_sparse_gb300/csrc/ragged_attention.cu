@@ -178,10 +178,11 @@ struct Items {
     Ctl* ctl;
     int at = 0;
     uint32_t phase = 0;
-    // nullptr: no more, or given up
+    // nullptr: no more, or given up. For one thread, or for a whole warp with one answer.
+    template <bool kWarp = false>
     __device__ __forceinline__ const Item* next(uint32_t* status) {
-        if (!wait_or_give_up(&ctl->item_full[at], phase, &ctl->abort, status) || ctl->items[at].valid == 0) return nullptr;
-        return &ctl->items[at];
+        const bool there = kWarp ? wait_warp(&ctl->item_full[at], phase, &ctl->abort, status) : wait_or_give_up(&ctl->item_full[at], phase, &ctl->abort, status);
+        return there && ctl->items[at].valid != 0 ? &ctl->items[at] : nullptr;
     }
     __device__ __forceinline__ void step() {
         if (++at == kItems) at = 0, phase ^= 1u;
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         Items items = {ctl};
         bool ok = true;
         for (;;) {
-            const Item* const it = items.next(status);
+            const Item* const it = items.next<true>(status);
             if (it == nullptr) break;
             const int n = h == 0 ? it->count0 : it->count1;
             // keys that the row, and the half's first row, see of those from the first block on
