@@ -24,7 +24,6 @@ D_HEAD_QK, D_HEAD_KV = D_HEAD_NOPE + D_ROPE, D_HEAD_NOPE + D_HEAD_V
 # These calls are small next to a layer's others, so their host time counts: checks read each property of a tensor once, and
 # messages are put together only where they are raised (one token with `out` given: 10.2 -> 7.6 us on the host, 3.6 of them in C).
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
-_current_device = torch._C._cuda_getDevice
 _calls = {}
 
 
@@ -32,7 +31,7 @@ def _call(name: str, dev: int, *args) -> None:
     f = _calls.get(name)
     if f is None:
         f = _calls[name] = getattr(load(), name)
-    if _current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:   # (read here: a build of torch without CUDA has no such name, and the package imports there too)
         st = f(*args)
     else:
         with torch.cuda.device(dev):
