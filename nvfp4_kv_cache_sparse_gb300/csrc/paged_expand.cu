@@ -191,6 +191,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_expand_kernel(const __grid_
                 }
                 if (++head == p.heads) head = 0;
             }
+            // The last boxes' arrivals: no barrier of the cluster orders what a commit sends to the other CTA, and it must not reach
+            // this CTA's shared memory after the CTA has left. (They come with products that the epilogue waits for anyway.)
+            bool landed = ok;
+            for (int c = 0; c < kStages && landed; ++c) {
+                landed = wait_or_give_up(&ctl->empty[stage], phase, abort, status);
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
