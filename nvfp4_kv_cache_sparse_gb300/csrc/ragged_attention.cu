@@ -516,6 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
                     for (int i = 1; i < n && ok; ++i) ok = load_k(i) && load_v(i);
                     if (!ok) break;
                 }
+                // The last arrivals: no barrier of the cluster orders what a commit sends to the other CTA, and it must not reach this CTA's shared
+                // memory after the CTA has left. (They come with products that the softmax warps wait for anyway.)
+                bool landed = *reinterpret_cast<volatile uint32_t*>(abort) == 0u;
+                for (int i = 0; i < kDepth<kPair> && landed; ++i) {
+                    landed = wait_or_give_up(&ctl->k_empty[e], phase ^ 1, abort, status) && wait_or_give_up(&ctl->v_empty[e], phase ^ 1, abort, status);
+                    if (++e == kDepth<kPair>) e = 0, phase ^= 1;
+                }
+                for (int h = 0; h < 2 && landed; ++h) landed = wait_or_give_up(&ctl->q_free[h], (q_phase >> h) & 1, abort, status);
             }
             __syncwarp();
         } else if (warp >= kWarpMma) {
