@@ -649,7 +649,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lt = (xl[hl] + xl[64 + hl]) + (xl[128 + hl] + xl[192 + hl]);
         bool have_o = false;
         if (ok && n_tiles > 0) {
-            have_o = wait_warp(ctl, &ctl->pvdone, (n_tiles - 1) & 1, a.status);
+            // No barrier of the cluster orders what a commit sends to the other CTA: the last arrivals that nobody else waits for must not
+            // reach this CTA's shared memory after the CTA has left. (They come before the last P V is done.)
+            const bool landed = warp != 0 || (wait_warp(ctl, &ctl->khalf, (n_tiles - 1) & 1, a.status) &&
+                                              wait_warp(ctl, &ctl->pvhalf, (n_tiles - 1) & 1, a.status));
+            have_o = landed && wait_warp(ctl, &ctl->pvdone, (n_tiles - 1) & 1, a.status);
             if (have_o) tc_fence_after_sync();
         }
         const int head = 64 * crank + hl;      // (kPaged: row of the job)
@@ -969,6 +973,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
+            // (the peer's last signals too, which no score waits for)
+            [[maybe_unused]] const bool landed = ok && n_tiles > 0 && wait_peer(ctl, &ctl->sfree, (n_tiles - 1) & 1, a.status);
             if (leader) mma_commit_cg2(&ctl->drain, 0x1u << pb);
             __syncwarp();
         }

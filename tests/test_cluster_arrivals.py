@@ -11,6 +11,9 @@ import pytest
 from test_cluster_barriers import kernels
 
 FOLLOWED = {
+    "decode_pair_kernel": {"qkdone": "the softmax, each tile", "pvdone": "the softmax, the last tile, and converters, the others",
+                           "kfull_a": "the QK issuer, each tile", "kfull_b": "the same", "vfull_a": "the PV issuer, each tile", "vfull_b": "the same",
+                           "pfull_a": "the PV issuer, each tile", "pfull_b": "the same", "qready": "the QK issuer", "drain": "the issuers, in whose CTA alone it counts"},
     "paged_expand_kernel": {"acc_full": "the epilogue, each unit", "a_free": "the converters: it is sent only where another tile follows",
                             "drain": "the issuer, in whose CTA alone it counts"},
     "ragged_attention_kernel": {"s_full": "the softmax, each block", "o_done": "the softmax, each tile", "drain": "the issuers, in whose CTA alone it counts"},
