@@ -844,6 +844,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) sparse_
                 st_async_v2(mapa_shared(smem_addr(smem + kOffFin) + 8 * h, 1), m_ref, l + xsum[h],
                             mapa_shared(smem_addr(&ctl->fin), 1));
             }
+            // No barrier of the cluster orders what CTA 1's commits send here: the last arrivals, which no tile waits for, must not
+            // reach this CTA's shared memory after the CTA has left. (CTA 1's output takes longer.)
+            bool landed = ok && warp == 0;
+            for (int i = max(n_tiles - kPStages, 0); i < n_tiles && landed; ++i)
+                landed = wait_warp(ctl, &ctl->pempty[i % kPStages], (i / kPStages) & 1, a.status);
         } else if (converter) {
             // ============ CTA 0, warps 8-23: dequant of whole records (K tiles) ============
             if constexpr (R == 656)

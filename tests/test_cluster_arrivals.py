@@ -16,6 +16,7 @@ FOLLOWED = {
                            "pfull_a": "the PV issuer, each tile", "pfull_b": "the same", "qready": "the QK issuer", "drain": "the issuers, in whose CTA alone it counts"},
     "paged_expand_kernel": {"acc_full": "the epilogue, each unit", "a_free": "the converters: it is sent only where another tile follows",
                             "drain": "the issuer, in whose CTA alone it counts"},
+    "sparse_decode_kernel": {},
     "ragged_attention_kernel": {"s_full": "the softmax, each block", "o_done": "the softmax, each tile", "drain": "the issuers, in whose CTA alone it counts"},
 }
 SENDS = r"\b(?:mma_commit_cg2|mma_commit_multicast|commit)\s*\(([^;]*);", r"\bsignal_leader\s*\(([^;]*);"
