@@ -709,7 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         const int h = warp >> 2, w = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w) << 16);
         const uint32_t s_addr = lanes + kColS + 128 * h, o_addr = lanes + kColO + 128 * h;
-        const float mul = p.sm_scale == 0.0f ? 1e-30f : fabsf(p.sm_scale) * kLog2e;   // (0 x -inf would be NaN where a key is masked)
+        // (0 x -inf would be NaN where a key is masked: 2^-149, which takes the largest score there is to 2^-21)
+        const float mul = p.sm_scale == 0.0f ? __uint_as_float(1u) : fabsf(p.sm_scale) * kLog2e;
         int seen = 0, number = 0;      // blocks of this half, items with blocks so far
         uint32_t done = 0;             // and tiles
         Items items = {ctl};
