@@ -406,8 +406,9 @@ NVFP4_MLA_API int nvfp4_mla_compact_pages(uint8_t* const* caches, int32_t num_ca
  * Sequences lie packed, one behind the other: sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32
  * [batch + 1], device, from 0 on and not decreasing; entries are read as clamped to [0, rows], and other values give
  * unspecified rows but touch nothing outside the tensors).
- * Rows from cu_seqlens[batch] on are neither read nor written, so buffers may be larger than what a batch fills, and a
- * captured call follows the lengths of its replay. A pipeline wait that gives up sets NVFP4_MLA_DEV_TIMEOUT.
+ * Rows from cu_seqlens[batch] on are never written and change no result, so buffers may be larger than what a batch fills, and a
+ * captured call follows the lengths of its replay. The attention reads whole boxes of rows, though, so inputs up to their last
+ * row may be read while a call runs. A pipeline wait that gives up sets NVFP4_MLA_DEV_TIMEOUT.
  */
 
 /*
@@ -459,8 +460,12 @@ NVFP4_MLA_API int nvfp4_ragged_mla_attention_workspace_size(size_t* bytes);
  *                    the GPU need one each.
  * A query without a visible key gets out = 0, lse = -inf. batch is at most 2^20, num_k below 2^26.
  * Precision: weights e^z are rounded to bf16 (2^-8 of themselves, however small), row sums are of the unrounded ones.
- * A NaN or infinity in a query or a key makes NaN the rows that see it, one in a value makes its dim, and may make all dims, of the
- * rows that see it NaN or infinite; rows that do not see it, and log-sum-exps, never.
+ * A NaN in a query or a key, and a score of +infinity, make NaN the rows that see it; a score of -infinity has the weight 0. A NaN or
+ * infinity in a value makes its dim, and may make all dims, of the rows that see it NaN or infinite; rows that do not see it, and
+ * log-sum-exps, never.
+ * Which of two kernels runs follows the average rows and keys of a sequence (num_q / batch, num_k / batch), as the lengths lie on the
+ * device: tensors that fit the batch, without padding sequences, let long chunks take the faster one. Results do not depend on
+ * it beyond the order of sums.
  */
 NVFP4_MLA_API int nvfp4_ragged_mla_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_q,
                                              const void* kv, int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe,

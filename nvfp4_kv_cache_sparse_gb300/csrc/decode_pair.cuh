@@ -22,7 +22,7 @@
 //   its own half of the dims for all 128 keys from that half's codes and scales. Both CTAs read
 //   the V half of a record around the time its owner reads the whole, so DRAM delivers each
 //   record once per pair and the second read comes from L2.
-// Numbers. e2m1 x e4m3 products are exact in f16 (<= 5 significant bits in [2^-10, 2688]), so K
+// Numbers. e2m1 x e4m3 products are exact in f16 (<= 6 significant bits in [2^-10, 2688]), so K
 // and V tiles are f16 (the bf16 RoPE of 432-byte records stays bf16). q enters as f16 scaled by a
 // per-head power of two (2^pre with max|q| 2^pre in [2^14, 2^15)): the products q_d K_d are the
 // same numbers as with bf16 q, and S comes out as 2^pre times the exact score, which the softmax

@@ -2,7 +2,7 @@
 // that dequantize NVFP4 records into 16-bit MMA operand tiles.
 //
 // An NVFP4 value is an e2m1 code times the e4m3 scale of its 16-value block; the product has at
-// most five significant bits and lies in [2^-10, 2688] (or is zero), so it is exact in f16 and in
+// most six significant bits (3 x 15 = 45) and lies in [2^-10, 2688] (or is zero), so it is exact in f16 and in
 // bf16 and every conversion below is exact.
 #pragma once
 

@@ -14,7 +14,7 @@
 // shared memory while the tokens' boxes of 64 dims stream through a ring; accumulators alternate between two
 // halves of the tensor memory, so that loads, products and stores of neighbouring tiles overlap. Results leave through shared
 // memory as boxes (32-byte stores of 32 rows at once take 130 cycles a warp).
-// 4001 tokens x 128 heads: absorb 160 us, 5.0 TB/s (73% of a copy's rate; two thirds are writes, and writes alone reach 4.07 TB/s), project 114 us,
+// 4001 tokens x 128 heads: absorb 160 to 162 us, 5.0 TB/s (73% of a copy's rate; 154 us without rotation), project 112 to 116 us,
 // 5.9 TB/s (87%). One token x 16 heads: 3.5 and 3.9 us on the device.
 #include "head_tiles.cuh"
 #include "launch.h"
@@ -91,7 +91,8 @@ __device__ __forceinline__ void rope_positions(const HeadProductArgs& p, int64_t
 }
 
 // The RoPE dims of a tile's tokens: all of a lane's loads are in flight at once (in four rounds of loads a tile,
-// positions ahead of tables, these warps bound the kernel: 262 against 161 us at 4001 tokens x 128 heads, 154 without rotation).
+// positions ahead of tables, these warps bound the kernel: 262 against 161 us at 4001 tokens x 128 heads, 154 without rotation). Fourteen
+// warps leave 128 registers a thread, of which these loads want a few more: 60 bytes are spilled.
 template <bool kHalf>
 __device__ __forceinline__ void rope_tile(const HeadProductArgs& p, int64_t t0, int head, int lane, const int64_t (&pos)[4]) {
     const int j = lane & 7;

@@ -2,17 +2,18 @@
 //
 //   kv[t, h, 0:256] = kv_b[h] c[t],   k_pe[t] = the record's RoPE dims
 // c[t] being the dequantized latent (512) of token t of the batch, its sequences lying one behind the other. An e2m1 code times its
-// e4m3 scale has five significant bits, so c is exact in bf16; the sums run in fp32 in tensor memory and are rounded to bf16 once.
+// e4m3 scale has six significant bits, so c is exact in bf16; the sums run in fp32 in tensor memory and are rounded to bf16 once.
 //
 // This is one product [tokens, 512] x [512, 256 heads] whose left side is gathered and dequantized on the way: 512 FLOP per
-// byte written, where the tensor cores (1.91 PFLOP/s) and the memory's writes (4.07 TB/s alone) take about the same time. A CTA pair holds the latents of 256 tokens in shared memory (128 KB a CTA, dequantized
+// byte written: the tensor cores bound it (1.91 PFLOP/s; whole lines written one behind the other reach 7.7 TB/s, half of that time). A CTA pair holds the latents of 256 tokens in shared memory (128 KB a CTA, dequantized
 // once) and runs over heads: each CTA streams half of a head's weights (CTA 0 the key's 128 rows, CTA 1 the value's)
 // through a ring, and every tcgen05.mma of M = 256, N = 256 works on both halves, which halves what a CTA has to
 // read of the weights through L2 (one CTA alone: 32 MB for every 128 tokens at 128 heads, 15 TB/s). Accumulators of two heads alternate in
 // tensor memory. Pairs take equal runs of (tile of 256 tokens, head), heads innermost, so that all work to the
 // end, and the records of the next tile are loaded into registers while the last heads of this one still run.
-// 32,600 tokens x 128 heads: 765 to 785 us, 1.3 PFLOP/s; 454 without the writes, 592 with all of them into 64 MB that stay in L2, the same with half
-// the loads: the scattered 512-byte writes bound it. 67,000 tokens x 16 heads: 216 to 228 us, 1.45 PFLOP/s.
+// 30,626 tokens x 128 heads: 765 to 791 us, 1.30 to 1.34 PFLOP/s; 454 without the writes, 592 with all of them into 64 MB that stay in L2, the same with
+// half the loads: the writes bound it, 512 bytes of a token 64 KB from the next one's (2.6 TB/s). 80,232 tokens x 16 heads: 216 to 235 us, 1.43 to
+// 1.56 PFLOP/s.
 #include "head_tiles.cuh"
 #include "launch.h"
 

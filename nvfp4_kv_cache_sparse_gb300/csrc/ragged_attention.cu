@@ -22,9 +22,9 @@
 // of 128 keys) units, heads inside tiles: neighbouring tiles of a head are then read by several CTAs at about the same
 // time, from L2. A tile that two runs share leaves fp32 parts in the workspace, which a second kernel joins.
 //
-// 2048 rows over 16640 keys, 64 heads: 760 us, 1.72 PFLOP/s (one CTA each: 868); 4 chunks of 512 rows over 500 to 16000 keys, 16 heads:
-// 139 us, 1.45 PFLOP/s (159); 16 prompts of 30 to 700 tokens, 16 heads: 48 us on one CTA each, where a tile's first loads, its softmax and
-// its way out (4 us) count more than its few blocks.
+// 2048 rows over 16640 keys, 64 heads: 760 us in a short run, 1.72 PFLOP/s (one CTA each: 868), 870 to 890 in a long one, where power limits the
+// clock; 4 chunks of 512 rows over 500 to 16000 keys, 16 heads: 139 to 154 us, 1.31 to 1.45 PFLOP/s (one CTA each: 159); 16 prompts of 30 to 700 tokens,
+// 16 heads: 45 to 48 us on one CTA each, where a tile's first loads, its softmax and its way out (4 us) count more than its few blocks.
 #include "head_tiles.cuh"
 #include "launch.h"
 
@@ -438,8 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_attention_kernel(const __g
         if (kPair) mma_commit_cg2(bar, 0x3u);
         else mma_commit(bar);
     };
-    // An arrival on a barrier of CTA 0. Weights are in tensor memory, and their stores were waited for: nothing is left for a release at
-    // cluster scope to order, which takes about 1000 cycles.
+    // An arrival on a barrier of CTA 0. Weights are in tensor memory: what orders their stores ahead of the products is that they were waited for
+    // (tcgen05.wait::st), with tcgen05's own fences ahead of the arrival and behind the issuer's wait. Where nothing else is handed over the
+    // arrival itself is relaxed: a release at cluster scope would order shared and global memory, and takes about 1000 cycles.
     auto arrive_first = [](uint64_t* bar, bool relaxed) {
         if (!kPair) mbar_arrive(bar);
         else if (relaxed) mbar_arrive_cluster_relaxed(mapa_shared(smem_addr(bar), 0));
@@ -919,6 +920,9 @@ cudaError_t launch_runs(KernelArgs& a, int sms, cudaStream_t stream) {
 // blocks cost besides. So pairs are for long sequences whose rows fill their tiles, by the average rows and keys of a sequence (one CTA / pairs, us):
 // 4 chunks of 512 rows over 4512 keys, 64 heads 276 / 246, of 384 rows 259 / 236, of 256 rows 148 / 210; one of 700 rows over 16700 keys
 // 355 / 390; 16 prompts of 512, 16 heads 51 / 55; 2 prompts of 4096, 64 heads 509 / 498; 2048 rows over 16640 keys, 64 heads 868 / 760.
+// The averages are all that the host knows, as lengths lie on the device. Where sequences are of very different lengths, or the tensors larger than
+// what they hold, the choice can be the slower one: that last chunk beside one token over 4000 keys, or in a batch padded with 63 empty
+// sequences, goes to one CTA each (920 and 910 us in a run where it alone takes 818).
 bool pairs_are_faster(const RaggedArgs& p) {
     const int64_t rows = (p.rows_q + p.batch - 1) / p.batch, keys = p.rows_k / p.batch;
     const int64_t blocks = keys > rows / 2 ? (keys - rows / 2) / 128 : 0;

@@ -6,7 +6,7 @@
 //     z_j = sm_scale * q[t,h,:] . K_j          (K_j: 576 dequantized values of record j)
 //     out = sum_j e^{z_j} V_j / (sum_j e^{z_j} + e^{sink_h}),   V_j = K_j[0:512]
 //     lse = ln sum_j e^{z_j}
-// Keys are dequantized in shared memory, exactly (e2m1 x e4m3 has <= 5 significant bits): to
+// Keys are dequantized in shared memory, exactly (e2m1 x e4m3 has <= 6 significant bits): to
 // bf16 for QK^T (q is bf16) and to f16 for PV (P in f16 keeps 11 significant bits); both
 // contractions run as tcgen05 16-bit MMAs with fp32 accumulation in tensor memory.
 //
@@ -192,7 +192,7 @@ __device__ __forceinline__ uint32_t dq_e2m1x2(uint32_t byte, __half2 scale2) {
     return pack_bf16x2(f.x, f.y);
 }
 
-// Two e2m1 codes times a scale -> f16x2 (exact: the products need at most 5 significant bits and
+// Two e2m1 codes times a scale -> f16x2 (exact: the products need at most 6 significant bits and
 // lie in [2^-10, 2688], inside the f16 normal range).
 __device__ __forceinline__ uint32_t dq_e2m1x2_f16(uint32_t byte, __half2 scale2) {
     uint32_t h;

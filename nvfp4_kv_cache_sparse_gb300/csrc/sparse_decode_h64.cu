@@ -27,7 +27,7 @@
 // as soon as the PV MMAs of tile k have read it; the QK MMAs of tile k + 1 follow the converters
 // block by block; the softmax of tile k + 1 then writes P^T, and the PV MMAs of tile k + 1 start.
 // The softmax warps load and convert the RoPE rows of tile k + 1 while they score tile k.
-// Numbers. K is f16 (exact: e2m1 x e4m3 has <= 5 significant bits in [2^-10, 2688]; the bf16 RoPE
+// Numbers. K is f16 (exact: e2m1 x e4m3 has <= 6 significant bits in [2^-10, 2688]; the bf16 RoPE
 // of 432-byte records stays bf16 and those four K-steps run as bf16 MMAs). q enters as f16 scaled
 // by a per-head power of two (2^pre with max|q| 2^pre in [2^14, 2^15)), so that the products
 // q_d K_d are the same numbers as with bf16 q; S^T column h comes out as 2^pre_h times the exact

@@ -169,7 +169,9 @@ def ragged_mla_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, 
     a projection of unquantized latents. Sequence b has the queries ``cu_seqlens_q[b]`` to ``cu_seqlens_q[b + 1]``
     (int32 [batch + 1], on the device) and the keys ``cu_seqlens_k[b]`` to ``cu_seqlens_k[b + 1]``; its last query sees all of
     them, the one before it one fewer, and so on. Returns (out bf16 [Tq, h, 128], lse fp32 [Tq, h]); a query without
-    a visible key gets out = 0, lse = -inf, rows from ``cu_seqlens_q[batch]`` on are left as they were."""
+    a visible key gets out = 0, lse = -inf, rows from ``cu_seqlens_q[batch]`` on are left as they were. The kernel is chosen by the
+    average rows and keys of a sequence (Tq / batch, Tk / batch): padding sequences, or tensors far larger than the batch, may cost long
+    chunks some of their speed."""
     Tq, h, qt, qh = _strides(q, D_HEAD_QK, "q")
     Tk, hk, kt, kh = _strides(kv, D_HEAD_KV, "kv")
     _need(hk == h, "q and kv disagree about the heads")
